@@ -385,6 +385,92 @@ sd_status sd_denoise(const sd_unet_cfg* cfg, const void* packed_w, int32_t sampl
 sd_status sd_vae_decode(const sd_vae_cfg* cfg, const void* packed_w, const void* latent, void* image,
                         void* workspace, size_t ws_bytes, sd_stream_t stream);
 
+/* ---------------------------------------------------------------- operators
+ * The operators that the blocks above are made of, by themselves: for any
+ * batch, with masks, in other types, and with their gradients. They follow the
+ * conventions at the top of this file, with these additions:
+ *   - sizes of zero are allowed where said; a call that has nothing to write
+ *     launches nothing;
+ *   - `workspace` holds scratch between the launches of one call and nothing from
+ *     one call to the next; it needs no initialisation. Calls that may overlap on
+ *     the GPU (other streams, two captured graphs) need workspaces of their own.
+ *     After a call, sd_query_device_status(workspace, stream) reports a bounded
+ *     wait that gave up;
+ *   - a workspace size is host arithmetic on the configuration (0 for one that
+ *     is refused) and serves the forward and the backward call;
+ *   - all work runs on the current device, which must be the one that owns the
+ *     stream and the tensors;
+ *   - sums, statistics and softmax are FP32; results repeat bit for bit. */
+
+enum { SD_DTYPE_BF16 = 0, SD_DTYPE_F16 = 1, SD_DTYPE_F32 = 2 };
+/* SD_ACT_SILU: z / (1 + e^-z). SD_ACT_GELU: z Phi(z), the exact erf form. */
+enum { SD_ACT_NONE = 0, SD_ACT_SILU = 1, SD_ACT_GELU = 2 };
+
+/* Group norm with an activation on channels-last tensors [batch, rows, channels]:
+ * y = act(gamma (x - mean) / sqrt(var + eps) + beta), mean and (biased) variance
+ * per image and group over rows x channels/groups values. The normalisation in
+ * front of every convolution and transformer here [SD21 section 4; TUT GSC
+ * bullet], for a batch and with gradients.
+ *   batch, rows >= 0; channels <= 8192, a multiple of groups; eps > 0.
+ *   dtype: of x, y, gamma, beta, dy and dx (BF16, F16 or F32).
+ *   ld_x / ld_y: elements from one row to the next of x and dx / of y and dy (0 =
+ *   channels); an image holds rows * ld of them. Rows of 16-byte multiples (sizes
+ *   and strides) are read in 16-byte accesses, others element by element. */
+typedef struct {
+  int32_t batch;
+  int64_t rows;
+  int32_t channels;
+  int32_t groups;
+  float eps;
+  int32_t act;    /* SD_ACT_* */
+  int32_t dtype;  /* SD_DTYPE_* */
+  int64_t ld_x;
+  int64_t ld_y;
+} sd_group_norm_cfg;
+
+size_t sd_group_norm_workspace_size(const sd_group_norm_cfg* cfg);
+/* gamma, beta: [channels], or NULL for ones and zeros. stats: FP32 [batch][groups]
+ * [2] receives mean and 1/sqrt(var + eps), or NULL. y may be x when ld_x = ld_y. */
+sd_status sd_group_norm_fwd(const sd_group_norm_cfg* cfg, const void* x, const void* gamma, const void* beta, void* y,
+                            float* stats, void* workspace, size_t ws_bytes, sd_stream_t stream);
+/* x, gamma, beta and stats as the forward call had and left them. dx: like x, may
+ * be x, or dy when ld_x = ld_y. dgamma, dbeta: FP32 [channels], each may be NULL;
+ * with no rows they are zeros. */
+sd_status sd_group_norm_bwd(const sd_group_norm_cfg* cfg, const void* x, const void* gamma, const void* beta,
+                            const float* stats, const void* dy, void* dx, float* dgamma, float* dbeta, void* workspace,
+                            size_t ws_bytes, sd_stream_t stream);
+
+/* Gated feed-forward block on a token matrix [TUT FeedForward bullet]:
+ *   [v | z] = x w1^T + b1,  h = v act(z),  y = h w2^T + b2,
+ * GEGLU with SD_ACT_GELU, SwiGLU with SD_ACT_SILU, a bilinear gate with
+ * SD_ACT_NONE. Weights stay in their canonical layout (no packing call, so a
+ * training step can use them as they are): w1 [2 d_hidden, d_in], the value rows
+ * first, then the gate rows; w2 [d_out, d_hidden]. Everything in `dtype` (BF16 or
+ * F16), contiguous, rows in order.
+ *   tokens >= 0; d_in, d_hidden, d_out multiples of 8. */
+typedef struct {
+  int64_t tokens;
+  int32_t d_in;
+  int32_t d_hidden;
+  int32_t d_out;
+  int32_t act;
+  int32_t dtype;
+} sd_gated_ff_cfg;
+
+size_t sd_gated_ff_workspace_size(const sd_gated_ff_cfg* cfg);
+/* b1 [2 d_hidden], b2 [d_out]: may be NULL. pre: NULL, or [tokens, 2 d_hidden]
+ * receives [v | z] for the backward call. h is rounded to dtype between the two
+ * products. */
+sd_status sd_gated_ff_fwd(const sd_gated_ff_cfg* cfg, const void* w1, const void* b1, const void* w2, const void* b2,
+                          const void* x, void* pre, void* y, void* workspace, size_t ws_bytes, sd_stream_t stream);
+/* pre as the forward call left it; dy [tokens, d_out]. Each of dx [tokens, d_in],
+ * dw1, db1, dw2, db2 (shaped as the parameters) may be NULL and is then not
+ * computed; with no tokens the parameter gradients are zeros. The gradients of v,
+ * z and the recomputed h are rounded to dtype between the products. */
+sd_status sd_gated_ff_bwd(const sd_gated_ff_cfg* cfg, const void* w1, const void* w2, const void* x, const void* pre,
+                          const void* dy, void* dx, void* dw1, void* db1, void* dw2, void* db2, void* workspace,
+                          size_t ws_bytes, sd_stream_t stream);
+
 /* Synchronises `stream`, then reads the device error word of `workspace`:
  * SD_OK, or SD_ERR_DEVICE_TIMEOUT when a bounded wait gave up; the word is
  * cleared afterwards. */

@@ -89,6 +89,20 @@ class sd_launch_record(ctypes.Structure):
                 ("bytes", ctypes.c_double), ("ms", c_float)]
 
 
+SD_DTYPE_BF16, SD_DTYPE_F16, SD_DTYPE_F32 = 0, 1, 2
+SD_ACT_NONE, SD_ACT_SILU, SD_ACT_GELU = 0, 1, 2
+
+
+class sd_group_norm_cfg(ctypes.Structure):
+    _fields_ = [("batch", c_int32), ("rows", c_int64), ("channels", c_int32), ("groups", c_int32), ("eps", c_float),
+                ("act", c_int32), ("dtype", c_int32), ("ld_x", c_int64), ("ld_y", c_int64)]
+
+
+class sd_gated_ff_cfg(ctypes.Structure):
+    _fields_ = [("tokens", c_int64), ("d_in", c_int32), ("d_hidden", c_int32), ("d_out", c_int32), ("act", c_int32),
+                ("dtype", c_int32)]
+
+
 FAMILY_NAMES = {0: "gemm_tc", 1: "attention", 2: "gn_stats", 3: "gn_apply", 4: "layernorm", 5: "gemv", 6: "other"}
 
 # name -> (restype, argtypes)
@@ -134,6 +148,12 @@ _SIGS = {
     "sd_denoise_workspace_size": (c_size_t, [POINTER(sd_unet_cfg)]),
     "sd_denoise": (c_int32, [POINTER(sd_unet_cfg), _P, c_int32, POINTER(ctypes.c_double), c_int32, POINTER(c_int32),
                              c_int32, c_float, _P, _P, _P, _P, _P, _P, POINTER(c_float), _P, _P, c_size_t, _P]),
+    "sd_group_norm_workspace_size": (c_size_t, [POINTER(sd_group_norm_cfg)]),
+    "sd_group_norm_fwd": (c_int32, [POINTER(sd_group_norm_cfg), _P, _P, _P, _P, _P, _P, c_size_t, _P]),
+    "sd_group_norm_bwd": (c_int32, [POINTER(sd_group_norm_cfg), _P, _P, _P, _P, _P, _P, _P, _P, _P, c_size_t, _P]),
+    "sd_gated_ff_workspace_size": (c_size_t, [POINTER(sd_gated_ff_cfg)]),
+    "sd_gated_ff_fwd": (c_int32, [POINTER(sd_gated_ff_cfg), _P, _P, _P, _P, _P, _P, _P, _P, c_size_t, _P]),
+    "sd_gated_ff_bwd": (c_int32, [POINTER(sd_gated_ff_cfg), _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, c_size_t, _P]),
     "sd_record_begin": (c_int32, [_P, c_size_t]),
     "sd_record_end": (c_int32, [POINTER(c_int32)]),
     "sd_record_read": (c_int32, [POINTER(sd_record_entry), c_int32, POINTER(c_int32)]),
@@ -421,6 +441,41 @@ def sd_vae_decode(cfg, packed_w, latent, image, workspace, ws_bytes, stream=None
     return _check(s, "sd_vae_decode") if check else s
 
 
+# ---------------------------------------------------------------- operators
+
+def sd_group_norm_workspace_size(cfg):
+    return lib().sd_group_norm_workspace_size(ctypes.byref(cfg))
+
+
+def sd_group_norm_fwd(cfg, x, gamma, beta, y, stats, workspace, ws_bytes, stream=None, check=True):
+    s = lib().sd_group_norm_fwd(ctypes.byref(cfg), _ptr(x), _ptr(gamma), _ptr(beta), _ptr(y), _ptr(stats),
+                                _ptr(workspace), int(ws_bytes), _stream(stream))
+    return _check(s, "sd_group_norm_fwd") if check else s
+
+
+def sd_group_norm_bwd(cfg, x, gamma, beta, stats, dy, dx, dgamma, dbeta, workspace, ws_bytes, stream=None, check=True):
+    s = lib().sd_group_norm_bwd(ctypes.byref(cfg), _ptr(x), _ptr(gamma), _ptr(beta), _ptr(stats), _ptr(dy), _ptr(dx),
+                                _ptr(dgamma), _ptr(dbeta), _ptr(workspace), int(ws_bytes), _stream(stream))
+    return _check(s, "sd_group_norm_bwd") if check else s
+
+
+def sd_gated_ff_workspace_size(cfg):
+    return lib().sd_gated_ff_workspace_size(ctypes.byref(cfg))
+
+
+def sd_gated_ff_fwd(cfg, w1, b1, w2, b2, x, pre, y, workspace, ws_bytes, stream=None, check=True):
+    s = lib().sd_gated_ff_fwd(ctypes.byref(cfg), _ptr(w1), _ptr(b1), _ptr(w2), _ptr(b2), _ptr(x), _ptr(pre), _ptr(y),
+                              _ptr(workspace), int(ws_bytes), _stream(stream))
+    return _check(s, "sd_gated_ff_fwd") if check else s
+
+
+def sd_gated_ff_bwd(cfg, w1, w2, x, pre, dy, dx, dw1, db1, dw2, db2, workspace, ws_bytes, stream=None, check=True):
+    s = lib().sd_gated_ff_bwd(ctypes.byref(cfg), _ptr(w1), _ptr(w2), _ptr(x), _ptr(pre), _ptr(dy), _ptr(dx),
+                              _ptr(dw1), _ptr(db1), _ptr(dw2), _ptr(db2), _ptr(workspace), int(ws_bytes),
+                              _stream(stream))
+    return _check(s, "sd_gated_ff_bwd") if check else s
+
+
 def sd_query_device_status(workspace, stream=None):
     return lib().sd_query_device_status(_ptr(workspace), _stream(stream))
 
@@ -470,6 +525,14 @@ def resblock_cfg(height, width, c_x, c_out, c_skip=0, temb_dim=1280, groups=32, 
 
 def transformer_cfg(height, width, channels, depth=1, ctx_len=77, ctx_dim=1024, groups=32, eps=1e-5):
     return sd_transformer_cfg(1, height, width, channels, 64, depth, ctx_len, ctx_dim, groups, eps, eps)
+
+
+def group_norm_cfg(batch, rows, channels, groups=32, eps=1e-5, act=SD_ACT_SILU, dtype=SD_DTYPE_BF16, ld_x=0, ld_y=0):
+    return sd_group_norm_cfg(batch, rows, channels, groups, eps, act, dtype, ld_x, ld_y)
+
+
+def gated_ff_cfg(tokens, d_in, d_hidden, d_out=None, act=SD_ACT_GELU, dtype=SD_DTYPE_BF16):
+    return sd_gated_ff_cfg(tokens, d_in, d_hidden, d_in if d_out is None else d_out, act, dtype)
 
 
 def unet_cfg(in_channels=4, out_channels=4, height=96, width=96, block_channels=(320, 640, 1280, 1280),

@@ -1,0 +1,159 @@
+// Shared pieces of the standalone operators (group norm, gated feed-forward,
+// attention): element types, activations with their derivatives, the tcgen05
+// forms they need beyond common.cuh, and the host-side checks.
+#pragma once
+
+#include "common.cuh"
+#include "sd_api.h"
+
+namespace sdo {
+
+using namespace sdk;
+
+// ------------------------------------------------------------------ element types
+template <typename T>
+struct Elem;
+template <>
+struct Elem<__nv_bfloat16> {
+  static constexpr bool kF16 = false;
+  static __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+  static __device__ __forceinline__ __nv_bfloat16 from_f(float v) { return __float2bfloat16_rn(v); }
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) { return pack_bf16x2(lo, hi); }
+  static __device__ __forceinline__ float lo(uint32_t v) { return bf16lo(v); }
+  static __device__ __forceinline__ float hi(uint32_t v) { return bf16hi(v); }
+};
+template <>
+struct Elem<__half> {
+  static constexpr bool kF16 = true;
+  static __device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
+  static __device__ __forceinline__ __half from_f(float v) { return __float2half_rn(v); }
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) { return pack_f16x2(lo, hi); }
+  static __device__ __forceinline__ float lo(uint32_t v) {
+    return __low2float(*reinterpret_cast<const __half2*>(&v));
+  }
+  static __device__ __forceinline__ float hi(uint32_t v) {
+    return __high2float(*reinterpret_cast<const __half2*>(&v));
+  }
+};
+template <>
+struct Elem<float> {
+  static __device__ __forceinline__ float to_f(float v) { return v; }
+  static __device__ __forceinline__ float from_f(float v) { return v; }
+};
+
+// V consecutive elements as FP32: one 16-byte access when V fills it, else element by element.
+template <typename T, int V>
+__device__ __forceinline__ void unpack_vec(const uint4& raw, float (&f)[V]) {
+  if constexpr (sizeof(T) == 2) {
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = Elem<T>::lo(w[i]);
+      f[2 * i + 1] = Elem<T>::hi(w[i]);
+    }
+  } else {
+    f[0] = __uint_as_float(raw.x);
+    f[1] = __uint_as_float(raw.y);
+    f[2] = __uint_as_float(raw.z);
+    f[3] = __uint_as_float(raw.w);
+  }
+}
+template <typename T, int V>
+__device__ __forceinline__ uint4 pack_vec(const float (&f)[V]) {
+  if constexpr (sizeof(T) == 2)
+    return make_uint4(Elem<T>::pack(f[0], f[1]), Elem<T>::pack(f[2], f[3]), Elem<T>::pack(f[4], f[5]),
+                      Elem<T>::pack(f[6], f[7]));
+  else
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+}
+template <typename T>
+constexpr int kVec = 16 / (int)sizeof(T);
+
+// ------------------------------------------------------------------ activations
+// 2^x and 1/x as one instruction each: relative errors near 2^-22, far below
+// half a step of the 16-bit types and below 1e-6 for FP32 outputs.
+__device__ __forceinline__ float fast_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float fast_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// 1 / (1 + e^-z); e^-z overflows to infinity below z = -88, where the result is 0.
+__device__ __forceinline__ float sigmoid_f(float z) { return fast_rcp(1.f + fast_ex2(-kLog2e * z)); }
+
+__device__ __forceinline__ float act_f(float z, int act) {
+  if (act == SD_ACT_SILU) return z * sigmoid_f(z);
+  if (act == SD_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+  return z;
+}
+// a = act(z), d = act'(z)
+__device__ __forceinline__ void act_grad_f(float z, int act, float& a, float& d) {
+  if (act == SD_ACT_SILU) {
+    const float s = sigmoid_f(z);
+    a = z * s;
+    d = s + a * (1.f - s);
+  } else if (act == SD_ACT_GELU) {
+    const float cdf = 0.5f * (1.f + erff(z * 0.70710678118654752f));
+    a = z * cdf;
+    d = fmaf(z * 0.39894228040143268f, fast_ex2(-0.5f * kLog2e * z * z), cdf);
+  } else {
+    a = z;
+    d = 1.f;
+  }
+}
+
+// ------------------------------------------------------------------ host side
+struct Device {
+  int index, sms;
+};
+// The current device's index and SM count; SD_ERR_NOT_SM100 off compute capability 10.0.
+sd_status current_device(Device* d);
+
+inline bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) != 0; }
+inline size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
+
+// Workspace bytes before an operator's own scratch: word 0 holds the device error
+// flags, which the first kernel of every call clears.
+constexpr size_t kOpHeader = 256;
+
+inline sd_status check_workspace(size_t need, const void* ws, size_t ws_bytes) {
+  if (!ws) return SD_ERR_NULL_ARG;
+  if (misaligned(ws)) return SD_ERR_MISALIGNED;
+  if (ws_bytes < need) return SD_ERR_WORKSPACE_TOO_SMALL;
+  return SD_OK;
+}
+
+// Raises a kernel's shared-memory limit once per device (the attribute belongs to
+// the device's copy of the kernel).
+template <auto kernel>
+inline sd_status allow_smem(size_t bytes, int device) {
+  static unsigned long long done = 0;  // one bit per device; a race sets the same value again
+  if ((__atomic_load_n(&done, __ATOMIC_RELAXED) >> device) & 1) return SD_OK;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return SD_ERR_LAUNCH;
+  }
+  __atomic_fetch_or(&done, 1ull << device, __ATOMIC_RELAXED);
+  return SD_OK;
+}
+
+inline sd_status launched(cudaError_t e) {
+  if (e == cudaSuccess) return SD_OK;
+  (void)cudaGetLastError();
+  return SD_ERR_LAUNCH;
+}
+
+#define OP_TRY(x)                      \
+  do {                                 \
+    const sd_status _s = (x);          \
+    if (_s != SD_OK) return _s;        \
+  } while (0)
+
+}  // namespace sdo
