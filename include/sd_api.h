@@ -386,7 +386,7 @@ sd_status sd_vae_decode(const sd_vae_cfg* cfg, const void* packed_w, const void*
                         void* workspace, size_t ws_bytes, sd_stream_t stream);
 
 /* ---------------------------------------------------------------- operators
- * The operators that the blocks above are made of, by themselves: for any
+ * The three operators that the blocks above are made of, by themselves: for any
  * batch, with masks, in other types, and with their gradients. They follow the
  * conventions at the top of this file, with these additions:
  *   - sizes of zero are allowed where said; a call that has nothing to write
@@ -470,6 +470,65 @@ sd_status sd_gated_ff_fwd(const sd_gated_ff_cfg* cfg, const void* w1, const void
 sd_status sd_gated_ff_bwd(const sd_gated_ff_cfg* cfg, const void* w1, const void* w2, const void* x, const void* pre,
                           const void* dy, void* dx, void* dw1, void* db1, void* dw2, void* db2, void* workspace,
                           size_t ws_bytes, sd_stream_t stream);
+
+/* Attention [SD15 section 3.4] with masks, capped scores and a distance bias. For
+ * query i and key j of head h (of key head h / (heads / kv_heads)):
+ *   s = scale q_i . k_j;  s = softcap tanh(s / softcap) if softcap > 0;
+ *   s = s - slopes[h] |p_i - j|,  p_i = n_b - q_len + i: the queries are the last
+ *   q_len positions of a sequence of n_b keys (n_b = k_lens[b], else k_len);
+ *   o_i = sum_j softmax_j(s) v_j over the keys that i sees:
+ *     j < n_b, and (not causal, or j <= p_i, or j < prefix[b]),
+ *     and q_doc[b][i] = k_doc[b][j].
+ * A query that sees no key gets o = 0, lse = -infinity and no gradient.
+ *   batch, q_len, k_len >= 0 (k_len <= 2^20); heads a multiple of kv_heads, at most
+ *   128 query heads per key head; head_dim a multiple of 8, at most 128; dtype BF16
+ *   or F16. scale 0 means 1/sqrt(head_dim); softcap 0 means none.
+ *   q_stride, k_stride, v_stride, o_stride: elements from one sequence, token and
+ *   head to the next (multiples of 8, below 2^38), so a projection's output is read in
+ *   place; all zero = contiguous [batch][token][head][head_dim]. */
+typedef struct {
+  int32_t batch;
+  int32_t q_len;
+  int32_t k_len;
+  int32_t heads;
+  int32_t kv_heads;
+  int32_t head_dim;
+  int32_t dtype;
+  int32_t causal;
+  float scale;
+  float softcap;
+  int64_t q_stride[3];
+  int64_t k_stride[3];
+  int64_t v_stride[3];
+  int64_t o_stride[3];
+} sd_attention_cfg;
+
+/* Device arrays, each may be NULL (as may the struct):
+ *   k_lens [batch]: keys that exist, clamped to 0 .. k_len. Keys and values behind
+ *     them are never used, whatever they hold (their gradients are zeros).
+ *   prefix [batch]: keys that every query sees although causal; needs causal.
+ *   q_doc [batch][q_len] and k_doc [batch][k_len]: document ids, both or none.
+ *   slopes [heads]: FP32 distance slopes, constants of the call.
+ * Keys and values hidden by anything but k_lens have to be finite. */
+typedef struct {
+  const int32_t* k_lens;
+  const int32_t* prefix;
+  const int32_t* q_doc;
+  const int32_t* k_doc;
+  const float* slopes;
+} sd_attention_masks;
+
+size_t sd_attention_workspace_size(const sd_attention_cfg* cfg);
+/* lse: NULL, or FP32 [batch][heads][q_len] receives log sum_j e^s. */
+sd_status sd_attention_fwd(const sd_attention_cfg* cfg, const void* q, const void* k, const void* v,
+                           const sd_attention_masks* masks, void* o, float* lse, void* workspace, size_t ws_bytes,
+                           sd_stream_t stream);
+/* q, k, v, masks as the forward call had them, o and lse as it left them; d_o
+ * strided like o, dq, dk, dv like q, k, v. The gradients of shared key heads are
+ * summed over their query heads; the slopes get none. */
+sd_status sd_attention_bwd(const sd_attention_cfg* cfg, const void* q, const void* k, const void* v,
+                           const sd_attention_masks* masks, const void* o, const float* lse, const void* d_o, void* dq,
+                           void* dk, void* dv, void* workspace, size_t ws_bytes, sd_stream_t stream);
 
 /* Synchronises `stream`, then reads the device error word of `workspace`:
  * SD_OK, or SD_ERR_DEVICE_TIMEOUT when a bounded wait gave up; the word is

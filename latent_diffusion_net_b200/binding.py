@@ -103,6 +103,18 @@ class sd_gated_ff_cfg(ctypes.Structure):
                 ("dtype", c_int32)]
 
 
+class sd_attention_cfg(ctypes.Structure):
+    _fields_ = [("batch", c_int32), ("q_len", c_int32), ("k_len", c_int32), ("heads", c_int32), ("kv_heads", c_int32),
+                ("head_dim", c_int32), ("dtype", c_int32), ("causal", c_int32), ("scale", c_float),
+                ("softcap", c_float), ("q_stride", c_int64 * 3), ("k_stride", c_int64 * 3), ("v_stride", c_int64 * 3),
+                ("o_stride", c_int64 * 3)]
+
+
+class sd_attention_masks(ctypes.Structure):
+    _fields_ = [("k_lens", c_void_p), ("prefix", c_void_p), ("q_doc", c_void_p), ("k_doc", c_void_p),
+                ("slopes", c_void_p)]
+
+
 FAMILY_NAMES = {0: "gemm_tc", 1: "attention", 2: "gn_stats", 3: "gn_apply", 4: "layernorm", 5: "gemv", 6: "other"}
 
 # name -> (restype, argtypes)
@@ -154,6 +166,11 @@ _SIGS = {
     "sd_gated_ff_workspace_size": (c_size_t, [POINTER(sd_gated_ff_cfg)]),
     "sd_gated_ff_fwd": (c_int32, [POINTER(sd_gated_ff_cfg), _P, _P, _P, _P, _P, _P, _P, _P, c_size_t, _P]),
     "sd_gated_ff_bwd": (c_int32, [POINTER(sd_gated_ff_cfg), _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, c_size_t, _P]),
+    "sd_attention_workspace_size": (c_size_t, [POINTER(sd_attention_cfg)]),
+    "sd_attention_fwd": (c_int32, [POINTER(sd_attention_cfg), _P, _P, _P, POINTER(sd_attention_masks), _P, _P, _P,
+                                   c_size_t, _P]),
+    "sd_attention_bwd": (c_int32, [POINTER(sd_attention_cfg), _P, _P, _P, POINTER(sd_attention_masks), _P, _P, _P, _P,
+                                   _P, _P, _P, c_size_t, _P]),
     "sd_record_begin": (c_int32, [_P, c_size_t]),
     "sd_record_end": (c_int32, [POINTER(c_int32)]),
     "sd_record_read": (c_int32, [POINTER(sd_record_entry), c_int32, POINTER(c_int32)]),
@@ -476,6 +493,29 @@ def sd_gated_ff_bwd(cfg, w1, w2, x, pre, dy, dx, dw1, db1, dw2, db2, workspace, 
     return _check(s, "sd_gated_ff_bwd") if check else s
 
 
+def attention_masks(k_lens=None, prefix=None, q_doc=None, k_doc=None, slopes=None):
+    """Device tensors (int32; slopes FP32) or None; the struct keeps their addresses, the caller the tensors."""
+    return sd_attention_masks(_ptr(k_lens), _ptr(prefix), _ptr(q_doc), _ptr(k_doc), _ptr(slopes))
+
+
+def sd_attention_workspace_size(cfg):
+    return lib().sd_attention_workspace_size(ctypes.byref(cfg))
+
+
+def sd_attention_fwd(cfg, q, k, v, masks, o, lse, workspace, ws_bytes, stream=None, check=True):
+    m = ctypes.byref(masks) if masks is not None else None
+    s = lib().sd_attention_fwd(ctypes.byref(cfg), _ptr(q), _ptr(k), _ptr(v), m, _ptr(o), _ptr(lse), _ptr(workspace),
+                               int(ws_bytes), _stream(stream))
+    return _check(s, "sd_attention_fwd") if check else s
+
+
+def sd_attention_bwd(cfg, q, k, v, masks, o, lse, d_o, dq, dk, dv, workspace, ws_bytes, stream=None, check=True):
+    m = ctypes.byref(masks) if masks is not None else None
+    s = lib().sd_attention_bwd(ctypes.byref(cfg), _ptr(q), _ptr(k), _ptr(v), m, _ptr(o), _ptr(lse), _ptr(d_o),
+                               _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace), int(ws_bytes), _stream(stream))
+    return _check(s, "sd_attention_bwd") if check else s
+
+
 def sd_query_device_status(workspace, stream=None):
     return lib().sd_query_device_status(_ptr(workspace), _stream(stream))
 
@@ -533,6 +573,15 @@ def group_norm_cfg(batch, rows, channels, groups=32, eps=1e-5, act=SD_ACT_SILU, 
 
 def gated_ff_cfg(tokens, d_in, d_hidden, d_out=None, act=SD_ACT_GELU, dtype=SD_DTYPE_BF16):
     return sd_gated_ff_cfg(tokens, d_in, d_hidden, d_in if d_out is None else d_out, act, dtype)
+
+
+def attention_cfg(batch, q_len, k_len, heads, kv_heads=None, head_dim=64, dtype=SD_DTYPE_BF16, causal=False, scale=0.0,
+                  softcap=0.0, q_stride=(0, 0, 0), k_stride=(0, 0, 0), v_stride=(0, 0, 0), o_stride=(0, 0, 0)):
+    """Strides in elements: (sequence, token, head); all zero = contiguous [batch][token][head][head_dim]."""
+    c3 = c_int64 * 3
+    return sd_attention_cfg(batch, q_len, k_len, heads, heads if kv_heads is None else kv_heads, head_dim, dtype,
+                            int(bool(causal)), scale, softcap, c3(*q_stride), c3(*k_stride), c3(*v_stride),
+                            c3(*o_stride))
 
 
 def unet_cfg(in_channels=4, out_channels=4, height=96, width=96, block_channels=(320, 640, 1280, 1280),

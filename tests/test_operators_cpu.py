@@ -93,3 +93,50 @@ def test_workspaces_cover_every_size():
     for n, r in ((1, 1), (64, 4096), (4096, 1)):
         cfg = B.group_norm_cfg(n, r, 320)
         assert B.sd_group_norm_workspace_size(cfg) >= n * 32 * 8
+
+
+def at_fwd(cfg, q=P, k=P, v=P, o=P, ws=P, n=None, masks=None, lse=None):
+    n = B.sd_attention_workspace_size(cfg) if n is None else n
+    return B.sd_attention_fwd(cfg, q, k, v, masks, o, lse, ws, n, check=False)
+
+
+def at_bwd(cfg, q=P, k=P, v=P, o=P, lse=P, d_o=P, dq=P, dk=P, dv=P, ws=P, n=None, masks=None):
+    n = B.sd_attention_workspace_size(cfg) if n is None else n
+    return B.sd_attention_bwd(cfg, q, k, v, masks, o, lse, d_o, dq, dk, dv, ws, n, check=False)
+
+
+def test_attention_refusals():
+    ok = B.attention_cfg(2, 100, 200, 8, 2, 64, causal=True)
+    size = B.sd_attention_workspace_size(ok)
+    assert at_fwd(ok) in NO_DEVICE and at_bwd(ok) in NO_DEVICE
+    for name in ("q", "k", "v", "o", "ws"):
+        assert at_fwd(ok, **{name: None}) == NULL, name
+    for name in ("q", "k", "v", "o", "lse", "d_o", "dq", "dk", "dv", "ws"):
+        assert at_bwd(ok, **{name: None}) == NULL, name
+        assert at_bwd(ok, **{name: P + 8}) == MISALIGNED, name
+    assert at_fwd(ok, lse=P + 4) == MISALIGNED
+    assert at_fwd(ok, n=size - 1) == SMALL and at_bwd(ok, n=size - 1) == SMALL
+    c = B.attention_cfg
+    for bad, code in [(c(-1, 1, 1, 1), SHAPE), (c(1, -1, 1, 1), SHAPE), (c(1, 1, -1, 1), SHAPE), (c(1, 1, 1, 0), SHAPE),
+                      (c(1, 1, 1, 8, 3), SHAPE), (c(1, 1, 1, 8, 0), SHAPE), (c(1, 1, 1, 1, 1, 0), SHAPE),
+                      (c(1, 1, 1, 1, 1, 64, scale=-1.0), SHAPE), (c(1, 1, 1, 1, 1, 64, scale=float("nan")), SHAPE),
+                      (c(1, 1, 1, 1, 1, 64, scale=1e30), SHAPE), (c(1, 1, 1, 1, 1, 64, softcap=-1.0), SHAPE),
+                      (c(1, 1, 1, 1, 1, 64, softcap=float("inf")), SHAPE),
+                      (c(1, 1, 1, 1, 1, 60), UNSUPPORTED), (c(1, 1, 1, 1, 1, 136), UNSUPPORTED),
+                      (c(1, 1, 1, 256, 1, 64), UNSUPPORTED), (c(1, 1, (1 << 20) + 1, 1), UNSUPPORTED),
+                      (c(1, (1 << 20) + 1, 1, 1), UNSUPPORTED), (c(1, 1, 1, 1, dtype=B.SD_DTYPE_F32), UNSUPPORTED),
+                      # strides: steps of 16 bytes, never backwards, never in place where there is more than one
+                      (c(2, 4, 4, 2, q_stride=(512, 128, 60)), SHAPE), (c(2, 4, 4, 2, k_stride=(512, 0, 64)), SHAPE),
+                      (c(2, 4, 4, 2, v_stride=(-512, 128, 64)), SHAPE),
+                      (c(2, 4, 4, 2, o_stride=(1 << 40, 128, 64)), SHAPE)]:
+        assert at_fwd(bad, n=1 << 40) == code and at_bwd(bad, n=1 << 40) == code
+        assert B.sd_attention_workspace_size(bad) == 0
+    # a stride that is never stepped may be anything
+    assert at_fwd(c(1, 1, 4, 2, q_stride=(0, 0, 64)), n=1 << 40) in NO_DEVICE
+    m = B.attention_masks
+    assert at_fwd(ok, masks=m(q_doc=P)) == NULL and at_fwd(ok, masks=m(k_doc=P)) == NULL
+    assert at_fwd(ok, masks=m(k_lens=P + 4)) == MISALIGNED and at_bwd(ok, masks=m(slopes=P + 4)) == MISALIGNED
+    assert at_fwd(c(2, 100, 200, 8, 2, 64), masks=m(prefix=P)) == SHAPE  # a prefix without a causal mask
+    assert at_fwd(ok, masks=m(prefix=P, k_lens=P, q_doc=P, k_doc=P, slopes=P)) in NO_DEVICE
+    assert at_fwd(c(0, 4, 4, 1), q=None, k=None, v=None, o=None, ws=None) == OK
+    assert at_fwd(c(1, 0, 4, 1), q=None, k=None, v=None, o=None, ws=None) == OK
