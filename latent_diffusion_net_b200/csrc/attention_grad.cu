@@ -4,25 +4,33 @@
 //   dQ = scale dS K.
 //
 // Bound by the tensor cores (10 D operations a pair in five products). Two kernels
-// recompute S and dP each, seven products in all, so that every gradient is
-// accumulated by one CTA in a fixed order: no atomics, results repeat bit for bit.
+// recompute S and dP each, so that every gradient is accumulated by one CTA in a
+// fixed order: no atomics, results repeat bit for bit.
+//   attn_dq_kernel   128 queries of one head walk their key tiles. delta from the saved
+//                    o carries o's rounding, which is no longer small beside dP - delta
+//                    where a row sees few keys; since the exact dS of a row sums to
+//                    zero, the row sum e of the computed P (dP - delta) is delta's
+//                    error, and dQ = scale (dS K - e P K) with P K as a third
+//                    accumulator is exact to FP32. The corrected delta is left for
 //   attn_dkv_kernel  a CTA owns 128 keys of one key head and walks the (head, query
 //                    tile) pairs that may see them: S^T = K Q^T and dP^T = V dO^T
 //                    have the keys as rows, so P^T and dS^T go from registers to
 //                    TMEM as A operands of dV += P^T dO and dK += dS^T Q, and no
 //                    transposed copy of anything is made
-//   attn_dq_kernel   a CTA owns 128 queries of one head and walks the key tiles
 // Few CTAs and a long walk: the walk is split and FP32 parts are joined in order.
 //
-// 320 threads, one CTA per SM: warps 0-7 turn scores into P and dS (two warps per
-// TMEM lane quarter, half of the columns each), warp 8 loads by TMA, one thread of
-// warp 9 issues the products. P and dS are rounded to the inputs' type (the tensor
-// core takes no other); everything else is FP32. For FP16 inputs P carries a
-// factor 2^shift (taken out of the results again) that keeps the small
-// probabilities of long sequences above FP16's subnormals.
+// 576 threads, one CTA per SM: warps 0-15 turn scores into P and dS (four warps per
+// TMEM lane quarter, 32 of the columns each: with eight warps of 64 columns a tile took
+// 1.8 times as long, the warps waiting for instructions and for one another), warp 16
+// loads by TMA, one thread of warp 17 issues the products: S of the next tile runs
+// beside dS of this one. P and dS
+// are rounded to the inputs' type (the tensor core takes no other); everything else is
+// FP32. For FP16 inputs P carries a factor 2^shift (taken out of the results again)
+// that keeps the small probabilities of long sequences above FP16's subnormals.
 #include <string.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "attention_op.cuh"
 #include "profile.h"
@@ -30,8 +38,8 @@
 namespace sdo {
 namespace {
 
-constexpr int kThreads = 320;
-constexpr int kCompute = 256;
+constexpr int kThreads = 576;
+constexpr int kCompute = 512;   // threads of the computing warps
 constexpr int kSms = 148;
 constexpr int kMaxSplits = 32;
 
@@ -39,8 +47,9 @@ struct GradArgs {
   AttnArgs f;
   int32_t qpad;         // query rows of lse2 and delta: a multiple of 128
   int32_t qblocks;      // 128-query tiles
-  float* lse2;          // [B][H][qpad] log2-domain sums, +inf where a row sees nothing or does not exist
-  float* delta;         // [B][H][qpad]
+  int32_t units;        // attn_dq_kernel: query tiles x heads x sequences x splits
+  float* nlse;          // [B][H][qpad] -lse in log2 units; -inf where a row sees nothing or does not exist
+  float* ndelta;        // [B][H][qpad] -delta
   const float* lse;
   const void* d_o;
   float out_scale, v_scale;  // factors of dQ and dK, of dV
@@ -48,90 +57,165 @@ struct GradArgs {
   int64_t s0[3], s1[3];      // output strides: dQ, or dK and dV
   void *out0, *out1;
   float* part;               // [splits][...] FP32 parts
+  float* part_e;             // attn_dq_kernel with splits: row sums e [splits][B][H][qpad]
 };
 
 struct __align__(64) GradMaps {
   CUtensorMap q, k, v, d_o;
 };
 
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   smem_u32(dst)),
-               "l"(src), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
-}
-
-// lse in log2 units and delta, 16 lanes per query row; rows up to qpad.
+// -lse in log2 units and -delta for rows up to qpad: 2^shift lanes share a row, eight
+// head dimensions each, and take four rows so that eight loads are under way.
 template <typename T>
-__global__ void __launch_bounds__(256) attn_delta_kernel(const __grid_constant__ GradArgs g) {
+__global__ void __launch_bounds__(256) attn_delta_kernel(const __grid_constant__ GradArgs g, int shift) {
   pdl_wait();
   pdl_trigger();
   const AttnArgs& a = g.f;
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.err = 0;
-  const int sub = threadIdx.x & 15;
-  const int64_t r = blockIdx.x * (int64_t)16 + (threadIdx.x >> 4);
-  if (r >= (int64_t)a.B * a.H * g.qpad) return;
-  const int i = (int)(r % g.qpad), h = (int)(r / g.qpad % a.H), b = (int)(r / g.qpad / a.H);
-  float s = 0.f;
-  if (i < a.Nq && sub * 8 < a.D) {
-    const int64_t at = b * a.os[0] + i * a.os[1] + h * a.os[2] + sub * 8;
-    float x[8], y[8];
-    unpack_vec<T, 8>(*reinterpret_cast<const uint4*>(static_cast<const T*>(a.o) + at), x);
-    unpack_vec<T, 8>(*reinterpret_cast<const uint4*>(static_cast<const T*>(g.d_o) + at), y);
+  const int sub = threadIdx.x & ((1 << shift) - 1), groups = 256 >> shift;
+  const int64_t rows = (int64_t)a.B * a.H * g.qpad, r0 = blockIdx.x * (int64_t)groups * 4 + (threadIdx.x >> shift);
+  uint4 x[4], y[4];
+  float lse[4];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) s = fmaf(x[u], y[u], s);
-  }
-  const uint32_t mask = 0xFFFFu << (threadIdx.x & 16);
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(mask, s, o);
-  if (sub == 0) {
-    const float lse = i < a.Nq ? g.lse[((int64_t)b * a.H + h) * a.Nq + i] : -INFINITY;
-    g.lse2[r] = lse == -INFINITY ? INFINITY : fmaf(lse, kLog2e, -g.shift);
-    g.delta[r] = s;
-  }
-}
-
-// Marks the tiles that the CTA visits; `base` rows against tiles of 128 columns.
-template <typename F>
-__device__ __forceinline__ void list_tiles(TileBits* tiles, int ntiles, int warp, int lane, F&& f) {
-  const int words = (ntiles + 31) >> 5;
-  for (int w = warp; w < words; w += kThreads / 32) {
-    const int t = w * 32 + lane;
-    bool see = false, all = false;
-    if (t < ntiles) f(t, see, all);
-    const uint32_t ms = __ballot_sync(0xffffffffu, see), ma = __ballot_sync(0xffffffffu, see && all);
-    if (lane == 0) {
-      tiles->see[w] = ms;
-      tiles->all[w] = ma;
+  for (int k = 0; k < 4; ++k) {
+    const int64_t r = r0 + k * groups;
+    // rows in the order of (token, head), in which o lies when it is contiguous
+    const int h = (int)(r % a.H), i = (int)(r / a.H % g.qpad), b = (int)(r / a.H / g.qpad);
+    x[k] = y[k] = make_uint4(0u, 0u, 0u, 0u);
+    lse[k] = -INFINITY;
+    if (r < rows && i < a.Nq) {
+      if (sub * 8 < a.D) {
+        const int64_t at = b * a.os[0] + i * a.os[1] + h * a.os[2] + sub * 8;
+        x[k] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.o) + at);
+        y[k] = *reinterpret_cast<const uint4*>(static_cast<const T*>(g.d_o) + at);
+      }
+      if (sub == 0) lse[k] = g.lse[((int64_t)b * a.H + h) * a.Nq + i];
     }
   }
-  __syncthreads();
-  if (warp == 0) {
-    int n = 0;
-    for (int w = lane; w < words; w += 32) n += __popc(tiles->see[w]);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-    if (lane == 0) tiles->count = n;
+  for (int k = 0; k < 4; ++k) {
+    const int64_t r = r0 + k * groups;
+    float u[8], v[8], s = 0.f;
+    unpack_vec<T, 8>(x[k], u);
+    unpack_vec<T, 8>(y[k], v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s = fmaf(u[e], v[e], s);
+    for (int o = 1 << shift >> 1; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (sub == 0 && r < rows) {
+      const int h = (int)(r % a.H), i = (int)(r / a.H % g.qpad), b = (int)(r / a.H / g.qpad);
+      const int64_t at = ((int64_t)b * a.H + h) * g.qpad + i;
+      g.nlse[at] = lse[k] == -INFINITY ? -INFINITY : fmaf(-lse[k], kLog2e, g.shift);
+      g.ndelta[at] = -s;
+    }
   }
-  __syncthreads();
 }
 
-// The score in log2 units and the cap's slope, without the bias.
-__device__ __forceinline__ float score(const AttnArgs& a, float s, float& fac) {
-  if (a.cap_out != 0.f) {
-    const float t = tanh_acc(s * a.cap_in);
-    fac = fmaf(-t, t, 1.f);
-    return a.cap_out * t;
+// What becomes of one 16-column chunk of scores: p, p times the cap's slope, and that
+// slope as FP16 pairs where asked for. The scores' columns lie `c` columns from the diagonal's column p0.
+// SHAPED: cap or bias; MASKED: columns outside [from, to) and of other documents are hidden.
+struct ScoreTerms {
+  float slope, p0;
+  int from, to, doc;
+  const int32_t* sdoc;  // the columns' documents, or null
+};
+template <bool SHAPED, bool MASKED>
+__device__ __forceinline__ void probabilities(const AttnArgs& a, const ScoreTerms& s, const uint32_t (&r)[16], int c,
+                                              const float (&nl)[16], float* p, float* pf, uint32_t* fac = nullptr) {
+  bool small = false;
+  if constexpr (SHAPED) {
+    if (a.cap_out != 0.f) {
+      float top = 0.f;
+#pragma unroll
+      for (int u = 0; u < 16; u += 2)
+        top = max3f(top, fabsf(__uint_as_float(r[u])), fabsf(__uint_as_float(r[u + 1])));
+      small = __all_sync(0xffffffffu, top * a.cap_in <= kTanhSmall);
+    }
   }
-  fac = 1.f;
-  return s * a.sl2;
+  auto two = [&](int u, auto form) {
+    constexpr int kForm = decltype(form)::value;  // 0: no cap, 1: tanh of small values, 2: any
+    float x0, x1, f0 = 1.f, f1 = 1.f;
+    if constexpr (kForm > 0) {
+      mul2(__uint_as_float(r[u]), __uint_as_float(r[u + 1]), a.cap_in, a.cap_in, x0, x1);
+      if constexpr (kForm == 1) {
+        tanh_small2(x0, x1, x0, x1);
+      } else {
+        x0 = tanh_acc(x0);
+        x1 = tanh_acc(x1);
+      }
+      fma2v(-x0, -x1, x0, x1, 1.f, 1.f, f0, f1);
+      fma2v(x0, x1, a.cap_out, a.cap_out, nl[u], nl[u + 1], x0, x1);
+    } else {
+      fma2v(__uint_as_float(r[u]), __uint_as_float(r[u + 1]), a.sl2, a.sl2, nl[u], nl[u + 1], x0, x1);
+    }
+    if constexpr (SHAPED) {
+      x0 = fmaf(-s.slope, fabsf(s.p0 + (float)(c + u)), x0);
+      x1 = fmaf(-s.slope, fabsf(s.p0 + (float)(c + u + 1)), x1);
+    }
+    p[u] = fast_ex2(x0);
+    p[u + 1] = fast_ex2(x1);
+    if constexpr (MASKED) {
+      bool h0 = c + u < s.from || c + u >= s.to, h1 = c + u + 1 < s.from || c + u + 1 >= s.to;
+      if (s.sdoc) {
+        const int2 d = *reinterpret_cast<const int2*>(s.sdoc + c + u);
+        h0 = h0 || d.x != s.doc;
+        h1 = h1 || d.y != s.doc;
+      }
+      if (h0) p[u] = 0.f;
+      if (h1) p[u + 1] = 0.f;
+    }
+    if constexpr (kForm > 0) {
+      mul2(p[u], p[u + 1], f0, f1, pf[u], pf[u + 1]);
+    } else {
+      pf[u] = p[u];
+      pf[u + 1] = p[u + 1];
+    }
+    if constexpr (SHAPED) {
+      if (fac) fac[u / 2] = pack_f16x2(f0, f1);
+    }
+  };
+  if constexpr (SHAPED) {
+    if (a.cap_out != 0.f) {
+      if (small) {
+#pragma unroll
+        for (int u = 0; u < 16; u += 2) two(u, std::integral_constant<int, 1>());
+      } else {
+#pragma unroll
+        for (int u = 0; u < 16; u += 2) two(u, std::integral_constant<int, 2>());
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < 16; u += 2) two(u, std::integral_constant<int, 0>());
+}
+// dS = pf (dP + nd) with nd = -delta. MASKED: dP of keys that do not exist may be anything.
+template <bool MASKED>
+__device__ __forceinline__ void score_grads(const uint32_t (&r)[16], const float (&nd)[16], const float* pf,
+                                            float (&ds)[16]) {
+#pragma unroll
+  for (int u = 0; u < 16; u += 2) {
+    float x0, x1;
+    add2(__uint_as_float(r[u]), __uint_as_float(r[u + 1]), nd[u], nd[u + 1], x0, x1);
+    mul2(x0, x1, pf[u], pf[u + 1], ds[u], ds[u + 1]);
+    if constexpr (MASKED) {
+      if (pf[u] == 0.f) ds[u] = 0.f;
+      if (pf[u + 1] == 0.f) ds[u + 1] = 0.f;
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ void pack16(const float* f, uint32_t (&pk)[8]) {
+#pragma unroll
+  for (int u = 0; u < 8; ++u) pk[u] = Elem<T>::pack(f[2 * u], f[2 * u + 1]);
 }
 
-// One row of an accumulator: to the output (scaled), or to the FP32 part.
+// Half `side` of the columns of one row of an accumulator: to the output (scaled), or to
+// the FP32 part.
 template <typename T, int NB>
-__device__ __forceinline__ void store_row(uint32_t tacc, bool have, bool in, int D, float scale, T* dst, float* part) {
+__device__ __forceinline__ void store_row(uint32_t tacc, int side, bool have, bool in, int D, float scale, T* dst,
+                                          float* part) {
 #pragma unroll 1
-  for (int c = 0; c < NB * 64; c += 32) {
+  for (int c = side * NB * 32; c < (side + 1) * NB * 32; c += 32) {
     if (c >= D) break;
     uint32_t r[32];
     if (have) {
@@ -162,17 +246,72 @@ __device__ __forceinline__ void store_row(uint32_t tacc, bool have, bool in, int
   }
 }
 
-constexpr size_t kTailBytes = sizeof(TileBits) + 512 + 256;  // tile list, documents, barriers
+constexpr size_t kTailBytes = kDocRing * 512 + kRing * sizeof(Record) + 512;  // documents, records, barriers
 
 template <int NB>
 constexpr size_t kDkvSmem = 1024 + (size_t)6 * NB * kBlockBytes + 2048 + kTailBytes;
 template <int NB>
-constexpr size_t kDqSmem = 1024 + (size_t)6 * NB * kBlockBytes + kTailBytes;
+constexpr size_t kDqSmem = 1024 + (size_t)6 * NB * kBlockBytes + 2048 + kTailBytes;
+
+// d = x y^T over the head dimension, both K-major.
+__device__ __forceinline__ void issue_scores(uint32_t d, uint32_t x0, uint32_t y0, int nd, uint32_t idesc, uint64_t* bar) {
+  for (int n = 0; n < nd; ++n) {
+    const uint32_t o = (n >> 2) * kBlockBytes + (n & 3) * 32;
+    umma_bf16(d, umma_desc_k_sw128(x0 + o), umma_desc_k_sw128(y0 + o), idesc, n > 0);
+  }
+  umma_commit(bar);
+}
+// d += x y, x packed over a score region (32 columns of scores hold their 16 packed ones in
+// their first half), y 128 rows MN-major.
+__device__ __forceinline__ void issue_sum(uint32_t d, uint32_t x, uint32_t y0, uint32_t idesc, bool more) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    umma_ts(d, x + (k >> 1) * 32 + (k & 1) * 8, umma_desc_mn(y0 + k * 2048, kBlockBytes), idesc,
+            (more || k > 0) ? 1u : 0u);
+}
+
+// The walk of a dkv CTA over (head of the group, query tile).
+struct HeadWalk {
+  KeyTiles v;
+  TileWalk<KeyTiles> w;
+  int hh, steps;
+  __device__ __forceinline__ HeadWalk(const KeyTiles& tiles, int G, int z, int splits) : v(tiles), w(tiles), hh(0) {
+    steps = INT32_MAX;
+    if (splits > 1) {
+      const int count = w.count();
+      const int64_t total = (int64_t)count * G, first = total * z / splits;
+      steps = (int)(total * (z + 1) / splits - first);
+      if (steps > 0) {
+        hh = (int)(first / count);
+        w.skip((int)(first % count));
+      }
+    }
+  }
+  __device__ __forceinline__ int step(int G, bool& whole) {
+    if (steps <= 0) return -1;
+    int t = w.next(whole);
+    while (t < 0) {
+      if (hh + 1 >= G || v.tiles() == 0) {
+        steps = 0;
+        return -1;
+      }
+      ++hh;
+      w.fetch(0);
+      t = w.next(whole);
+      if (t < 0) {  // no query tile sees these keys, in any head
+        steps = 0;
+        return -1;
+      }
+    }
+    --steps;
+    return t;
+  }
+};
 
 // TMEM: S^T [0,128), dP^T [128,256), dK [256,384), dV [384,512). P^T and dS^T lie over
-// their scores: columns [0,32) hold queries [0,64), columns [64,96) queries [64,128), so
-// that the two warps of a lane quarter never write where the other still reads.
-template <typename T, int NB>
+// their scores, each warp's 32 columns packed into the first 16 of them, so that no warp
+// writes where another still reads.
+template <typename T, int NB, bool SHAPED>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_dkv_kernel(const __grid_constant__ GradMaps maps, const __grid_constant__ GradArgs g) {
   constexpr bool f16 = Elem<T>::kF16;
@@ -184,10 +323,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sV = sK + kBytes;
   uint8_t* sQ = sV + kBytes;       // [2]
   uint8_t* sDo = sQ + 2 * kBytes;  // [2]
-  float* sstat = reinterpret_cast<float*>(sDo + 2 * kBytes);  // [2][lse2 128 | delta 128]
-  TileBits* tiles = reinterpret_cast<TileBits*>(sstat + 512);
-  int32_t* sdoc = reinterpret_cast<int32_t*>(tiles + 1);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(sdoc) + 512);
+  float* sstat = reinterpret_cast<float*>(sDo + 2 * kBytes);  // [2][-lse 128 | -delta 128]
+  int32_t* sdocs = reinterpret_cast<int32_t*>(sstat + 512);  // [kDocRing][128]
+  Record* recs = reinterpret_cast<Record*>(sdocs + kDocRing * kTile);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(recs + kRing);
   uint64_t* kv_full = bars;
   uint64_t* q_full = bars + 1;   // [2]
   uint64_t* q_empty = bars + 3;  // [2]
@@ -196,8 +335,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* acc_done = bars + 7;
   uint64_t* p_full = bars + 8;
   uint64_t* ds_full = bars + 9;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 10);
+  uint64_t* rec_full = bars + 10;   // [kRing]
+  uint64_t* rec_empty = bars + 14;  // [kRing], the computing warps and the MMA warp
+  uint64_t* doc_full = bars + 18;   // [kDocRing]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 18 + kDocRing);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const RecordRing ring{recs, rec_full, rec_empty, abort_flag, a.err};
+  const DocRing docs{sdocs, doc_full, abort_flag, a.err};
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int z = blockIdx.x % a.splits, item = blockIdx.x / a.splits;
@@ -207,7 +351,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int j0 = kt * kTile;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 10; ++i) mbar_init(bars + i, i >= 8 ? kCompute : 1);
+    for (int i = 0; i < kDocRing; ++i) mbar_init(&doc_full[i], 1);
+    for (int i = 0; i < 18; ++i) mbar_init(bars + i, i >= 14 ? 17 : i == 8 || i == 9 ? kCompute : 1);
     *abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&maps.q);
@@ -215,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&maps.v);
     tma_prefetch_desc(&maps.d_o);
   }
-  if (warp == 9) tmem_alloc(tmem_slot, 512);
+  if (warp == 17) tmem_alloc(tmem_slot, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -225,170 +370,134 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_trigger();
 
   const int nk = keys_of(a, b), off = nk - a.Nq, pre = prefix_of(a, b);
-  int32_t klo = 0, khi = 0;
-  if (a.k_range) {
-    klo = a.k_range[((int64_t)b * a.ktiles + kt) * 2];
-    khi = a.k_range[((int64_t)b * a.ktiles + kt) * 2 + 1];
-  }
-  list_tiles(tiles, g.qblocks, warp, lane, [&](int t, bool& see, bool& all) {
-    const int i0 = t * kTile, i1 = min(a.Nq, i0 + kTile) - 1;
-    see = j0 < nk && (!a.causal || j0 <= max(i1 + off, pre - 1));
-    all = j0 + kTile <= nk && (!a.causal || j0 + kTile - 1 <= max(i0 + off, pre - 1));
-    if (see && a.q_range) {
-      const int32_t lo = a.q_range[((int64_t)b * g.qblocks + t) * 2], hi = a.q_range[((int64_t)b * g.qblocks + t) * 2 + 1];
-      see = lo <= khi && klo <= hi;
-      all = all && lo == hi && klo == lo && khi == lo;
-    }
-  });
-  const int count = tiles->count;
-  const int64_t total = (int64_t)count * a.G;
-  const int64_t first = total * z / a.splits;
-  const int steps = (int)(total * (z + 1) / a.splits - first);
-  // the walk over (head of the group, query tile)
-  struct Walk {
-    TileWalk w;
-    int hh, left;
-  };
-  auto begin = [&](Walk& w) {
-    w.hh = (int)(first / count);
-    const int r = (int)(first % count);
-    w.left = count - r;
-    w.w.start(tiles, g.qblocks, r);
-  };
-  auto next = [&](Walk& w) {
-    if (w.left == 0) {
-      ++w.hh;
-      w.left = count;
-      w.w.start(tiles, g.qblocks, 0);
-    }
-    --w.left;
-    return w.w.next();
-  };
-
-  if (warp == 8) {
-    if (lane == 0 && steps > 0) {
-      Walk w;
-      begin(w);
-      mbar_arrive_expect_tx(kv_full, 2 * kBytes);
-      for (int c = 0; c < NB; ++c) {
-        tma_load_4d(sK + c * kBlockBytes, &maps.k, kv_full, c * 64, kv, j0, b);
-        tma_load_4d(sV + c * kBlockBytes, &maps.v, kv_full, c * 64, kv, j0, b);
-      }
-      for (int t = 0; t < steps; ++t) {
-        const int i0 = next(w) * kTile, s = t & 1;
-        const int h = kv * a.G + w.hh;
-        if (t >= 2 && !mbar_wait(&q_empty[s], ((t >> 1) - 1) & 1, abort_flag, a.err)) break;
-        mbar_arrive_expect_tx(&q_full[s], 2 * kBytes + 1024);
-        for (int c = 0; c < NB; ++c) {
-          tma_load_4d(sQ + s * kBytes + c * kBlockBytes, &maps.q, &q_full[s], c * 64, h, i0, b);
-          tma_load_4d(sDo + s * kBytes + c * kBlockBytes, &maps.d_o, &q_full[s], c * 64, h, i0, b);
+  if (warp == 16) {
+    HeadWalk walk(KeyTiles(a, b, kt, g.qblocks, off, nk, pre), a.G, z, a.splits);
+    bool ok = true, whole;
+    int t = 0;
+    for (int tile; ok && (tile = walk.step(a.G, whole)) >= 0; ++t) {
+      if (lane == 0) {
+        const int i0 = tile * kTile, s = t & 1, h = kv * a.G + walk.hh;
+        Record rec = {tile, whole ? kWhole : 0, 0, nk, pre, 0, b, h, i0, z, {0, 0}};
+        rec.flags |= walk.w.one_doc(tile, rec.doc);
+        ok = ring.put(t, rec);
+        if (ok && a.q_pad) docs.load(t, a.q_pad + ((int64_t)b * g.qblocks + tile) * kTile);
+        if (t == 0) {
+          mbar_arrive_expect_tx(kv_full, 2 * kBytes);
+          for (int c = 0; c < NB; ++c) {
+            tma_load_4d(sK + c * kBlockBytes, &maps.k, kv_full, c * 64, kv, j0, b);
+            tma_load_4d(sV + c * kBlockBytes, &maps.v, kv_full, c * 64, kv, j0, b);
+          }
         }
-        const int64_t at = ((int64_t)b * a.H + h) * g.qpad + i0;
-        bulk_load(sstat + s * 256, g.lse2 + at, 512, &q_full[s]);
-        bulk_load(sstat + s * 256 + 128, g.delta + at, 512, &q_full[s]);
-      }
-    }
-  } else if (warp == 9) {
-    if (lane == 0 && steps > 0) {
-      const int nd = (a.D + 15) >> 4;
-      const uint32_t id_s = idesc_f16(128, 128, f16, false, false);
-      const uint32_t id_o = idesc_f16(128, nd * 16, f16, false, true);
-      const uint32_t k0 = smem_u32(sK), v0 = smem_u32(sV);
-      // S^T = K Q^T and dP^T = V dO^T
-      auto scores = [&](uint32_t d, uint32_t x0, uint32_t y0, uint64_t* bar) {
-        for (int n = 0; n < nd; ++n) {
-          const uint32_t o = (n >> 2) * kBlockBytes + (n & 3) * 32;
-          umma_bf16(d, umma_desc_k_sw128(x0 + o), umma_desc_k_sw128(y0 + o), id_s, n > 0);
+        ok = ok && (t < 2 || mbar_wait(&q_empty[s], ((t >> 1) - 1) & 1, abort_flag, a.err));
+        if (ok) {
+          mbar_arrive_expect_tx(&q_full[s], 2 * kBytes + 1024);
+          for (int c = 0; c < NB; ++c) {
+            tma_load_4d(sQ + s * kBytes + c * kBlockBytes, &maps.q, &q_full[s], c * 64, h, i0, b);
+            tma_load_4d(sDo + s * kBytes + c * kBlockBytes, &maps.d_o, &q_full[s], c * 64, h, i0, b);
+          }
+          const int64_t at = ((int64_t)b * a.H + h) * g.qpad + i0;
+          bulk_load(sstat + s * 256, g.nlse + at, 512, &q_full[s]);
+          bulk_load(sstat + s * 256 + 128, g.ndelta + at, 512, &q_full[s]);
         }
-        umma_commit(bar);
-      };
-      // acc += A^T-form operand over the scores x 128 query rows of y
-      auto accumulate = [&](uint32_t d, uint32_t x, uint32_t y0, bool more) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          umma_ts(d, x + (k >> 2) * 64 + (k & 3) * 8, umma_desc_mn(y0 + k * 2048, kBlockBytes), id_o,
-                  (more || k > 0) ? 1u : 0u);
-      };
-      bool ok = mbar_wait(kv_full, 0, abort_flag, a.err) && mbar_wait(&q_full[0], 0, abort_flag, a.err);
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+    }
+    if (lane == 0 && ok) ring.end(t);
+  } else if (warp == 17) {
+    const int nd = (a.D + 15) >> 4;
+    const uint32_t id_s = idesc_f16(128, 128, f16, false, false);
+    const uint32_t id_o = idesc_f16(128, nd * 16, f16, false, true);
+    const uint32_t k0 = smem_u32(sK), v0 = smem_u32(sV), q0 = smem_u32(sQ), d0 = smem_u32(sDo);
+    bool ok = true;
+    int t = 0;
+    bool have = ring.get(0).x >= 0;
+    if (have && lane == 0) {
+      ok = mbar_wait(kv_full, 0, abort_flag, a.err) && mbar_wait(&q_full[0], 0, abort_flag, a.err);
       if (ok) {
         tc_fence_after();
-        scores(tS, k0, smem_u32(sQ), s_full);
-        scores(tDp, v0, smem_u32(sDo), dp_full);
+        issue_scores(tS, k0, q0, nd, id_s, s_full);
+        issue_scores(tDp, v0, d0, nd, id_s, dp_full);
       }
-      for (int t = 0; t < steps && ok; ++t) {
+    }
+    ok = __shfl_sync(0xffffffffu, ok, 0);
+    for (; have && ok; ++t) {
+      const bool more = ring.get(t + 1).x >= 0;
+      if (lane == 0) {
         const int s = t & 1, s1 = s ^ 1;
-        const bool more = t + 1 < steps;
-        if (!(ok = mbar_wait(p_full, t & 1, abort_flag, a.err))) break;
-        tc_fence_after();
-        accumulate(tDv, tS, smem_u32(sDo + s * kBytes), t > 0);
-        if (more) {
-          if (!(ok = mbar_wait(&q_full[s1], ((t + 1) >> 1) & 1, abort_flag, a.err))) break;
+        ok = mbar_wait(p_full, t & 1, abort_flag, a.err);
+        if (ok) {
           tc_fence_after();
-          scores(tS, k0, smem_u32(sQ + s1 * kBytes), s_full);  // over P^T, whose product was issued before
+          issue_sum(tDv, tS, d0 + s * kBytes, id_o, t > 0);
         }
-        if (!(ok = mbar_wait(ds_full, t & 1, abort_flag, a.err))) break;
-        tc_fence_after();
-        accumulate(tDk, tDp, smem_u32(sQ + s * kBytes), t > 0);
-        umma_commit(&q_empty[s]);
-        if (more) scores(tDp, v0, smem_u32(sDo + s1 * kBytes), dp_full);
+        if (ok && more && (ok = mbar_wait(&q_full[s1], ((t + 1) >> 1) & 1, abort_flag, a.err))) {
+          tc_fence_after();
+          issue_scores(tS, k0, q0 + s1 * kBytes, nd, id_s, s_full);  // over P^T, whose product was issued before
+        }
+        ok = ok && mbar_wait(ds_full, t & 1, abort_flag, a.err);
+        if (ok) {
+          tc_fence_after();
+          issue_sum(tDk, tDp, q0 + s * kBytes, id_o, t > 0);
+          umma_commit(&q_empty[s]);
+          if (more)
+            issue_scores(tDp, v0, d0 + s1 * kBytes, nd, id_s, dp_full);
+          else
+            umma_commit(acc_done);
+        }
       }
-      if (ok) umma_commit(acc_done);
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      have = more;
     }
   } else {
-    const int q4 = warp & 3, half = warp >> 2;
+    const int q4 = warp & 3, cq = warp >> 2, c0 = cq * 32;  // lane quarter, column quarter
     const int row = q4 * 32 + lane, j = j0 + row;
     const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
-    const int doc = a.k_doc && j < a.Nk ? a.k_doc[(int64_t)b * a.Nk + j] : 0;
-    Walk w;
-    if (steps > 0) begin(w);
+    const uint32_t tSr = tS + lane_off + c0, tDpr = tDp + lane_off + c0;
+    ScoreTerms st;
+    st.to = kTile;
+    st.doc = a.k_doc && j < a.Nk ? a.k_doc[(int64_t)b * a.Nk + j] : 0;
     bool alive = true;
-    for (int t = 0; t < steps; ++t) {
-      const int tile = next(w), i0 = tile * kTile, s = t & 1;
-      const bool whole = w.w.whole(tile);
-      const float slope = a.slopes ? a.slopes[kv * a.G + w.hh] * kLog2e : 0.f;
-      const float* st = sstat + s * 256 + half * 64;
-      const bool docs = !whole && a.q_doc;
-      if (docs) {
-        asm volatile("bar.sync 1, 256;" ::: "memory");
-        if (half == 0) sdoc[row] = i0 + row < a.Nq ? a.q_doc[(int64_t)b * a.Nq + i0 + row] : 0;
-        asm volatile("bar.sync 1, 256;" ::: "memory");
+    int t = 0;
+    for (;; ++t) {
+      const Record* const rec = ring.at(t);
+      if (!(alive = rec != nullptr) || (rec->flags & kEnd)) break;
+      const int flags = rec->flags;
+      const bool whole = flags & kWhole;
+      const int i0 = rec->i0, s = t & 1;
+      if (SHAPED) st.slope = a.slopes ? a.slopes[rec->head] * kLog2e : 0.f;
+      st.p0 = (float)(i0 + off - j);
+      // queries of this tile from column `from` on see the key (none when it does not exist)
+      st.from = j >= nk || ((flags & kOneDoc) && rec->doc != st.doc) ? kTile : a.causal && j >= pre ? j - off - i0 : 0;
+      const float* stat = sstat + s * 256 + c0;
+      st.sdoc = nullptr;
+      if (!whole && a.q_pad && !(flags & kOneDoc)) {
+        st.sdoc = docs.get(t, alive);
+        if (!alive) break;
       }
       if (!(alive = mbar_wait_all(&q_full[s], (t >> 1) & 1, abort_flag, a.err) &&
                     mbar_wait_all(s_full, t & 1, abort_flag, a.err)))
         break;
       tc_fence_after();
-      // queries of this tile from column `from` on see the key (none when it does not exist)
-      const int from = j >= nk ? kTile : a.causal && j >= pre ? j - off - i0 : 0;
-      const float p0 = (float)(i0 + off - j);
-      float pf[64];
+      float pf[32];
 #pragma unroll
-      for (int c0 = 0; c0 < 64; c0 += 32) {
-        uint32_t r[32], pk[16];
-        tmem_ld_32x32b_x32(tS + lane_off + half * 64 + c0, r);
-        tmem_ld_wait_regs(r);
+      for (int e = 0; e < 32; e += 16) {
+        uint32_t q[16], pk[8];
+        float nl[16], p[16];
+        tmem_ld_x16(tSr + e, q);
 #pragma unroll
-        for (int u = 0; u < 32; u += 4) {
-          const float4 ls = *reinterpret_cast<const float4*>(st + c0 + u);
-          const float lv[4] = {ls.x, ls.y, ls.z, ls.w};
-          int4 qd = make_int4(0, 0, 0, 0);
-          if (docs) qd = *reinterpret_cast<const int4*>(sdoc + half * 64 + c0 + u);
-          const int dv[4] = {qd.x, qd.y, qd.z, qd.w};
-          float p[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int c = half * 64 + c0 + u + e;
-            float fac;
-            float x = score(a, __uint_as_float(r[u + e]), fac);
-            if (a.slopes) x = fmaf(-slope, fabsf(p0 + (float)c), x);
-            p[e] = fast_ex2(x - lv[e]);
-            if (!whole && (c < from || (docs && dv[e] != doc))) p[e] = 0.f;
-            pf[c0 + u + e] = p[e] * fac;
-          }
-          pk[u / 2] = Elem<T>::pack(p[0], p[1]);
-          pk[u / 2 + 1] = Elem<T>::pack(p[2], p[3]);
+        for (int u = 0; u < 16; u += 4) {
+          const float4 v = *reinterpret_cast<const float4*>(stat + e + u);
+          nl[u] = v.x;
+          nl[u + 1] = v.y;
+          nl[u + 2] = v.z;
+          nl[u + 3] = v.w;
         }
-        // queries [64 half + c0, +32) as 16 packed columns; c0 = 32 goes over scores already read
-        tmem_st_x16(tS + lane_off + half * 64 + c0 / 2, pk);
+        tmem_ld_wait_16(q);
+        if (whole)
+          probabilities<SHAPED, false>(a, st, q, c0 + e, nl, p, pf + e);
+        else
+          probabilities<SHAPED, true>(a, st, q, c0 + e, nl, p, pf + e);
+        pack16<T>(p, pk);
+        tmem_st_x8(tSr + e / 2, pk);  // over scores already read
       }
       tmem_store_wait();
       tc_fence_before();
@@ -396,51 +505,125 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!(alive = mbar_wait_all(dp_full, t & 1, abort_flag, a.err))) break;
       tc_fence_after();
 #pragma unroll
-      for (int c0 = 0; c0 < 64; c0 += 32) {
-        uint32_t r[32], pk[16];
-        tmem_ld_32x32b_x32(tDp + lane_off + half * 64 + c0, r);
-        tmem_ld_wait_regs(r);
+      for (int e = 0; e < 32; e += 16) {
+        uint32_t q[16], pk[8];
+        float nd[16], ds[16];
+        tmem_ld_x16(tDpr + e, q);
 #pragma unroll
-        for (int u = 0; u < 32; u += 4) {
-          const float4 de = *reinterpret_cast<const float4*>(st + 128 + c0 + u);
-          const float dl[4] = {de.x, de.y, de.z, de.w};
-          float ds[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float p = pf[c0 + u + e];
-            ds[e] = p * (__uint_as_float(r[u + e]) - dl[e]);
-            if (!whole && p == 0.f) ds[e] = 0.f;  // dP of keys that do not exist may be anything
-          }
-          pk[u / 2] = Elem<T>::pack(ds[0], ds[1]);
-          pk[u / 2 + 1] = Elem<T>::pack(ds[2], ds[3]);
+        for (int u = 0; u < 16; u += 4) {
+          const float4 v = *reinterpret_cast<const float4*>(stat + 128 + e + u);
+          nd[u] = v.x;
+          nd[u + 1] = v.y;
+          nd[u + 2] = v.z;
+          nd[u + 3] = v.w;
         }
-        tmem_st_x16(tDp + lane_off + half * 64 + c0 / 2, pk);
+        tmem_ld_wait_16(q);
+        if (whole)
+          score_grads<false>(q, nd, pf + e, ds);
+        else
+          score_grads<true>(q, nd, pf + e, ds);
+        pack16<T>(ds, pk);
+        tmem_st_x8(tDpr + e / 2, pk);
       }
       tmem_store_wait();
       tc_fence_before();
       mbar_arrive(ds_full);
+      ring.done(t);
     }
-    if (alive && steps > 0) alive = mbar_wait_all(acc_done, 0, abort_flag, a.err);
+    if (alive && t > 0) alive = mbar_wait_all(acc_done, 0, abort_flag, a.err);
     tc_fence_after();
     if (alive) {
-      // half 0 writes dK, half 1 dV
-      const int64_t* st = half ? g.s1 : g.s0;
-      T* dst = static_cast<T*>(half ? g.out1 : g.out0) + b * st[0] + j * st[1] + kv * st[2];
+      // two warps of a lane quarter write dK, two dV, half of the columns each
+      const int which = cq >> 1;
+      const int64_t* os = which ? g.s1 : g.s0;
+      T* dst = static_cast<T*>(which ? g.out1 : g.out0) + b * os[0] + j * os[1] + kv * os[2];
       float* part = nullptr;
       if (a.splits > 1)
-        part = g.part + ((((int64_t)z * 2 + half) * heads + b * a.KV + kv) * a.ktiles * kTile + j) * a.D;
-      store_row<T, NB>((half ? tDv : tDk) + lane_off, steps > 0, j < a.Nk, a.D, half ? g.v_scale : g.out_scale, dst,
-                       part);
+        part = g.part + ((((int64_t)z * 2 + which) * heads + b * a.KV + kv) * a.ktiles * kTile + j) * a.D;
+      store_row<T, NB>((which ? tDv : tDk) + lane_off, cq & 1, t > 0, j < a.Nk, a.D, which ? g.v_scale : g.out_scale,
+                       dst, part);
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 9) tmem_dealloc(tmem, 512);
+  if (warp == 17) tmem_dealloc(tmem, 512);
 }
 
-// TMEM: S [0,128), dP [128,256) with dS over it, dQ [256,384).
+// A unit of dq work: split z of 128 queries of one head, the last query tiles first.
+struct DqUnit {
+  int z, b, h, i0, i1, qt;
+  __device__ __forceinline__ DqUnit(const GradArgs& g, int u) {
+    const AttnArgs& a = g.f;
+    z = u % a.splits;
+    const int item = u / a.splits, heads = a.B * a.H, at = item % heads;
+    qt = g.qblocks - 1 - item / heads;
+    b = at / a.H;
+    h = at % a.H;
+    i0 = qt * kTile;
+    i1 = min(a.Nq, i0 + kTile) - 1;
+  }
+};
+struct DqWalk : TileWalk<RowTiles> {
+  int steps;
+  __device__ __forceinline__ DqWalk(const GradArgs& g, const DqUnit& u, int off, int nk, int pre)
+      : TileWalk<RowTiles>(RowTiles(g.f, u.b, u.i0, u.i1, off, nk, pre,
+                                    g.f.q_range + ((int64_t)u.b * g.qblocks + u.qt) * 2)) {
+    steps = INT32_MAX;
+    if (g.f.splits > 1) {
+      const int n = count(), first = (int)((int64_t)n * u.z / g.f.splits);
+      steps = (int)((int64_t)n * (u.z + 1) / g.f.splits) - first;
+      if (steps > 0) skip(first);
+    }
+  }
+  __device__ __forceinline__ int step(bool& whole) { return steps-- > 0 ? next(whole) : -1; }
+};
+
+// The end of a dq unit, one query row per thread: dQ = scale (dS K - e P K) and the
+// corrected delta, or the parts of a split. Out of line: its registers would compete
+// with the loop's.
 template <typename T, int NB>
+__device__ __noinline__ void store_dq(const GradArgs& g, int b, int h, int i, int z, int side, uint32_t tDq, uint32_t tPk,
+                                      bool some, float e) {
+  const AttnArgs& a = g.f;
+  const bool valid = i < a.Nq;
+  T* dst = static_cast<T*>(g.out0) + b * g.s0[0] + i * g.s0[1] + h * g.s0[2];
+  const int64_t at = ((int64_t)b * a.H + h) * g.qpad + i;
+  if (a.splits > 1) {
+    const int64_t rows = (int64_t)a.B * a.H * g.qpad, at_row = z * rows + at;
+    store_row<T, NB>(tDq, side, some, valid, a.D, 1.f, dst, g.part + at_row * a.D);
+    store_row<T, NB>(tPk, side, some, valid, a.D, 1.f, dst, g.part + (a.splits * rows + at_row) * a.D);
+    if (valid && side == 0) g.part_e[at_row] = e;
+    return;
+  }
+  if (valid && side == 0) g.ndelta[at] -= e;
+#pragma unroll 1
+  for (int c = side * NB * 32; c < (side + 1) * NB * 32; c += 16) {
+    if (c >= a.D) break;
+    uint32_t r[16], q[16];
+    if (some) {
+      tmem_ld_x16(tDq + c, r);
+      tmem_ld_x16(tPk + c, q);
+      tmem_ld_wait_16(r);
+      tmem_ld_wait_16(q);
+    }
+    if (!valid) continue;
+    float f[16];
+#pragma unroll
+    for (int y = 0; y < 16; ++y)
+      f[y] = some ? g.out_scale * fmaf(-e, __uint_as_float(q[y]), __uint_as_float(r[y])) : 0.f;
+#pragma unroll
+    for (int y = 0; y < 2; ++y)
+      if (c + 8 * y < a.D)
+        *reinterpret_cast<uint4*>(dst + c + 8 * y) =
+            make_uint4(Elem<T>::pack(f[8 * y], f[8 * y + 1]), Elem<T>::pack(f[8 * y + 2], f[8 * y + 3]),
+                       Elem<T>::pack(f[8 * y + 4], f[8 * y + 5]), Elem<T>::pack(f[8 * y + 6], f[8 * y + 7]));
+  }
+}
+
+// TMEM: S [0,128) with P over it, dP [128,256) with dS over it, dS K [256,384), P K [384,512).
+// CTAs take over units as in the forward kernel; t counts steps and n units with steps.
+template <typename T, int NB, bool SHAPED>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_dq_kernel(const __grid_constant__ GradMaps maps, const __grid_constant__ GradArgs g) {
   constexpr bool f16 = Elem<T>::kF16;
@@ -452,29 +635,33 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sDo = sQ + kBytes;
   uint8_t* sK = sDo + kBytes;     // [2]
   uint8_t* sV = sK + 2 * kBytes;  // [2]
-  TileBits* tiles = reinterpret_cast<TileBits*>(sV + 2 * kBytes);
-  int32_t* sdoc = reinterpret_cast<int32_t*>(tiles + 1);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(sdoc) + 512);
+  float* srow = reinterpret_cast<float*>(sV + 2 * kBytes);  // [4][128] the column quarters' row sums
+  int32_t* sdocs = reinterpret_cast<int32_t*>(srow + 4 * kTile);  // [kDocRing][128]
+  Record* recs = reinterpret_cast<Record*>(sdocs + kDocRing * kTile);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(recs + kRing);
   uint64_t* q_full = bars;
-  uint64_t* kv_full = bars + 1;   // [2]
-  uint64_t* kv_empty = bars + 3;  // [2]
-  uint64_t* s_full = bars + 5;
-  uint64_t* dp_full = bars + 6;
-  uint64_t* acc_done = bars + 7;
-  uint64_t* s_free = bars + 8;
-  uint64_t* ds_full = bars + 9;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 10);
+  uint64_t* q_empty = bars + 1;
+  uint64_t* kv_full = bars + 2;   // [2]
+  uint64_t* kv_empty = bars + 4;  // [2]
+  uint64_t* s_full = bars + 6;
+  uint64_t* dp_full = bars + 7;
+  uint64_t* acc_done = bars + 8;
+  uint64_t* p_full = bars + 9;
+  uint64_t* ds_full = bars + 10;
+  uint64_t* rec_full = bars + 11;   // [kRing]
+  uint64_t* rec_empty = bars + 15;  // [kRing], the computing warps and the MMA warp
+  uint64_t* next_bar = bars + 19;
+  uint8_t* next_unit = reinterpret_cast<uint8_t*>(bars + 20);  // 16 bytes
+  uint64_t* doc_full = bars + 22;  // [kDocRing]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 22 + kDocRing);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const RecordRing ring{recs, rec_full, rec_empty, abort_flag, a.err};
+  const DocRing docs{sdocs, doc_full, abort_flag, a.err};
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int z = blockIdx.x % a.splits, item = blockIdx.x / a.splits;
-  const int heads = a.B * a.H;
-  const int qt = g.qblocks - 1 - item / heads;
-  const int b = item % heads / a.H, h = item % heads % a.H, kv = h / a.G;
-  const int i0 = qt * kTile, i1 = min(a.Nq, i0 + kTile) - 1;
-
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 10; ++i) mbar_init(bars + i, i >= 8 ? kCompute : 1);
+    for (int i = 0; i < kDocRing; ++i) mbar_init(&doc_full[i], 1);
+    for (int i = 0; i < 20; ++i) mbar_init(bars + i, i == 9 || i == 10 ? kCompute : i >= 15 && i < 19 ? 17 : 1);
     *abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&maps.q);
@@ -482,201 +669,272 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&maps.v);
     tma_prefetch_desc(&maps.d_o);
   }
-  if (warp == 9) tmem_alloc(tmem_slot, 512);
+  if (warp == 17) tmem_alloc(tmem_slot, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const uint32_t tS = tmem, tDp = tmem + 128, tDq = tmem + 256;
+  const uint32_t tS = tmem, tDp = tmem + 128, tDq = tmem + 256, tPk = tmem + 384;
   pdl_wait();
   pdl_trigger();
 
-  const int nk = keys_of(a, b), off = nk - a.Nq, pre = prefix_of(a, b);
-  const int lim_any = a.causal ? min(nk, max(i1 + off + 1, pre)) : nk;
-  const int lim_all = a.causal ? min(nk, max(i0 + off + 1, pre)) : nk;
-  int32_t qlo = 0, qhi = 0;
-  if (a.q_range) {
-    qlo = a.q_range[((int64_t)b * g.qblocks + qt) * 2];
-    qhi = a.q_range[((int64_t)b * g.qblocks + qt) * 2 + 1];
-  }
-  list_tiles(tiles, a.ktiles, warp, lane, [&](int t, bool& see, bool& all) {
-    see = t * kTile < lim_any;
-    all = (t + 1) * kTile <= lim_all;
-    if (see && a.k_range) {
-      const int32_t lo = a.k_range[((int64_t)b * a.ktiles + t) * 2], hi = a.k_range[((int64_t)b * a.ktiles + t) * 2 + 1];
-      see = lo <= qhi && qlo <= hi;
-      all = all && lo == hi && qlo == lo && qhi == lo;
-    }
-  });
-  const int first = (int)((int64_t)tiles->count * z / a.splits);
-  const int steps = (int)((int64_t)tiles->count * (z + 1) / a.splits) - first;
-
-  if (warp == 8) {
-    if (lane == 0 && steps > 0) {
-      TileWalk w;
-      w.start(tiles, a.ktiles, first);
-      mbar_arrive_expect_tx(q_full, 2 * kBytes);
-      for (int c = 0; c < NB; ++c) {
-        tma_load_4d(sQ + c * kBlockBytes, &maps.q, q_full, c * 64, h, i0, b);
-        tma_load_4d(sDo + c * kBlockBytes, &maps.d_o, q_full, c * 64, h, i0, b);
-      }
-      for (int t = 0; t < steps; ++t) {
-        const int j = w.next() * kTile, s = t & 1;
-        if (t >= 2 && !mbar_wait(&kv_empty[s], ((t >> 1) - 1) & 1, abort_flag, a.err)) break;
-        mbar_arrive_expect_tx(&kv_full[s], 2 * kBytes);
-        for (int c = 0; c < NB; ++c) {
-          tma_load_4d(sK + s * kBytes + c * kBlockBytes, &maps.k, &kv_full[s], c * 64, kv, j, b);
-          tma_load_4d(sV + s * kBytes + c * kBlockBytes, &maps.v, &kv_full[s], c * 64, kv, j, b);
+  if (warp == 16) {
+    int t = 0, n = 0, r = 0, asked = 0;
+    bool ok = true;
+    for (int x = blockIdx.x; x >= 0 && ok;) {
+      const DqUnit u(g, x);
+      const int nk = keys_of(a, u.b), pre = prefix_of(a, u.b), kv = u.h / a.G;
+      DqWalk walk(g, u, nk - a.Nq, nk, pre);
+      bool whole, whole_next;
+      int j = walk.step(whole), after;
+      int first = kFirst;
+      do {
+        after = j >= 0 ? walk.step(whole_next) : -1;
+        if (lane == 0) {
+          Record rec = {j, first | (after < 0 ? kLast : 0) | (j >= 0 && whole ? kWhole : 0), x, nk, pre, 0, u.b, u.h, u.i0,
+                        u.z, {0, 0}};
+          if (j >= 0) rec.flags |= walk.one_doc(j, rec.doc);
+          ok = ring.put(r, rec);
+          if (after < 0) {
+            // at the unit's end: a unit asked for early would wait behind a long one
+            mbar_arrive_expect_tx(next_bar, 16);
+            ask_unit(next_unit, next_bar);
+          }
+          if (ok && a.k_pad && j < 0) docs.skip(r);
+          if (j >= 0) {
+            if (ok && a.k_pad) docs.load(r, a.k_pad + ((int64_t)u.b * a.ktiles + j) * kTile);
+            if (first && (ok = ok && (n == 0 || mbar_wait(q_empty, (n - 1) & 1, abort_flag, a.err)))) {
+              mbar_arrive_expect_tx(q_full, 2 * kBytes);
+              for (int c = 0; c < NB; ++c) {
+                tma_load_4d(sQ + c * kBlockBytes, &maps.q, q_full, c * 64, u.h, u.i0, u.b);
+                tma_load_4d(sDo + c * kBlockBytes, &maps.d_o, q_full, c * 64, u.h, u.i0, u.b);
+              }
+            }
+            const int s = t & 1;
+            ok = ok && (t < 2 || mbar_wait(&kv_empty[s], ((t >> 1) - 1) & 1, abort_flag, a.err));
+            if (ok) {
+              mbar_arrive_expect_tx(&kv_full[s], 2 * kBytes);
+              for (int c = 0; c < NB; ++c) {
+                tma_load_4d(sK + s * kBytes + c * kBlockBytes, &maps.k, &kv_full[s], c * 64, kv, j * kTile, u.b);
+                tma_load_4d(sV + s * kBytes + c * kBlockBytes, &maps.v, &kv_full[s], c * 64, kv, j * kTile, u.b);
+              }
+            }
+          }
         }
-      }
-    }
-  } else if (warp == 9) {
-    if (lane == 0 && steps > 0) {
-      const int nd = (a.D + 15) >> 4;
-      const uint32_t id_s = idesc_f16(128, 128, f16, false, false);
-      const uint32_t id_o = idesc_f16(128, nd * 16, f16, false, true);
-      const uint32_t q0 = smem_u32(sQ), d0 = smem_u32(sDo);
-      auto scores = [&](uint32_t d, uint32_t x0, uint32_t y0, uint64_t* bar) {
-        for (int n = 0; n < nd; ++n) {
-          const uint32_t o = (n >> 2) * kBlockBytes + (n & 3) * 32;
-          umma_bf16(d, umma_desc_k_sw128(x0 + o), umma_desc_k_sw128(y0 + o), id_s, n > 0);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        ++r;
+        if (j >= 0) {
+          ++t;
+          n += first ? 1 : 0;
         }
-        umma_commit(bar);
-      };
-      bool ok = mbar_wait(q_full, 0, abort_flag, a.err) && mbar_wait(&kv_full[0], 0, abort_flag, a.err);
-      if (ok) {
-        tc_fence_after();
-        scores(tS, q0, smem_u32(sK), s_full);
-        scores(tDp, d0, smem_u32(sV), dp_full);
+        first = 0;
+        j = after;
+        whole = whole_next;
+      } while (j >= 0 && ok);
+      if (lane == 0) {
+        ok = mbar_wait(next_bar, asked & 1, abort_flag, a.err) && ok;
+        x = ok ? asked_unit(next_unit) : -1;
+        fence_async_smem();  // read before the next answer is written
       }
-      for (int t = 0; t < steps && ok; ++t) {
-        const int s = t & 1, s1 = s ^ 1;
-        const bool more = t + 1 < steps;
-        if (more) {
-          if (!(ok = mbar_wait(s_free, t & 1, abort_flag, a.err) &&
-                     mbar_wait(&kv_full[s1], ((t + 1) >> 1) & 1, abort_flag, a.err)))
-            break;
+      ++asked;
+      x = __shfl_sync(0xffffffffu, x, 0);
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+    }
+    if (lane == 0 && ok) ring.end(r);
+  } else if (warp == 17) {
+    const int nd = (a.D + 15) >> 4;
+    const uint32_t id_s = idesc_f16(128, 128, f16, false, false);
+    const uint32_t id_o = idesc_f16(128, nd * 16, f16, false, true);
+    const uint32_t q0 = smem_u32(sQ), d0 = smem_u32(sDo), k0 = smem_u32(sK), v0 = smem_u32(sV);
+    // steps follow one another across units: while one is summed, the scores of the next
+    // are issued, whichever unit it belongs to. Only one record is looked ahead: one
+    // without a tile is not waited past, since the ring moves on only with this step.
+    int n = -1, t = 0;
+    bool ok = true, issued = false;
+    auto s_of = [&](int tt, int nn, bool fst) {
+      if (fst && !mbar_wait(q_full, nn & 1, abort_flag, a.err)) return false;
+      if (!mbar_wait(&kv_full[tt & 1], (tt >> 1) & 1, abort_flag, a.err)) return false;
+      tc_fence_after();
+      issue_scores(tS, q0, k0 + (tt & 1) * kBytes, nd, id_s, s_full);
+      return true;
+    };
+    auto dp_of = [&](int tt, int flags) {
+      issue_scores(tDp, d0, v0 + (tt & 1) * kBytes, nd, id_s, dp_full);
+      if (flags & kLast) umma_commit(q_empty);
+    };
+    int2 cur = ring.get(0);  // tile, flags
+    for (int r = 1; !(cur.y & kEnd) && ok; ++r) {
+      const int2 nx = ring.get(r);
+      if (cur.x < 0) {
+        cur = nx;
+        continue;
+      }
+      const bool more = nx.x >= 0;
+      if (!issued) {
+        if (cur.y & kFirst) ++n;
+        if (lane == 0 && (ok = s_of(t, n, cur.y & kFirst))) dp_of(t, cur.y);
+      }
+      if (more && (nx.y & kFirst)) ++n;
+      if (lane == 0 && ok) {
+        const int s = t & 1;
+        const bool sum = !(cur.y & kFirst);
+        ok = mbar_wait(p_full, t & 1, abort_flag, a.err);
+        if (ok) {
           tc_fence_after();
-          scores(tS, q0, smem_u32(sK + s1 * kBytes), s_full);
+          issue_sum(tPk, tS, k0 + s * kBytes, id_o, sum);
         }
-        if (!(ok = mbar_wait(ds_full, t & 1, abort_flag, a.err))) break;
-        tc_fence_after();
-        const uint32_t k0 = smem_u32(sK + s * kBytes);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          umma_ts(tDq, tDp + (k >> 2) * 64 + (k & 3) * 8, umma_desc_mn(k0 + k * 2048, kBlockBytes), id_o,
-                  (t > 0 || k > 0) ? 1u : 0u);
-        umma_commit(&kv_empty[s]);
-        if (more) scores(tDp, d0, smem_u32(sV + s1 * kBytes), dp_full);
+        if (ok && more) ok = s_of(t + 1, n, nx.y & kFirst);
+        ok = ok && mbar_wait(ds_full, t & 1, abort_flag, a.err);
+        if (ok) {
+          tc_fence_after();
+          issue_sum(tDq, tDp, k0 + s * kBytes, id_o, sum);
+          umma_commit(&kv_empty[s]);
+          if (cur.y & kLast) umma_commit(acc_done);
+          if (more) dp_of(t + 1, nx.y);
+        }
       }
-      if (ok) umma_commit(acc_done);
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      issued = more;
+      ++t;
+      cur = nx;
     }
   } else {
-    const int q4 = warp & 3, half = warp >> 2;
-    const int row = q4 * 32 + lane, i = i0 + row;
+    const int q4 = warp & 3, cq = warp >> 2, c0 = cq * 32;  // lane quarter, column quarter
+    const int row = q4 * 32 + lane;
     const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
-    const bool valid = i < a.Nq;
-    const int64_t at = ((int64_t)b * a.H + h) * g.qpad + i;
-    const float lse2 = g.lse2[at], delta = g.delta[at];
-    const int pos = i + off;
-    const int lim = a.causal ? min(nk, max(pos + 1, pre)) : nk;
-    const int doc = a.q_doc && valid ? a.q_doc[(int64_t)b * a.Nq + i] : 0;
-    const float slope = a.slopes ? a.slopes[h] * kLog2e : 0.f;
-    TileWalk w;
-    if (steps > 0) w.start(tiles, a.ktiles, first);
+    const uint32_t tSr = tS + lane_off + c0, tDpr = tDp + lane_off + c0;
+    int t = 0, n = 0;
     bool alive = true;
-    for (int t = 0; t < steps; ++t) {
-      const int tile = w.next(), j0 = tile * kTile, s = t & 1;
-      const bool whole = w.whole(tile);
-      const bool docs = !whole && a.k_doc;
-      if (docs) {
-        asm volatile("bar.sync 1, 256;" ::: "memory");
-        if (half == 0) sdoc[row] = j0 + row < a.Nk ? a.k_doc[(int64_t)b * a.Nk + j0 + row] : 0;
-        asm volatile("bar.sync 1, 256;" ::: "memory");
+    ScoreTerms st;
+    st.from = 0;
+    int nk = 0, lim = 0, pos = 0;
+    float nlse = 0.f, ndelta = 0.f;
+    float e0 = 0.f, e1 = 0.f;  // the row's sum of P (dP - delta) over this half's columns
+    for (int r = 0;; ++r) {
+      const Record* const rec = ring.at(r);
+      if (!rec || (rec->flags & kEnd)) break;
+      const int flags = rec->flags, tile = rec->tile;
+      const bool whole = flags & kWhole;
+      if (flags & kFirst) {
+        const int i = rec->i0 + row;
+        const int64_t at = ((int64_t)rec->b * a.H + rec->head) * g.qpad + i;
+        nk = rec->nk;
+        pos = i + nk - a.Nq;
+        lim = a.causal ? min(nk, max(pos + 1, rec->pre)) : nk;
+        nlse = g.nlse[at];
+        ndelta = g.ndelta[at];
+        st.doc = a.q_doc && i < a.Nq ? a.q_doc[(int64_t)rec->b * a.Nq + i] : 0;
+        if (SHAPED) st.slope = a.slopes ? a.slopes[rec->head] * kLog2e : 0.f;
+        e0 = e1 = 0.f;
       }
-      if (!(alive = mbar_wait_all(s_full, t & 1, abort_flag, a.err))) break;
-      tc_fence_after();
-      const int lc = lim - j0;
-      const float p0 = (float)(pos - j0);
-      float pf[64];
-#pragma unroll
-      for (int c0 = 0; c0 < 64; c0 += 32) {
-        uint32_t r[32];
-        tmem_ld_32x32b_x32(tS + lane_off + half * 64 + c0, r);
-        tmem_ld_wait_regs(r);
-#pragma unroll
-        for (int u = 0; u < 32; u += 4) {
-          int4 kd = make_int4(0, 0, 0, 0);
-          if (docs) kd = *reinterpret_cast<const int4*>(sdoc + half * 64 + c0 + u);
-          const int dv[4] = {kd.x, kd.y, kd.z, kd.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int c = half * 64 + c0 + u + e;
-            float fac;
-            float x = score(a, __uint_as_float(r[u + e]), fac);
-            if (a.slopes) x = fmaf(-slope, fabsf(p0 - (float)c), x);
-            float p = fast_ex2(x - lse2) * fac;
-            if (!whole && (c >= lc || (docs && dv[e] != doc))) p = 0.f;
-            pf[c0 + u + e] = p;
-          }
+      const bool some = tile >= 0;
+      if (some) {
+        const int j0 = tile * kTile;
+        st.sdoc = nullptr;
+        if (!whole && a.k_pad && !(flags & kOneDoc)) {
+          st.sdoc = docs.get(r, alive);
+          if (!alive) break;
         }
-      }
-      tc_fence_before();
-      mbar_arrive(s_free);
-      if (!whole && j0 + kTile > nk && nk < a.Nk) {
-        // keys behind the last one count as zeros in dS K, whatever they hold (S of this tile is done)
-        if (half == 0 && j0 + row >= nk) {
+        if (!(alive = mbar_wait_all(s_full, t & 1, abort_flag, a.err))) break;
+        tc_fence_after();
+        st.to = (flags & kOneDoc) && rec->doc != st.doc ? 0 : lim - j0;
+        st.p0 = (float)(j0 - pos);
+        // P, and the cap's slope as FP16 pairs (in [0, 1]: off by 2^-12, below dS's own rounding)
+        float p[32];
+        [[maybe_unused]] uint32_t fac[SHAPED ? 16 : 1];
 #pragma unroll
-          for (int c = 0; c < NB; ++c) {
-            uint4* p = reinterpret_cast<uint4*>(sK + s * kBytes + c * kBlockBytes + row * 128);
+        for (int e = 0; e < 32; e += 16) {
+          uint32_t q[16], pk[8];
+          float nl[16], pf[16];
+          tmem_ld_x16(tSr + e, q);
 #pragma unroll
-            for (int u = 0; u < 8; ++u) p[u] = make_uint4(0u, 0u, 0u, 0u);
-          }
+          for (int y = 0; y < 16; ++y) nl[y] = nlse;
+          tmem_ld_wait_16(q);
+          if (whole)
+            probabilities<SHAPED, false>(a, st, q, c0 + e, nl, p + e, pf, SHAPED ? fac + e / 2 : nullptr);
+          else
+            probabilities<SHAPED, true>(a, st, q, c0 + e, nl, p + e, pf, SHAPED ? fac + e / 2 : nullptr);
+          pack16<T>(pf, pk);
+          tmem_st_x8(tSr + e / 2, pk);  // over scores already read
         }
-        fence_async_smem();
-      }
-      if (!(alive = mbar_wait_all(dp_full, t & 1, abort_flag, a.err))) break;
-      tc_fence_after();
+        if (!whole && j0 + kTile > nk && nk < a.Nk) {
+          // keys behind the last one count as zeros in the sums, whatever they hold (S of this tile is done)
+          if (cq == 0 && j0 + row >= nk) {
 #pragma unroll
-      for (int c0 = 0; c0 < 64; c0 += 32) {
-        uint32_t r[32], pk[16];
-        tmem_ld_32x32b_x32(tDp + lane_off + half * 64 + c0, r);
-        tmem_ld_wait_regs(r);
+            for (int c = 0; c < NB; ++c) {
+              uint4* k = reinterpret_cast<uint4*>(sK + (t & 1) * kBytes + c * kBlockBytes + row * 128);
 #pragma unroll
-        for (int u = 0; u < 32; u += 2) {
-          float ds[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float p = pf[c0 + u + e];
-            ds[e] = p * (__uint_as_float(r[u + e]) - delta);
-            if (!whole && p == 0.f) ds[e] = 0.f;  // dP of keys that do not exist may be anything
+              for (int y = 0; y < 8; ++y) k[y] = make_uint4(0u, 0u, 0u, 0u);
+            }
           }
-          pk[u / 2] = Elem<T>::pack(ds[0], ds[1]);
+          fence_async_smem();
         }
-        tmem_st_x16(tDp + lane_off + half * 64 + c0 / 2, pk);
+        tmem_store_wait();
+        tc_fence_before();
+        mbar_arrive(p_full);
+        if (!(alive = mbar_wait_all(dp_full, t & 1, abort_flag, a.err))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int e = 0; e < 32; e += 16) {
+          uint32_t q[16], pk[8];
+          float nd[16], ds[16];
+          tmem_ld_x16(tDpr + e, q);
+#pragma unroll
+          for (int y = 0; y < 16; ++y) nd[y] = ndelta;
+          tmem_ld_wait_16(q);
+          if (whole)
+            score_grads<false>(q, nd, p + e, ds);
+          else
+            score_grads<true>(q, nd, p + e, ds);
+#pragma unroll
+          for (int y = 0; y < 16; y += 2) add2(e0, e1, ds[y], ds[y + 1], e0, e1);
+          if constexpr (SHAPED) {
+#pragma unroll
+            for (int y = 0; y < 16; y += 2)
+              mul2(ds[y], ds[y + 1], Elem<__half>::lo(fac[(e + y) / 2]), Elem<__half>::hi(fac[(e + y) / 2]), ds[y],
+                   ds[y + 1]);
+          }
+          pack16<T>(ds, pk);
+          tmem_st_x8(tDpr + e / 2, pk);
+        }
+        tmem_store_wait();
+        tc_fence_before();
+        mbar_arrive(ds_full);
+        ++t;
       }
-      tmem_store_wait();
-      tc_fence_before();
-      mbar_arrive(ds_full);
-    }
-    if (alive && steps > 0) alive = mbar_wait_all(acc_done, 0, abort_flag, a.err);
-    tc_fence_after();
-    if (alive && half == 0) {
-      T* dst = static_cast<T*>(g.out0) + b * g.s0[0] + i * g.s0[1] + h * g.s0[2];
-      float* part = nullptr;
-      if (a.splits > 1) part = g.part + (((int64_t)z * heads + b * a.H + h) * g.qpad + i) * a.D;
-      store_row<T, NB>(tDq + lane_off, steps > 0, valid, a.D, g.out_scale, dst, part);
+      if (flags & kLast) {
+        // the row sums of the four column quarters meet
+        asm volatile("bar.sync 1, 512;" ::: "memory");
+        srow[cq * kTile + row] = e0 + e1;
+        asm volatile("bar.sync 1, 512;" ::: "memory");
+        if (some && !(alive = mbar_wait_all(acc_done, n & 1, abort_flag, a.err))) break;
+        n += some;
+        tc_fence_after();
+        // the accumulators are free for the next unit once they have been read: these threads
+        // arrive at p_full only after that
+        if (cq < 2) {
+          const float e = (srow[row] + srow[kTile + row]) + (srow[2 * kTile + row] + srow[3 * kTile + row]);
+          store_dq<T, NB>(g, rec->b, rec->head, rec->i0 + row, rec->z, cq, tDq + lane_off, tPk + lane_off, some,
+                          e * g.v_scale);
+        }
+        tc_fence_before();
+      }
+      ring.done(r);
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 9) tmem_dealloc(tmem, 512);
+  if (warp == 17) tmem_dealloc(tmem, 512);
 }
 
-// out = scale * sum of the parts, in order; eight head dimensions per thread.
+// out = scale * sum of the parts, in order; eight head dimensions per thread. For dQ
+// (part_e given) the parts are dS K, and behind them P K, which the summed row error e
+// multiplies; delta is corrected by e.
 struct JoinArgs {
-  const float* part;   // [splits][sets][B][heads][rows_pad][D]
+  const float* part;   // [splits][sets][B][heads][rows_pad][D], or dQ: [2][splits][B][heads][rows_pad][D]
+  const float* part_e; // [splits][B][heads][rows_pad] or null
+  float* ndelta;       // [B][heads][rows_pad]
   void* out[2];
   int64_t s[2][3];
   float scale[2];
@@ -696,20 +954,32 @@ __global__ void __launch_bounds__(256) attn_grad_join_kernel(const __grid_consta
     const int b = (int)(r / a.rows / a.heads % a.B), set = (int)(r / a.rows / a.heads / a.B);
     const float* p = a.part + ((((int64_t)set * a.B + b) * a.heads + h) * a.rows_pad + i) * a.D + d;
     float f[8];
+    auto sum = [&](const float* q, float (&o)[8]) {
 #pragma unroll
-    for (int u = 0; u < 8; ++u) f[u] = 0.f;
+      for (int u = 0; u < 8; ++u) o[u] = 0.f;
 #pragma unroll 4
-    for (int z = 0; z < a.splits; ++z) {
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(p + z * stride));
-      const float4 w = __ldcg(reinterpret_cast<const float4*>(p + z * stride) + 1);
-      f[0] += v.x;
-      f[1] += v.y;
-      f[2] += v.z;
-      f[3] += v.w;
-      f[4] += w.x;
-      f[5] += w.y;
-      f[6] += w.z;
-      f[7] += w.w;
+      for (int z = 0; z < a.splits; ++z) {
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(q + z * stride));
+        const float4 w = __ldcg(reinterpret_cast<const float4*>(q + z * stride) + 1);
+        o[0] += v.x;
+        o[1] += v.y;
+        o[2] += v.z;
+        o[3] += v.w;
+        o[4] += w.x;
+        o[5] += w.y;
+        o[6] += w.z;
+        o[7] += w.w;
+      }
+    };
+    sum(p, f);
+    if (a.part_e) {
+      const int64_t row = ((int64_t)b * a.heads + h) * a.rows_pad + i, rows = (int64_t)a.B * a.heads * a.rows_pad;
+      float e = 0.f, k[8];
+      for (int z = 0; z < a.splits; ++z) e += __ldcg(a.part_e + z * rows + row);
+      sum(p + a.splits * stride, k);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) f[u] = fmaf(-e, k[u], f[u]);
+      if (d == 0) a.ndelta[row] -= e;
     }
 #pragma unroll
     for (int u = 0; u < 8; ++u) f[u] *= a.scale[set];
@@ -742,7 +1012,7 @@ GradPlan plan_grad(const sd_attention_cfg& c) {
   p.dq_splits = splits(p.dq_items, p.ktiles);
   p.rows_bytes = up256((size_t)c.batch * c.heads * p.qpad * 4);
   const size_t dkv = p.dkv_splits > 1 ? (size_t)p.dkv_splits * 2 * p.dkv_items * kTile * c.head_dim * 4 : 0;
-  const size_t dq = p.dq_splits > 1 ? (size_t)p.dq_splits * p.dq_items * kTile * c.head_dim * 4 : 0;
+  const size_t dq = p.dq_splits > 1 ? (size_t)p.dq_splits * p.dq_items * kTile * (2 * c.head_dim + 1) * 4 : 0;
   p.part_bytes = up256(std::max(dkv, dq));
   return p;
 }
@@ -765,8 +1035,8 @@ sd_status backward(AttnCall& c) {
   g.f.o = const_cast<void*>(c.o);
   g.qpad = p.qpad;
   g.qblocks = p.qblocks;
-  g.lse2 = reinterpret_cast<float*>(c.ws);
-  g.delta = reinterpret_cast<float*>(c.ws + p.rows_bytes);
+  g.nlse = reinterpret_cast<float*>(c.ws);
+  g.ndelta = reinterpret_cast<float*>(c.ws + p.rows_bytes);
   g.part = reinterpret_cast<float*>(c.ws + 2 * p.rows_bytes);
   g.lse = c.lse;
   g.d_o = c.d_o;
@@ -789,14 +1059,17 @@ sd_status backward(AttnCall& c) {
       !attn_map(&maps.v, f16, s.k_len ? c.v : any, s.k_len ? c.vs : unit, s.batch, nk, s.kv_heads, s.head_dim, 1, kTile))
     return SD_ERR_LAUNCH;
 
-  if (g.f.k_doc && s.k_len) OP_TRY(attn_doc_ranges(g.f.k_doc, s.batch, s.k_len, const_cast<int32_t*>(g.f.k_range), c.st));
-  if (g.f.q_doc && s.q_len) OP_TRY(attn_doc_ranges(g.f.q_doc, s.batch, s.q_len, const_cast<int32_t*>(g.f.q_range), c.st));
+  if (g.f.k_doc) OP_TRY(attn_doc_ranges(g.f, kTile, c.st));
   const double pairs = (double)s.batch * s.heads * s.q_len * s.k_len;
   const double act = 2.0 * s.batch * s.head_dim;
   if (s.q_len) {
     const int64_t rows = (int64_t)s.batch * s.heads * p.qpad;
     sdp::Scope sc("attn_delta", sdp::F_OTHER, 0, 2 * act * s.q_len * s.heads, c.st);
-    OP_TRY(launched(launch_pdl(attn_delta_kernel<T>, dim3((unsigned)((rows + 15) / 16)), dim3(256), 0, c.st, g)));
+    int lanes = 0;
+    while (8 << lanes < s.head_dim) ++lanes;
+    const int64_t per = 4 * (256 >> lanes);
+    OP_TRY(launched(
+        launch_pdl(attn_delta_kernel<T>, dim3((unsigned)((rows + per - 1) / per)), dim3(256), 0, c.st, g, lanes)));
   }
   if (!s.q_len) OP_TRY(launched(cudaMemsetAsync(c.args.err, 0, sizeof(int), c.st)));
   JoinArgs j;
@@ -804,42 +1077,23 @@ sd_status backward(AttnCall& c) {
   j.part = g.part;
   j.B = s.batch;
   j.D = s.head_dim;
-  if (s.k_len) {
-    g.f.splits = p.dkv_splits;
-    for (int i = 0; i < 3; ++i) {
-      g.s0[i] = j.s[0][i] = c.ks[i];
-      g.s1[i] = j.s[1][i] = c.vs[i];
-    }
-    g.out0 = j.out[0] = c.dk;
-    g.out1 = j.out[1] = c.dv;
-    OP_TRY((allow_smem<attn_dkv_kernel<T, NB>>(kDkvSmem<NB>, c.dev.index)));
-    {
-      sdp::Scope sc("attn_dkv", sdp::F_ATTN, 8.0 * pairs * s.head_dim,
-                    act * (2.0 * s.q_len * s.heads + 4.0 * s.k_len * s.kv_heads), c.st);
-      OP_TRY(launched(launch_pdl(attn_dkv_kernel<T, NB>, dim3((unsigned)(p.dkv_items * p.dkv_splits)), dim3(kThreads),
-                                 kDkvSmem<NB>, c.st, maps, g)));
-    }
-    if (p.dkv_splits > 1) {
-      j.scale[0] = g.out_scale;
-      j.scale[1] = g.v_scale;
-      j.splits = p.dkv_splits;
-      j.sets = 2;
-      j.heads = s.kv_heads;
-      j.rows = s.k_len;
-      j.rows_pad = p.ktiles * kTile;
-      sdp::Scope sc("attn_grad_join", sdp::F_OTHER, 0, 0, c.st);
-      OP_TRY(join<T>(c, j));
-    }
-  }
+  const bool shaped = g.f.cap_out != 0.f || g.f.slopes;
   if (s.q_len) {
+    // dq first: it corrects delta
     g.f.splits = p.dq_splits;
+    g.units = (int32_t)(p.dq_items * p.dq_splits);
+    g.part_e = g.part + (size_t)2 * p.dq_splits * p.dq_items * kTile * s.head_dim;
     for (int i = 0; i < 3; ++i) g.s0[i] = j.s[0][i] = c.qs[i];
     g.out0 = j.out[0] = c.dq;
-    OP_TRY((allow_smem<attn_dq_kernel<T, NB>>(kDqSmem<NB>, c.dev.index)));
+    auto* kernel = shaped ? attn_dq_kernel<T, NB, true> : attn_dq_kernel<T, NB, false>;
+    if (shaped)
+      OP_TRY((allow_smem<attn_dq_kernel<T, NB, true>>(kDqSmem<NB>, c.dev.index)));
+    else
+      OP_TRY((allow_smem<attn_dq_kernel<T, NB, false>>(kDqSmem<NB>, c.dev.index)));
     {
       sdp::Scope sc("attn_dq", sdp::F_ATTN, 2.0 * pairs * s.head_dim,
                     act * (3.0 * s.q_len * s.heads + 2.0 * s.k_len * s.kv_heads), c.st);
-      OP_TRY(launched(launch_pdl(attn_dq_kernel<T, NB>, dim3((unsigned)(p.dq_items * p.dq_splits)), dim3(kThreads),
+      OP_TRY(launched(launch_pdl(kernel, dim3((unsigned)g.units), dim3(kThreads),
                                  kDqSmem<NB>, c.st, maps, g)));
     }
     if (p.dq_splits > 1) {
@@ -849,6 +1103,40 @@ sd_status backward(AttnCall& c) {
       j.heads = s.heads;
       j.rows = s.q_len;
       j.rows_pad = p.qpad;
+      j.part_e = g.part_e;
+      j.ndelta = g.ndelta;
+      sdp::Scope sc("attn_grad_join", sdp::F_OTHER, 0, 0, c.st);
+      OP_TRY(join<T>(c, j));
+    }
+  }
+  if (s.k_len) {
+    g.f.splits = p.dkv_splits;
+    for (int i = 0; i < 3; ++i) {
+      g.s0[i] = j.s[0][i] = c.ks[i];
+      g.s1[i] = j.s[1][i] = c.vs[i];
+    }
+    g.out0 = j.out[0] = c.dk;
+    g.out1 = j.out[1] = c.dv;
+    auto* kernel = shaped ? attn_dkv_kernel<T, NB, true> : attn_dkv_kernel<T, NB, false>;
+    if (shaped)
+      OP_TRY((allow_smem<attn_dkv_kernel<T, NB, true>>(kDkvSmem<NB>, c.dev.index)));
+    else
+      OP_TRY((allow_smem<attn_dkv_kernel<T, NB, false>>(kDkvSmem<NB>, c.dev.index)));
+    {
+      sdp::Scope sc("attn_dkv", sdp::F_ATTN, 8.0 * pairs * s.head_dim,
+                    act * (2.0 * s.q_len * s.heads + 4.0 * s.k_len * s.kv_heads), c.st);
+      OP_TRY(launched(launch_pdl(kernel, dim3((unsigned)(p.dkv_items * p.dkv_splits)), dim3(kThreads),
+                                 kDkvSmem<NB>, c.st, maps, g)));
+    }
+    if (p.dkv_splits > 1) {
+      j.scale[0] = g.out_scale;
+      j.scale[1] = g.v_scale;
+      j.splits = p.dkv_splits;
+      j.sets = 2;
+      j.part_e = nullptr;
+      j.heads = s.kv_heads;
+      j.rows = s.k_len;
+      j.rows_pad = p.ktiles * kTile;
       sdp::Scope sc("attn_grad_join", sdp::F_OTHER, 0, 0, c.st);
       OP_TRY(join<T>(c, j));
     }

@@ -6,22 +6,26 @@
 // operations and one exponential a pair; three with a cap), by reading keys and
 // values for single tokens.
 //
-// A CTA owns 128 query rows: kTile / G tokens with the G query heads that share a
-// key head, so a key tile is read once for all of them. It lists the key tiles
-// that its rows may see (length, causal limit with prefix, document ranges) as
-// bits in shared memory and visits only those; tiles that every row sees whole
-// skip the masks. Few rows and many keys: the visible tiles are split between CTAs
-// and a second kernel joins the parts.
+// A unit of work is 128 query rows: kTile / G tokens with the G query heads that
+// share a key head, so a key tile is read once for all of them. Its key tiles are
+// found by vote, 32 at a time (length, causal limit with prefix, document ranges),
+// and only those that some row may see are visited; tiles that every row sees whole
+// skip the masks. Few rows and many keys: the visible tiles are split between units
+// and a second kernel joins the parts. The grid has one CTA per unit, and a CTA that
+// runs takes over units of CTAs that have not been launched yet (cluster launch
+// control), so the loads and the first product of a unit run beside the end of the
+// one before and long units even out.
 //
-// 192 threads, two CTAs per SM:
-//   warps 0-3  one query row per thread: S from TMEM into registers, cap, bias, mask,
-//              running maximum (log2 domain), P = exp2(s - m) rounded to the inputs'
-//              type (the tensor core takes no other; the row sum uses the unrounded
-//              FP32 values) and written back to TMEM, where the second product
-//              takes it as its A operand. O stays in TMEM and is rescaled only when
-//              the maximum grew by more than 2^8.
-//   warp 4     TMA: Q once, K and V tiles
-//   warp 5     one thread issues S = Q K^T and O += P V
+// 320 threads, two CTAs per SM:
+//   warps 0-7  two threads per query row, 64 keys each: S from TMEM into registers, cap,
+//              bias, mask, running maximum (log2 domain; the halves meet in shared
+//              memory), P = exp2(s - m) rounded to the inputs' type (the tensor core
+//              takes no other; the row sum uses the unrounded FP32 values) and
+//              written back to TMEM, where the second product takes it as its A
+//              operand. O stays in TMEM and is rescaled only when the maximum grew
+//              by more than 2^8.
+//   warp 8     TMA: Q once, K and V tiles
+//   warp 9     one thread issues S = Q K^T and O += P V
 // TMEM (256 columns): head_dim <= 64: S [0,128), P [128,192), O [192,256), so S of the
 // next tile is computed beside P of this one; head_dim <= 128: S [0,128) with P over its
 // first half, O [128,256): there the two CTAs of an SM overlap each other instead.
@@ -36,24 +40,108 @@
 namespace sdo {
 namespace {
 
-constexpr int kThreads = 192;
-constexpr int kSlots = 296;      // CTAs that fill 148 SMs
+constexpr int kThreads = 320;
+constexpr int kSoftmax = 256;   // threads of the softmax warps
+constexpr int kSms = 148;
 constexpr int kMaxSplits = 64;
 
 template <int NB>
 struct Shape {
-  static constexpr int kStages = NB == 1 ? 2 : 1;
-  static constexpr int kQBytes = NB * kBlockBytes;
+  static constexpr int kStages = NB == 1 ? 2 : 1;  // of Q, K and V each
+  static constexpr int kBytes = NB * kBlockBytes;
   static constexpr uint32_t kP = NB == 1 ? 128 : 0;
   static constexpr uint32_t kO = NB == 1 ? 192 : 128;
-  static constexpr size_t kSmem = 1024 + (size_t)(1 + 2 * kStages) * kQBytes + sizeof(TileBits) + 512 + 256;
+  static constexpr size_t kSmem = 1024 + (size_t)3 * kStages * kBytes + kDocRing * 512 + 2048 + kRing * sizeof(Record) + 512;
 };
 
 struct __align__(64) FwdMaps {
   CUtensorMap q, k, v;
 };
 
+// A unit of work: split z of 128 query rows. The last query tiles come first (with
+// a causal mask they are the longest).
+struct Unit {
+  int item, z, b, kv, i0, i1, qt;
+  __device__ __forceinline__ Unit(const AttnArgs& a, int u) {
+    z = u % a.splits;
+    item = u / a.splits;
+    const int heads = a.B * a.KV, at = item % heads;
+    qt = a.qtiles - 1 - item / heads;
+    b = at / a.KV;
+    kv = at % a.KV;
+    i0 = qt * a.tq;
+    i1 = min(a.Nq, i0 + a.tq) - 1;
+  }
+  __device__ __forceinline__ const int32_t* docs(const AttnArgs& a) const {
+    return a.q_range + ((int64_t)b * a.qtiles + qt) * 2;
+  }
+};
+// The unit's walk and its number of steps (INT32_MAX: until the walk ends).
+struct UnitWalk : TileWalk<RowTiles> {
+  int steps;
+  __device__ __forceinline__ UnitWalk(const AttnArgs& a, const Unit& u, int off, int nk, int pre)
+      : TileWalk<RowTiles>(RowTiles(a, u.b, u.i0, u.i1, off, nk, pre, u.docs(a))) {
+    steps = INT32_MAX;
+    if (a.splits > 1) {
+      const int n = count(), first = (int)((int64_t)n * u.z / a.splits);
+      steps = (int)((int64_t)n * (u.z + 1) / a.splits) - first;
+      if (steps > 0) skip(first);
+    }
+  }
+  __device__ __forceinline__ int step(bool& whole) { return steps-- > 0 ? next(whole) : -1; }
+};
+
+// The end of a unit: one query row per thread, normalised to the output, or its part
+// of a split. Out of line: it runs once per unit and its registers would compete with
+// the score row of the loop.
 template <typename T, int NB>
+__device__ __noinline__ void store_rows(const AttnArgs& a, int64_t slot, int b, int i, int h, int half, uint32_t tO,
+                                        bool some, bool valid, float m, float l) {
+  const bool part = a.splits > 1;
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  T* dst = static_cast<T*>(a.o) + b * a.os[0] + i * a.os[1] + h * a.os[2];
+#pragma unroll 1
+  for (int k = 0; k < NB * 32; k += 32) {
+    const int c = half * NB * 32 + k;
+    if (c >= a.D) break;
+    uint32_t r[32];
+    if (some) {
+      tmem_ld_32x32b_x32(tO + k, r);
+      tmem_ld_wait_regs(r);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 32; ++q) r[q] = 0u;
+    }
+    if (valid && part && some) {
+      float4* p = reinterpret_cast<float4*>(a.partial + slot * a.D + c);
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (c + 4 * q < a.D)
+          __stcg(p + q, make_float4(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]),
+                                    __uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3])));
+    } else if (valid && !part) {
+      // a row whose mask leaves nothing has l = 0 and gets zeros
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (c + 8 * q < a.D)
+          *reinterpret_cast<uint4*>(dst + c + 8 * q) = make_uint4(
+              Elem<T>::pack(__uint_as_float(r[8 * q]) * inv, __uint_as_float(r[8 * q + 1]) * inv),
+              Elem<T>::pack(__uint_as_float(r[8 * q + 2]) * inv, __uint_as_float(r[8 * q + 3]) * inv),
+              Elem<T>::pack(__uint_as_float(r[8 * q + 4]) * inv, __uint_as_float(r[8 * q + 5]) * inv),
+              Elem<T>::pack(__uint_as_float(r[8 * q + 6]) * inv, __uint_as_float(r[8 * q + 7]) * inv));
+    }
+  }
+  if (half) return;
+  if (valid && part) {
+    a.partial_ml[slot * 2] = m;
+    a.partial_ml[slot * 2 + 1] = l;
+  } else if (valid && a.lse) {
+    a.lse[((int64_t)b * a.H + h) * a.Nq + i] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+  }
+}
+
+// SHAPED: the scores are capped or biased before the mask.
+template <typename T, int NB, bool SHAPED>
 __global__ void __launch_bounds__(kThreads, 2)
     attn_fwd_kernel(const __grid_constant__ FwdMaps maps, const __grid_constant__ AttnArgs a) {
   using Sh = Shape<NB>;
@@ -62,45 +150,43 @@ __global__ void __launch_bounds__(kThreads, 2)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;
-  uint8_t* sK = sQ + Sh::kQBytes;
-  uint8_t* sV = sK + KS * Sh::kQBytes;
-  TileBits* tiles = reinterpret_cast<TileBits*>(sV + KS * Sh::kQBytes);
-  int32_t* sdoc = reinterpret_cast<int32_t*>(tiles + 1);  // [128] documents of the current key tile
-  uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(sdoc) + 512);
-  uint64_t* q_full = bars;
-  uint64_t* k_full = bars + 1;    // [KS]
-  uint64_t* k_empty = bars + 3;   // [KS]
-  uint64_t* v_full = bars + 5;    // [KS]
-  uint64_t* v_empty = bars + 7;   // [KS]
-  uint64_t* s_full = bars + 9;
-  uint64_t* s_free = bars + 10;
-  uint64_t* p_full = bars + 11;
-  uint64_t* pv_done = bars + 12;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 13);
+  uint8_t* sK = sQ + KS * Sh::kBytes;
+  uint8_t* sV = sK + KS * Sh::kBytes;
+  int32_t* sdocs = reinterpret_cast<int32_t*>(sV + KS * Sh::kBytes);  // [kDocRing][128]
+  float* smax = reinterpret_cast<float*>(sdocs + kDocRing * kTile);  // [2][2][128] the halves' row maxima, by step parity
+  Record* recs = reinterpret_cast<Record*>(smax + 4 * kTile);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(recs + kRing);
+  uint64_t* q_full = bars;        // [KS]
+  uint64_t* q_empty = bars + 2;   // [KS]
+  uint64_t* k_full = bars + 4;    // [KS]
+  uint64_t* k_empty = bars + 6;   // [KS]
+  uint64_t* v_full = bars + 8;    // [KS]
+  uint64_t* v_empty = bars + 10;  // [KS]
+  uint64_t* s_full = bars + 12;
+  uint64_t* pv_done = bars + 13;
+  uint64_t* s_free = bars + 14;
+  uint64_t* p_full = bars + 15;
+  uint64_t* rec_full = bars + 16;   // [kRing]
+  uint64_t* rec_empty = bars + 20;  // [kRing], eight softmax warps and the MMA warp
+  uint64_t* next_bar = bars + 24;
+  uint8_t* next_unit = reinterpret_cast<uint8_t*>(bars + 26);  // 16 bytes
+  uint64_t* doc_full = bars + 28;  // [kDocRing]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 28 + kDocRing);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int32_t* doc_lo = reinterpret_cast<int32_t*>(tmem_slot + 2);
-  int32_t* doc_hi = doc_lo + 1;
+  const RecordRing ring{recs, rec_full, rec_empty, abort_flag, a.err};
+  const DocRing docs{sdocs, doc_full, abort_flag, a.err};
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // item: the last query tiles first (with a causal mask they are the longest)
-  const int z = blockIdx.x % a.splits;
-  const int item = blockIdx.x / a.splits;
-  const int heads = a.B * a.KV;
-  const int qt = a.qtiles - 1 - item / heads;
-  const int b = item % heads / a.KV, kv = item % heads % a.KV;
-  const int i0 = qt * a.tq, i1 = min(a.Nq, i0 + a.tq) - 1;
-
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 13; ++i) mbar_init(bars + i, i == 10 || i == 11 ? 128 : 1);
+    for (int i = 0; i < kDocRing; ++i) mbar_init(&doc_full[i], 1);
+    for (int i = 0; i < 25; ++i) mbar_init(bars + i, i == 14 || i == 15 ? kSoftmax : i >= 20 && i < 24 ? 9 : 1);
     *abort_flag = 0;
-    *doc_lo = INT32_MAX;
-    *doc_hi = INT32_MIN;
     fence_barrier_init();
     tma_prefetch_desc(&maps.q);
     tma_prefetch_desc(&maps.k);
     tma_prefetch_desc(&maps.v);
   }
-  if (warp == 5) tmem_alloc(tmem_slot, 256);
+  if (warp == 9) tmem_alloc(tmem_slot, 256);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -110,312 +196,346 @@ __global__ void __launch_bounds__(kThreads, 2)
   pdl_trigger();
   if (a.clear_err && blockIdx.x == 0 && threadIdx.x == 0) *a.err = 0;
 
-  const int nk = keys_of(a, b), off = nk - a.Nq, pre = prefix_of(a, b);
-  if (a.q_doc) {
-    for (int i = i0 + (int)threadIdx.x; i <= i1; i += kThreads) {
-      const int d = a.q_doc[(int64_t)b * a.Nq + i];
-      atomicMin(doc_lo, d);
-      atomicMax(doc_hi, d);
-    }
-    __syncthreads();
-  }
-  // the last key any row sees, and the last one that all rows see, but for documents
-  const int lim_any = a.causal ? min(nk, max(i1 + off + 1, pre)) : nk;
-  const int lim_all = a.causal ? min(nk, max(i0 + off + 1, pre)) : nk;
-  {
-    const int words = (a.ktiles + 31) >> 5;
-    for (int w = warp; w < words; w += kThreads / 32) {
-      const int j = w * 32 + lane;
-      bool see = j < a.ktiles && j * kTile < lim_any;
-      bool all = see && (j + 1) * kTile <= lim_all;
-      if (see && a.k_range) {
-        const int32_t lo = a.k_range[((int64_t)b * a.ktiles + j) * 2], hi = a.k_range[((int64_t)b * a.ktiles + j) * 2 + 1];
-        see = lo <= *doc_hi && *doc_lo <= hi;
-        all = all && lo == hi && *doc_lo == lo && *doc_hi == lo;
-      }
-      const uint32_t ms = __ballot_sync(0xffffffffu, see), ma = __ballot_sync(0xffffffffu, all);
+  // t counts steps and n units with steps since the kernel began: they give each
+  // barrier's phase.
+  if (warp == 8) {
+    int t = 0, n = 0, r = 0, asked = 0;
+    bool ok = true;
+    for (int x = blockIdx.x; x >= 0 && ok;) {
+      const Unit u(a, x);
+      const int nk = keys_of(a, u.b), pre = prefix_of(a, u.b);
+      UnitWalk walk(a, u, nk - a.Nq, nk, pre);
+      bool whole, whole_next;
+      int j = walk.step(whole), after;
+      int first = kFirst;
+      do {
+        after = j >= 0 ? walk.step(whole_next) : -1;
+        if (lane == 0) {
+          Record rec = {j, first | (after < 0 ? kLast : 0) | (j >= 0 && whole ? kWhole : 0), u.item, nk, pre, 0, u.b,
+                        u.kv, u.i0, u.z, {0, 0}};
+          if (j >= 0) rec.flags |= walk.one_doc(j, rec.doc);
+          ok = ring.put(r, rec);
+          if (after < 0) {
+            // at the unit's end: a unit asked for early would wait behind a long one
+            mbar_arrive_expect_tx(next_bar, 16);
+            ask_unit(next_unit, next_bar);
+          }
+          if (ok && a.k_pad && j < 0) docs.skip(r);
+          if (j >= 0) {
+            if (ok && a.k_pad) docs.load(r, a.k_pad + ((int64_t)u.b * a.ktiles + j) * kTile);
+            if (first) {
+              const int s = n % KS;
+              ok = ok && (n < KS || mbar_wait(&q_empty[s], (n / KS - 1) & 1, abort_flag, a.err));
+              if (ok) {
+                mbar_arrive_expect_tx(&q_full[s], (uint32_t)(NB * 128 * a.tq * a.G));
+                for (int c = 0; c < NB; ++c)
+                  tma_load_4d(sQ + s * Sh::kBytes + c * kBlockBytes, &maps.q, &q_full[s], c * 64, u.kv * a.G, u.i0,
+                              u.b);
+              }
+            }
+            const int s = t % KS;
+            const uint32_t ph = (t / KS - 1) & 1;
+            ok = ok && (t < KS || mbar_wait(&k_empty[s], ph, abort_flag, a.err));
+            if (ok) {
+              mbar_arrive_expect_tx(&k_full[s], Sh::kBytes);
+              for (int c = 0; c < NB; ++c)
+                tma_load_4d(sK + s * Sh::kBytes + c * kBlockBytes, &maps.k, &k_full[s], c * 64, u.kv, j * kTile, u.b);
+            }
+            ok = ok && (t < KS || mbar_wait(&v_empty[s], ph, abort_flag, a.err));
+            if (ok) {
+              mbar_arrive_expect_tx(&v_full[s], Sh::kBytes);
+              for (int c = 0; c < NB; ++c)
+                tma_load_4d(sV + s * Sh::kBytes + c * kBlockBytes, &maps.v, &v_full[s], c * 64, u.kv, j * kTile, u.b);
+            }
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        ++r;
+        if (j >= 0) {
+          ++t;
+          n += first ? 1 : 0;
+        }
+        first = 0;
+        j = after;
+        whole = whole_next;
+      } while (j >= 0 && ok);
       if (lane == 0) {
-        tiles->see[w] = ms;
-        tiles->all[w] = ma;
+        ok = mbar_wait(next_bar, asked & 1, abort_flag, a.err) && ok;
+        x = ok ? asked_unit(next_unit) : -1;
+        fence_async_smem();  // read before the next answer is written
       }
+      ++asked;
+      x = __shfl_sync(0xffffffffu, x, 0);
+      ok = __shfl_sync(0xffffffffu, ok, 0);
     }
-    __syncthreads();
-    if (warp == 0) {
-      int n = 0;
-      for (int w = lane; w < words; w += 32) n += __popc(tiles->see[w]);
+    if (lane == 0 && ok) ring.end(r);
+  } else if (warp == 9) {
+    const int nd = (a.D + 15) >> 4;  // head dimension in steps of 16
+    const uint32_t id_s = idesc_f16(128, 128, f16, false, false);
+    const uint32_t id_o = idesc_f16(128, nd * 16, f16, false, true);
+    auto issue_s = [&](int t, int n, bool first, bool last) {
+      const int s = t % KS, sq = n % KS;
+      if (first && !mbar_wait(&q_full[sq], (n / KS) & 1, abort_flag, a.err)) return false;
+      if (!mbar_wait(&k_full[s], (t / KS) & 1, abort_flag, a.err)) return false;
+      tc_fence_after();
+      const uint32_t q0 = smem_u32(sQ + sq * Sh::kBytes), k0 = smem_u32(sK + s * Sh::kBytes);
+      for (int d = 0; d < nd; ++d) {
+        const uint32_t o = (d >> 2) * kBlockBytes + (d & 3) * 32;
+        umma_bf16(tS, umma_desc_k_sw128(q0 + o), umma_desc_k_sw128(k0 + o), id_s, d > 0);
+      }
+      umma_commit(&k_empty[s]);
+      umma_commit(s_full);
+      if (last) umma_commit(&q_empty[sq]);
+      return true;
+    };
+    auto issue_pv = [&](int t, bool first) {
+      const int s = t % KS;
+      if (!mbar_wait(p_full, t & 1, abort_flag, a.err)) return false;
+      if (!mbar_wait(&v_full[s], (t / KS) & 1, abort_flag, a.err)) return false;
+      tc_fence_after();
+      const uint32_t v0 = smem_u32(sV + s * Sh::kBytes);
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-      if (lane == 0) tiles->count = n;
-    }
-    __syncthreads();
-  }
-  const int first = (int)((int64_t)tiles->count * z / a.splits);
-  const int steps = (int)((int64_t)tiles->count * (z + 1) / a.splits) - first;
-
-  if (warp == 4) {
-    if (lane == 0 && steps > 0) {
-      TileWalk walk;
-      walk.start(tiles, a.ktiles, first);
-      mbar_arrive_expect_tx(q_full, (uint32_t)(NB * 128 * a.tq * a.G));
-      for (int c = 0; c < NB; ++c) tma_load_4d(sQ + c * kBlockBytes, &maps.q, q_full, c * 64, kv * a.G, i0, b);
-      for (int t = 0; t < steps; ++t) {
-        const int j = walk.next() * kTile, s = t % KS;
-        const uint32_t ph = (t / KS - 1) & 1;
-        if (t >= KS && !mbar_wait(&k_empty[s], ph, abort_flag, a.err)) break;
-        mbar_arrive_expect_tx(&k_full[s], Sh::kQBytes);
-        for (int c = 0; c < NB; ++c)
-          tma_load_4d(sK + s * Sh::kQBytes + c * kBlockBytes, &maps.k, &k_full[s], c * 64, kv, j, b);
-        if (t >= KS && !mbar_wait(&v_empty[s], ph, abort_flag, a.err)) break;
-        mbar_arrive_expect_tx(&v_full[s], Sh::kQBytes);
-        for (int c = 0; c < NB; ++c)
-          tma_load_4d(sV + s * Sh::kQBytes + c * kBlockBytes, &maps.v, &v_full[s], c * 64, kv, j, b);
-      }
-    }
-  } else if (warp == 5) {
-    if (lane == 0 && steps > 0) {
-      const int nd = (a.D + 15) >> 4;  // head dimension in steps of 16
-      const uint32_t id_s = idesc_f16(128, 128, f16, false, false);
-      const uint32_t id_o = idesc_f16(128, nd * 16, f16, false, true);
-      const uint32_t q0 = smem_u32(sQ);
-      bool ok = mbar_wait(q_full, 0, abort_flag, a.err);
-      auto issue_s = [&](int t) {
-        const int s = t % KS;
-        if (!mbar_wait(&k_full[s], (t / KS) & 1, abort_flag, a.err)) return false;
-        tc_fence_after();
-        const uint32_t k0 = smem_u32(sK + s * Sh::kQBytes);
-        for (int d = 0; d < nd; ++d) {
-          const uint32_t o = (d >> 2) * kBlockBytes + (d & 3) * 32;
-          umma_bf16(tS, umma_desc_k_sw128(q0 + o), umma_desc_k_sw128(k0 + o), id_s, d > 0);
+      for (int k = 0; k < 8; ++k)
+        umma_ts(tO, tP + 8 * k, umma_desc_mn(v0 + k * 2048, kBlockBytes), id_o, (!first || k > 0) ? 1u : 0u);
+      umma_commit(&v_empty[s]);
+      umma_commit(pv_done);
+      return true;
+    };
+    // NB = 1: S of a step beside the softmax of the one before, across units; that
+    // step's PV product is pending meanwhile
+    int t = 0, n = -1;
+    bool ok = true, pending = false, pending_first = false;
+    for (int r = 0; ok; ++r) {
+      const int2 rec = ring.get(r);  // tile, flags
+      if (rec.x >= 0) {
+        const bool first = rec.y & kFirst, last = rec.y & kLast;
+        n += first;
+        if (lane == 0) {
+          if constexpr (NB == 1) {
+            ok = (t == 0 || mbar_wait(s_free, (t - 1) & 1, abort_flag, a.err)) && issue_s(t, n, first, last);
+            if (ok && pending) ok = issue_pv(t - 1, pending_first);
+          } else {
+            ok = issue_s(t, n, first, last) && issue_pv(t, first);
+          }
         }
-        umma_commit(&k_empty[s]);
-        umma_commit(s_full);
-        return true;
-      };
-      auto issue_pv = [&](int t) {
-        const int s = t % KS;
-        if (!mbar_wait(p_full, t & 1, abort_flag, a.err)) return false;
-        if (!mbar_wait(&v_full[s], (t / KS) & 1, abort_flag, a.err)) return false;
-        tc_fence_after();
-        const uint32_t v0 = smem_u32(sV + s * Sh::kQBytes);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          umma_ts(tO, tP + 8 * k, umma_desc_mn(v0 + k * 2048, kBlockBytes), id_o, (t > 0 || k > 0) ? 1u : 0u);
-        umma_commit(&v_empty[s]);
-        umma_commit(pv_done);
-        return true;
-      };
-      if constexpr (NB == 1) {
-        // S of step t beside the softmax of step t - 1
-        for (int t = 0; t <= steps && ok; ++t) {
-          if (t < steps) ok = (t == 0 || mbar_wait(s_free, (t - 1) & 1, abort_flag, a.err)) && issue_s(t);
-          if (ok && t > 0) ok = issue_pv(t - 1);
-        }
-      } else {
-        for (int t = 0; t < steps && ok; ++t) ok = issue_s(t) && issue_pv(t);
+        ++t;
+        pending = NB == 1;
+        pending_first = first;
       }
+      if (pending && rec.x < 0) {
+        // nothing to issue beside it: the next record has no tile, or there is none
+        if (lane == 0) ok = issue_pv(t - 1, pending_first);
+        pending = false;
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (rec.y & kEnd) break;
     }
   } else {
-    const int row = threadIdx.x;
-    const int i = i0 + row / a.G, h = kv * a.G + row % a.G;
-    const bool valid = row < a.tq * a.G && i < a.Nq;
-    const bool work = __any_sync(0xffffffffu, valid);  // a warp without rows only keeps the barriers going
-    const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
-    const int pos = i + off;
-    const int lim = !valid ? 0 : a.causal ? min(nk, max(pos + 1, pre)) : nk;
-    const int doc = a.q_doc && valid ? a.q_doc[(int64_t)b * a.Nq + i] : 0;
-    const float slope = a.slopes && valid ? a.slopes[h] * kLog2e : 0.f;
-    const bool scaled = a.cap_out != 0.f || a.slopes;  // the scores are in log2 units before the maximum
-    const float mul = scaled ? 1.f : a.sl2;
-    float m = -INFINITY, l = 0.f;
-    TileWalk walk;
-    if (steps > 0) walk.start(tiles, a.ktiles, first);
-    bool alive = true;
-    for (int t = 0; t < steps; ++t) {
-      const int j = walk.next(), j0 = j * kTile;
-      const bool whole = walk.whole(j);
-      const int s = t % KS;
-      if (!mbar_wait_all(s_full, t & 1, abort_flag, a.err)) {
-        alive = false;
-        break;
+    const int q4 = warp & 3, half = warp >> 2;
+    const int row = q4 * 32 + lane, row_i = row / a.G, row_h = row % a.G;  // token and head within the unit
+    const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
+    const uint32_t tSr = tS + lane_off + half * 64, tPr = tP + lane_off + half * 32;
+    const uint32_t tOr = tO + lane_off + half * NB * 32;  // the columns of O this half rescales and stores
+    const float mul = SHAPED ? 1.f : a.sl2;  // shaped scores are in log2 units before the maximum
+    int t = 0;
+    bool alive = true, valid = false, work = false, some = false;
+    int nk = 0, pos = 0, lim = 0, doc = 0;
+    float slope = 0.f, m = -INFINITY, l = 0.f;
+    for (int r = 0;; ++r) {
+      const Record* const rec = ring.at(r);
+      if (!rec || (rec->flags & kEnd)) break;
+      const int flags = rec->flags, tile = rec->tile;
+      const bool first = flags & kFirst, whole = flags & kWhole;
+      if (first) {
+        const int i = rec->i0 + row_i;
+        nk = rec->nk;
+        valid = row < a.tq * a.G && i < a.Nq;
+        work = __any_sync(0xffffffffu, valid);
+        pos = i + nk - a.Nq;
+        lim = !valid ? 0 : a.causal ? min(nk, max(pos + 1, rec->pre)) : nk;
+        doc = a.q_doc && valid ? a.q_doc[(int64_t)rec->b * a.Nq + i] : 0;
+        if (SHAPED) slope = a.slopes && valid ? a.slopes[rec->head * a.G + row_h] * kLog2e : 0.f;
+        m = -INFINITY;
+        l = 0.f;
       }
-      tc_fence_after();
-      uint32_t sv[128];
-      if (work) {
-        tmem_ld_32x32b_x32(tS + lane_off, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
-        tmem_ld_32x32b_x32(tS + lane_off + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
-        tmem_ld_32x32b_x32(tS + lane_off + 64, *reinterpret_cast<uint32_t(*)[32]>(&sv[64]));
-        tmem_ld_32x32b_x32(tS + lane_off + 96, *reinterpret_cast<uint32_t(*)[32]>(&sv[96]));
-        tmem_ld_wait();
-      }
-      if constexpr (NB == 1) {
-        tc_fence_before();
-        mbar_arrive(s_free);
-      }
-      if (!whole && a.k_doc) {
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        sdoc[row] = j0 + row < a.Nk ? a.k_doc[(int64_t)b * a.Nk + j0 + row] : 0;
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-      }
-      if (!whole && j0 + kTile > nk && nk < a.Nk) {
-        // values behind the last key count as zeros, whatever they hold
-        if (!mbar_wait_all(&v_full[s], (t / KS) & 1, abort_flag, a.err)) {
-          alive = false;
-          break;
-        }
-        if (j0 + row >= nk) {
+      some = tile >= 0;
+      if (some) {
+        const int j0 = tile * kTile;
+        // what all softmax warps do together for a tile that not every row sees whole
+        auto prepare_masks = [&]() {
+          if (j0 + kTile > nk && nk < a.Nk) {
+            // values behind the last key count as zeros, whatever they hold
+            const int s = t % KS;
+            if (!mbar_wait_all(&v_full[s], (t / KS) & 1, abort_flag, a.err)) return false;
+            if (half == 0 && j0 + row >= nk) {
 #pragma unroll
-          for (int c = 0; c < NB; ++c) {
-            uint4* p = reinterpret_cast<uint4*>(sV + s * Sh::kQBytes + c * kBlockBytes + row * 128);
+              for (int c = 0; c < NB; ++c) {
+                uint4* p = reinterpret_cast<uint4*>(sV + s * Sh::kBytes + c * kBlockBytes + row * 128);
 #pragma unroll
-            for (int u = 0; u < 8; ++u) p[u] = make_uint4(0u, 0u, 0u, 0u);
-          }
-        }
-        fence_async_smem();
-      }
-      float alpha = 1.f;
-      bool rescale = false;
-      uint32_t pk[64];
-      if (work) {
-        if (a.cap_out != 0.f) {
-#pragma unroll
-          for (int c = 0; c < 128; ++c)
-            sv[c] = __float_as_uint(a.cap_out * tanh_acc(__uint_as_float(sv[c]) * a.cap_in));
-        } else if (scaled) {
-#pragma unroll
-          for (int c = 0; c < 128; ++c) sv[c] = __float_as_uint(__uint_as_float(sv[c]) * a.sl2);
-        }
-        if (a.slopes) {
-          const float p0 = (float)(pos - j0);
-#pragma unroll
-          for (int c = 0; c < 128; ++c)
-            sv[c] = __float_as_uint(fmaf(-slope, fabsf(p0 - (float)c), __uint_as_float(sv[c])));
-        }
-        if (!whole) {
-          const int lc = lim - j0;
-          if (a.k_doc) {
-#pragma unroll
-            for (int c = 0; c < 128; c += 4) {
-              const int4 d = *reinterpret_cast<const int4*>(sdoc + c);
-              if (c >= lc || d.x != doc) sv[c] = __float_as_uint(-INFINITY);
-              if (c + 1 >= lc || d.y != doc) sv[c + 1] = __float_as_uint(-INFINITY);
-              if (c + 2 >= lc || d.z != doc) sv[c + 2] = __float_as_uint(-INFINITY);
-              if (c + 3 >= lc || d.w != doc) sv[c + 3] = __float_as_uint(-INFINITY);
+                for (int q = 0; q < 8; ++q) p[q] = make_uint4(0u, 0u, 0u, 0u);
+              }
             }
-          } else {
-#pragma unroll
-            for (int c = 0; c < 128; ++c)
-              if (c >= lc) sv[c] = __float_as_uint(-INFINITY);
+            fence_async_smem();
           }
-        }
-        float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < 128; c += 8) {
-          m0 = max3f(m0, __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
-          m1 = max3f(m1, __uint_as_float(sv[c + 2]), __uint_as_float(sv[c + 3]));
-          m2 = max3f(m2, __uint_as_float(sv[c + 4]), __uint_as_float(sv[c + 5]));
-          m3 = max3f(m3, __uint_as_float(sv[c + 6]), __uint_as_float(sv[c + 7]));
-        }
-        const float m_new = fmaxf(m, max3f(m0, m1, fmaxf(m2, m3)) * mul);
-        if (m == -INFINITY) {
-          m = m_new;  // nothing seen so far: O's row is zeros (or not written yet)
-        } else if (m_new > m + 8.f) {
-          alpha = fast_ex2(m - m_new);
-          l *= alpha;
-          m = m_new;
-          rescale = true;
-        }
-        const float base = m == -INFINITY ? 0.f : -m;  // a row without keys: exp2(-inf) = 0 throughout
-        float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
-#pragma unroll
-        for (int c = 0; c < 128; c += 4) {
-          float x0, x1, x2, x3;
-          fma2v(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1]), mul, mul, base, base, x0, x1);
-          fma2v(__uint_as_float(sv[c + 2]), __uint_as_float(sv[c + 3]), mul, mul, base, base, x2, x3);
-          x0 = fast_ex2(x0);
-          x1 = fast_ex2(x1);
-          x2 = fast_ex2(x2);
-          x3 = fast_ex2(x3);
-          add2(l0, l1, x0, x1, l0, l1);
-          add2(l2, l3, x2, x3, l2, l3);
-          pk[c / 2] = Elem<T>::pack(x0, x1);
-          pk[c / 2 + 1] = Elem<T>::pack(x2, x3);
-        }
-        l += (l0 + l1) + (l2 + l3);
-      }
-      // P and O are free once the previous product is done
-      if (t > 0 && !mbar_wait_all(pv_done, (t - 1) & 1, abort_flag, a.err)) {
-        alive = false;
-        break;
-      }
-      tc_fence_after();
-      if (__any_sync(0xffffffffu, rescale)) {
-#pragma unroll 1
-        for (int c = 0; c < 2 * NB; ++c) {
-          uint32_t r[32];
-          tmem_ld_32x32b_x32(tO + lane_off + c * 32, r);
-          tmem_ld_wait_regs(r);
-#pragma unroll
-          for (int u = 0; u < 32; ++u) r[u] = __float_as_uint(__uint_as_float(r[u]) * alpha);
-          tmem_st_x32(tO + lane_off + c * 32, r);
-        }
-      }
-      if (work) {
-        tmem_st_x32(tP + lane_off, pk);
-        tmem_st_x32(tP + lane_off + 32, pk + 32);
-      }
-      tmem_store_wait();
-      tc_fence_before();
-      mbar_arrive(p_full);
-    }
-    if (alive && steps > 0) alive = mbar_wait_all(pv_done, (steps - 1) & 1, abort_flag, a.err);
-    tc_fence_after();
-    if (alive && work) {
-      const bool part = a.splits > 1;
-      const float inv = l > 0.f ? 1.f / l : 0.f;
-      T* dst = static_cast<T*>(a.o) + b * a.os[0] + i * a.os[1] + h * a.os[2];
-      const int64_t slot = ((int64_t)item * a.splits + z) * kTile + row;
-#pragma unroll 1
-      for (int c = 0; c < NB * 64; c += 32) {
-        if (c >= a.D) break;
-        uint32_t r[32];
-        if (steps > 0) {
-          tmem_ld_32x32b_x32(tO + lane_off + c, r);
-          tmem_ld_wait_regs(r);
+          return true;
+        };
+        if (!(alive = mbar_wait_all(s_full, t & 1, abort_flag, a.err))) break;
+        tc_fence_after();
+        if (!work) {
+          // a warp without rows only keeps the barriers going (its rows of P and O are never read)
+          if (NB == 1) mbar_arrive(s_free);
+          if (!whole && !(alive = prepare_masks())) break;
+          // not ahead of the working warps by more than this tile: their arrivals share a phase
+          if (!first && !(alive = mbar_wait_all(pv_done, (t - 1) & 1, abort_flag, a.err))) break;
+          mbar_arrive(p_full);
         } else {
+          uint32_t sv[64];
+          tmem_ld_32x32b_x32(tSr, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
+          tmem_ld_32x32b_x32(tSr + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
+          tmem_ld_wait_regs(*reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
+          tmem_ld_wait_regs(*reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
+          if constexpr (NB == 1) {
+            tc_fence_before();
+            mbar_arrive(s_free);
+          }
+          if constexpr (SHAPED) {
+            if (a.cap_out != 0.f) {
+              float top = 0.f;
 #pragma unroll
-          for (int u = 0; u < 32; ++u) r[u] = 0u;
+              for (int c = 0; c < 64; c += 2)
+                top = max3f(top, fabsf(__uint_as_float(sv[c])), fabsf(__uint_as_float(sv[c + 1])));
+              if (__all_sync(0xffffffffu, top * a.cap_in <= kTanhSmall)) {
+#pragma unroll
+                for (int c = 0; c < 64; c += 2) {
+                  float x0, x1;
+                  mul2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1]), a.cap_in, a.cap_in, x0, x1);
+                  tanh_small2(x0, x1, x0, x1);
+                  mul2(x0, x1, a.cap_out, a.cap_out, x0, x1);
+                  sv[c] = __float_as_uint(x0);
+                  sv[c + 1] = __float_as_uint(x1);
+                }
+              } else {
+#pragma unroll
+                for (int c = 0; c < 64; ++c)
+                  sv[c] = __float_as_uint(a.cap_out * tanh_acc(__uint_as_float(sv[c]) * a.cap_in));
+              }
+            } else {
+#pragma unroll
+              for (int c = 0; c < 64; ++c) sv[c] = __float_as_uint(__uint_as_float(sv[c]) * a.sl2);
+            }
+            if (a.slopes) {
+              const float p0 = (float)(pos - j0 - half * 64);
+#pragma unroll
+              for (int c = 0; c < 64; ++c)
+                sv[c] = __float_as_uint(fmaf(-slope, fabsf(p0 - (float)c), __uint_as_float(sv[c])));
+            }
+          }
+          if (!whole) {
+            if (!(alive = prepare_masks())) break;
+            const int lc = (flags & kOneDoc) && rec->doc != doc ? 0 : lim - j0 - half * 64;
+            if (__any_sync(0xffffffffu, lc < 64)) {
+#pragma unroll
+              for (int c = 0; c < 64; ++c)
+                if (c >= lc) sv[c] = __float_as_uint(-INFINITY);
+            }
+            if (a.k_pad && !(flags & kOneDoc)) {
+              const int32_t* sdoc = docs.get(r, alive) + half * 64;
+              if (!alive) break;
+#pragma unroll
+              for (int c = 0; c < 64; c += 4) {
+                const int4 d = *reinterpret_cast<const int4*>(sdoc + c);
+                if (d.x != doc) sv[c] = __float_as_uint(-INFINITY);
+                if (d.y != doc) sv[c + 1] = __float_as_uint(-INFINITY);
+                if (d.z != doc) sv[c + 2] = __float_as_uint(-INFINITY);
+                if (d.w != doc) sv[c + 3] = __float_as_uint(-INFINITY);
+              }
+            }
+          }
+          float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 64; c += 8) {
+            m0 = max3f(m0, __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
+            m1 = max3f(m1, __uint_as_float(sv[c + 2]), __uint_as_float(sv[c + 3]));
+            m2 = max3f(m2, __uint_as_float(sv[c + 4]), __uint_as_float(sv[c + 5]));
+            m3 = max3f(m3, __uint_as_float(sv[c + 6]), __uint_as_float(sv[c + 7]));
+          }
+          // the row's two halves share a maximum (two buffers: one barrier of the two warps per step)
+          m0 = max3f(m0, m1, fmaxf(m2, m3));
+          float* const sm = smax + (t & 1) * 2 * kTile;
+          sm[half * kTile + row] = m0;
+          asm volatile("bar.sync %0, 64;" ::"r"(1 + q4) : "memory");
+          const float m_new = fmaxf(m, fmaxf(m0, sm[(half ^ 1) * kTile + row]) * mul);
+          float alpha = 1.f;
+          bool rescale = false;
+          if (m == -INFINITY) {
+            m = m_new;  // nothing seen so far: O's row is zeros (or not written yet)
+          } else if (m_new > m + 8.f) {
+            alpha = fast_ex2(m - m_new);
+            l *= alpha;
+            m = m_new;
+            rescale = true;
+          }
+          const float base = m == -INFINITY ? 0.f : -m;  // a row without keys: exp2(-inf) = 0 throughout
+          uint32_t pk[32];
+          float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+#pragma unroll
+          for (int c = 0; c < 64; c += 4) {
+            float x0, x1, x2, x3;
+            fma2v(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1]), mul, mul, base, base, x0, x1);
+            fma2v(__uint_as_float(sv[c + 2]), __uint_as_float(sv[c + 3]), mul, mul, base, base, x2, x3);
+            x0 = fast_ex2(x0);
+            x1 = fast_ex2(x1);
+            x2 = fast_ex2(x2);
+            x3 = fast_ex2(x3);
+            add2(l0, l1, x0, x1, l0, l1);
+            add2(l2, l3, x2, x3, l2, l3);
+            pk[c / 2] = Elem<T>::pack(x0, x1);
+            pk[c / 2 + 1] = Elem<T>::pack(x2, x3);
+          }
+          l += (l0 + l1) + (l2 + l3);
+          // P and O are free once the previous product is done
+          if (!first && !(alive = mbar_wait_all(pv_done, (t - 1) & 1, abort_flag, a.err))) break;
+          tc_fence_after();
+          if (__any_sync(0xffffffffu, rescale)) {
+#pragma unroll 1
+            for (int c = 0; c < NB * 32; c += 32) {
+              uint32_t q[32];
+              tmem_ld_32x32b_x32(tOr + c, q);
+              tmem_ld_wait_regs(q);
+#pragma unroll
+              for (int y = 0; y < 32; ++y) q[y] = __float_as_uint(__uint_as_float(q[y]) * alpha);
+              tmem_st_x32(tOr + c, q);
+            }
+          }
+          tmem_st_x32(tPr, pk);
+          tmem_store_wait();
+          tc_fence_before();
+          mbar_arrive(p_full);
         }
-        if (valid && part && steps > 0) {
-          float4* p = reinterpret_cast<float4*>(a.partial + slot * a.D + c);
-#pragma unroll
-          for (int u = 0; u < 8; ++u)
-            if (c + 4 * u < a.D)
-              __stcg(p + u, make_float4(__uint_as_float(r[4 * u]), __uint_as_float(r[4 * u + 1]),
-                                        __uint_as_float(r[4 * u + 2]), __uint_as_float(r[4 * u + 3])));
-        } else if (valid && !part) {
-          // a row whose mask leaves nothing has l = 0 and gets zeros
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            if (c + 8 * u < a.D)
-              *reinterpret_cast<uint4*>(dst + c + 8 * u) = make_uint4(
-                  Elem<T>::pack(__uint_as_float(r[8 * u]) * inv, __uint_as_float(r[8 * u + 1]) * inv),
-                  Elem<T>::pack(__uint_as_float(r[8 * u + 2]) * inv, __uint_as_float(r[8 * u + 3]) * inv),
-                  Elem<T>::pack(__uint_as_float(r[8 * u + 4]) * inv, __uint_as_float(r[8 * u + 5]) * inv),
-                  Elem<T>::pack(__uint_as_float(r[8 * u + 6]) * inv, __uint_as_float(r[8 * u + 7]) * inv));
+        ++t;
+      }
+      if (flags & kLast) {
+        if (some && !(alive = mbar_wait_all(pv_done, (t - 1) & 1, abort_flag, a.err))) break;
+        tc_fence_after();
+        if (work) {
+          // the row sum of both halves
+          float* const sm = smax + (t & 1) * 2 * kTile;
+          sm[half * kTile + row] = l;
+          asm volatile("bar.sync %0, 64;" ::"r"(1 + q4) : "memory");
+          l += sm[(half ^ 1) * kTile + row];
+          asm volatile("bar.sync %0, 64;" ::"r"(1 + q4) : "memory");
+          store_rows<T, NB>(a, ((int64_t)rec->unit * a.splits + rec->z) * kTile + row, rec->b, rec->i0 + row_i,
+                            rec->head * a.G + row_h, half, tOr, some, valid, m, l);
         }
+        tc_fence_before();
       }
-      if (valid && part) {
-        a.partial_ml[slot * 2] = m;
-        a.partial_ml[slot * 2 + 1] = l;
-      } else if (valid && a.lse) {
-        a.lse[((int64_t)b * a.H + h) * a.Nq + i] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
-      }
+      ring.done(r);
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 5) tmem_dealloc(tmem, 256);
+  if (warp == 9) tmem_dealloc(tmem, 256);
 }
 
 // Joins the parts of split items, one warp per query row: m = max m_z, o = sum
@@ -477,24 +597,36 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ 
   if (lane == 0 && a.lse) a.lse[((int64_t)b * a.H + h) * a.Nq + i] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
 
-__global__ void __launch_bounds__(128) attn_doc_range_kernel(const int32_t* doc, int len, int tiles, int32_t* range) {
+// One warp per tile: the key tiles of all sequences, then the query tiles.
+struct DocArgs {
+  const int32_t* doc[2];
+  int32_t *range[2], *pad[2];
+  int32_t len[2], width[2], tiles[2];
+  int64_t total[2];
+};
+__global__ void __launch_bounds__(128) attn_doc_range_kernel(const __grid_constant__ DocArgs a) {
   pdl_wait();
   pdl_trigger();
-  const int64_t w = blockIdx.x * (int64_t)4 + (threadIdx.x >> 5);  // one warp per tile
-  const int lane = threadIdx.x & 31;
-  const int64_t b = w / tiles;
-  const int tile = (int)(w % tiles);
+  int64_t w = blockIdx.x * (int64_t)4 + (threadIdx.x >> 5);
+  const int set = w >= a.total[0];
+  if (set) w -= a.total[0];
+  if (w >= a.total[set]) return;
+  const int lane = threadIdx.x & 31, len = a.len[set], width = a.width[set];
+  const int64_t b = w / a.tiles[set];
+  const int tile = (int)(w % a.tiles[set]);
   int lo = INT32_MAX, hi = INT32_MIN;
-  for (int i = tile * kTile + lane; i < min(len, (tile + 1) * kTile); i += 32) {
-    const int d = doc[b * len + i];
+  const int row = (len + kTile - 1) / kTile * kTile;
+  for (int i = tile * width + lane; i < min(len, (tile + 1) * width); i += 32) {
+    const int d = a.doc[set][b * len + i];
     lo = min(lo, d);
     hi = max(hi, d);
+    a.pad[set][b * row + i] = d;
   }
   lo = __reduce_min_sync(0xffffffffu, lo);
   hi = __reduce_max_sync(0xffffffffu, hi);
   if (lane == 0) {
-    range[w * 2] = lo;
-    range[w * 2 + 1] = hi;
+    a.range[set][w * 2] = lo;
+    a.range[set][w * 2 + 1] = hi;
   }
 }
 
@@ -513,16 +645,47 @@ FwdPlan plan_forward(const sd_attention_cfg& c) {
   p.qtiles = (c.q_len + p.tq - 1) / p.tq;
   p.ktiles = tiles_of(c.k_len);
   p.items = (int64_t)c.batch * c.kv_heads * p.qtiles;
-  // split while it leaves every part two tiles and all parts fit on the GPU at once
-  int64_t s = std::min<int64_t>(std::min<int64_t>(kSlots / std::max<int64_t>(p.items, 1), p.ktiles / 2), kMaxSplits);
-  p.splits = (int)std::max<int64_t>(s, 1);
+  // Time in key tiles of one SM for 1, 2, ... splits of every item. Two CTAs share an SM
+  // and take turns (measured: 1.2 us a tile and SM at head_dim 64, 1.5 at 128, 0.8 more for
+  // capped or biased scores; a CTA alone needs 1.25 of that). Units start longest first, so
+  // the last ones end about half the longest unit's tiles after the average; parts cost
+  // one more launch and their FP32 rows, written and joined at 1.3 TB/s.
+  const double nq = c.q_len, nk = c.k_len;
+  const double seen = !c.causal ? 1.0 : nq <= nk ? 1.0 - nq / (2.0 * std::max(nk, 1.0)) : nk / (2.0 * nq);
+  const double total = (double)p.items * p.ktiles * seen / kSms;
+  const double tile_us = (c.head_dim <= 64 ? 1.2 : 1.5) + (c.softcap > 0.f ? 0.8 : 0.0);
+  const double rows = (double)c.batch * c.heads * nq;
+  double best = 0;
+  p.splits = 1;
+  for (int s = 1; s <= std::min(kMaxSplits, std::max(p.ktiles, 1)); ++s) {
+    // one more tile's time for beginning and ending a unit
+    const double units = (double)p.items * s, longest = 1 + (p.ktiles + s - 1) / s;
+    double t = units <= kSms ? 1.25 * longest : std::max(total + units / kSms + 0.5 * longest, 1.25 * longest);
+    if (s > 1) t += (3.0 + rows * s * (c.head_dim + 2) * 8.0 / 1.3e6) / tile_us;
+    if (s == 1 || t < best) {
+      best = t;
+      p.splits = s;
+    }
+    if (units > 16.0 * kSms) break;
+  }
   return p;
 }
 
-// Scratch after the header: document ranges of the key tiles and query tiles, then
-// the forward's parts or what the backward needs.
-size_t range_bytes(int batch, int len) { return up256((size_t)batch * tiles_of(len) * 8); }
-size_t ranges_bytes(const sd_attention_cfg& c) { return range_bytes(c.batch, c.k_len) + range_bytes(c.batch, c.q_len); }
+// Scratch after the header: the documents' ranges and padded rows, then the forward's
+// parts or what the backward needs.
+struct DocSpace {
+  size_t q_range, k_pad, q_pad, bytes;  // k_range comes first
+};
+DocSpace doc_space(const sd_attention_cfg& c) {
+  DocSpace s;
+  const size_t b = (size_t)c.batch;
+  s.q_range = up256(b * tiles_of(c.k_len) * 8);
+  s.k_pad = s.q_range + up256(b * std::max(plan_forward(c).qtiles, tiles_of(c.q_len)) * 8);
+  s.q_pad = s.k_pad + b * tiles_of(c.k_len) * kTile * 4;
+  s.bytes = s.q_pad + b * tiles_of(c.q_len) * kTile * 4;
+  return s;
+}
+size_t ranges_bytes(const sd_attention_cfg& c) { return doc_space(c).bytes; }
 size_t parts_bytes(const sd_attention_cfg& c) {
   const FwdPlan p = plan_forward(c);
   return p.splits > 1 ? up256((size_t)p.items * p.splits * kTile * (c.head_dim + 2) * 4) : 0;
@@ -588,11 +751,16 @@ sd_status forward(AttnCall& c, const FwdPlan& p) {
       !attn_map(&maps.k, f16, c.k, c.ks, g.batch, g.k_len, g.kv_heads, g.head_dim, 1, kTile) ||
       !attn_map(&maps.v, f16, c.v, c.vs, g.batch, g.k_len, g.kv_heads, g.head_dim, 1, kTile))
     return SD_ERR_LAUNCH;
-  OP_TRY((allow_smem<attn_fwd_kernel<T, NB>>(Shape<NB>::kSmem, c.dev.index)));
+  const bool shaped = a.cap_out != 0.f || a.slopes;
+  if (shaped)
+    OP_TRY((allow_smem<attn_fwd_kernel<T, NB, true>>(Shape<NB>::kSmem, c.dev.index)));
+  else
+    OP_TRY((allow_smem<attn_fwd_kernel<T, NB, false>>(Shape<NB>::kSmem, c.dev.index)));
+  auto* kernel = shaped ? attn_fwd_kernel<T, NB, true> : attn_fwd_kernel<T, NB, false>;
   const double pairs = (double)g.batch * g.heads * g.q_len * g.k_len;
   const double bytes = 2.0 * g.batch * g.head_dim * (2.0 * g.q_len * g.heads + 2.0 * g.k_len * g.kv_heads);
   sdp::Scope sc("attn_fwd", sdp::F_ATTN, 4.0 * pairs * g.head_dim, bytes, c.st, p.splits > 1 ? 2 : 1);
-  OP_TRY(launched(launch_pdl(attn_fwd_kernel<T, NB>, dim3((unsigned)(p.items * p.splits)), dim3(kThreads),
+  OP_TRY(launched(launch_pdl(kernel, dim3((unsigned)a.units), dim3(kThreads),
                              Shape<NB>::kSmem, c.st, maps, a)));
   if (p.splits == 1) return SD_OK;
   const int64_t rows = (int64_t)g.batch * g.heads * g.q_len;
@@ -609,12 +777,25 @@ bool attn_map(CUtensorMap* m, bool f16, const void* p, const int64_t* s, int bat
   return encode_map(m, f16, p, 4, dims, strides, box);
 }
 
-sd_status attn_doc_ranges(const int32_t* doc, int batch, int len, int32_t* range, cudaStream_t st) {
-  const int tiles = tiles_of(len);
-  const int64_t warps = (int64_t)batch * tiles;
-  sdp::Scope sc("attn_doc_range", sdp::F_OTHER, 0, 4.0 * batch * len, st);
-  return launched(launch_pdl(attn_doc_range_kernel, dim3((unsigned)((warps + 3) / 4)), dim3(128), 0, st, doc, len, tiles,
-                             range));
+sd_status attn_doc_ranges(const AttnArgs& a, int tq, cudaStream_t st) {
+  DocArgs d;
+  d.doc[0] = a.k_doc;
+  d.doc[1] = a.q_doc;
+  d.range[0] = const_cast<int32_t*>(a.k_range);
+  d.range[1] = const_cast<int32_t*>(a.q_range);
+  d.pad[0] = const_cast<int32_t*>(a.k_pad);
+  d.pad[1] = const_cast<int32_t*>(a.q_pad);
+  d.len[0] = a.Nk;
+  d.len[1] = a.Nq;
+  d.width[0] = kTile;
+  d.width[1] = tq;
+  for (int i = 0; i < 2; ++i) {
+    d.tiles[i] = std::max(1, (d.len[i] + d.width[i] - 1) / d.width[i]);
+    d.total[i] = d.len[i] ? (int64_t)a.B * d.tiles[i] : 0;
+  }
+  sdp::Scope sc("attn_doc_range", sdp::F_OTHER, 0, 4.0 * a.B * (a.Nk + a.Nq), st);
+  const int64_t warps = d.total[0] + d.total[1];
+  return launched(launch_pdl(attn_doc_range_kernel, dim3((unsigned)((warps + 3) / 4)), dim3(128), 0, st, d));
 }
 
 void attn_fill(AttnCall& c, const sd_attention_masks* m) {
@@ -645,8 +826,14 @@ void attn_fill(AttnCall& c, const sd_attention_masks* m) {
   for (int i = 0; i < 3; ++i) a.os[i] = c.os[i];
   a.ktiles = tiles_of(g.k_len);
   a.err = reinterpret_cast<int*>(c.ws);
-  a.k_range = a.k_doc ? reinterpret_cast<int32_t*>(c.ws + kOpHeader) : nullptr;
-  a.q_range = a.k_doc ? reinterpret_cast<int32_t*>(c.ws + kOpHeader + range_bytes(g.batch, g.k_len)) : nullptr;
+  if (a.k_doc) {
+    const DocSpace d = doc_space(g);
+    uint8_t* w = c.ws + kOpHeader;
+    a.k_range = reinterpret_cast<int32_t*>(w);
+    a.q_range = reinterpret_cast<int32_t*>(w + d.q_range);
+    a.k_pad = reinterpret_cast<int32_t*>(w + d.k_pad);
+    a.q_pad = reinterpret_cast<int32_t*>(w + d.q_pad);
+  }
 }
 
 }  // namespace sdo
@@ -690,6 +877,7 @@ sd_status sd_attention_fwd(const sd_attention_cfg* cfg, const void* q, const voi
   a.tq = p.tq;
   a.qtiles = p.qtiles;
   a.splits = p.splits;
+  a.units = (int32_t)(p.items * p.splits);
   a.o = o;
   a.lse = lse;
   a.clear_err = 1;
@@ -701,7 +889,7 @@ sd_status sd_attention_fwd(const sd_attention_cfg* cfg, const void* q, const voi
     shaped.k_len = 1;  // a map has no empty dimension; no tile of it is visited
     c.cfg = &shaped;
   }
-  if (a.k_doc) OP_TRY(attn_doc_ranges(a.k_doc, cfg->batch, cfg->k_len, const_cast<int32_t*>(a.k_range), c.st));
+  if (a.k_doc) OP_TRY(attn_doc_ranges(a, p.tq, c.st));
   const bool wide = cfg->head_dim > 64;
   if (cfg->dtype == SD_DTYPE_F16) return wide ? forward<__half, 2>(c, p) : forward<__half, 1>(c, p);
   return wide ? forward<__nv_bfloat16, 2>(c, p) : forward<__nv_bfloat16, 1>(c, p);

@@ -6,10 +6,15 @@
 //   dx = rstd * (u - mean(u) - xh * mean(u * xh)).
 //
 // Bound by memory: forward reads x and writes y, backward reads x and dy and
-// writes dx. Both run as two kernels: the first sums over a share of an
-// image's rows per CTA, the second combines the shares in a fixed order (so
-// results repeat bit for bit) and walks the same rows from their end, so that it
-// finds the rows that the first one read last still in L2.
+// writes dx. Groups are independent, so an image's channels are cut into slices of
+// whole groups, and a thread block cluster takes one slice of one image:
+//   gn_cluster_fwd / _bwd_kernel  where the slice (of x, or of x and dy) fits into the
+//       shared memory of up to eight CTAs: read once, summed, the sums joined
+//       through distributed shared memory, normalised from shared memory
+//   otherwise two kernels: the first sums over a share of an image's rows per CTA,
+//       the second joins the shares and walks the same rows from their end, so that
+//       it finds the rows that the first one read last still in L2
+// Sums are joined in a fixed order, so results repeat bit for bit.
 //
 // A thread owns one 16-byte vector of channels for all its rows (channel terms
 // stay in registers, a warp reads whole sectors whatever C/G is); sums are FP32
@@ -18,16 +23,22 @@
 // costs no precision.
 #include <string.h>
 
+#include <algorithm>
+#include <numeric>
+
 #include "op_common.cuh"
 #include "profile.h"
 
 namespace sdo {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 constexpr int kMaxChannels = 8192;  // per-channel sums of a CTA: 64 KB of shared memory
-constexpr int kMaxChunks = 256;     // shares of one image
-constexpr int kTargetCtas = 592;    // four CTAs for each of 148 SMs
+constexpr int kMaxChunks = 320;     // shares of one image (two CTAs for each of 148 SMs, and some)
+constexpr int kTargetCtas = 296;
+constexpr int kSms = 148;
+constexpr int kMaxCluster = 8;
+constexpr size_t kClusterSmem = 220 * 1024;
 
 struct GnArgs {
   const void *x, *gamma, *beta, *dy;
@@ -37,44 +48,108 @@ struct GnArgs {
   float *pg, *pc;  // shares: per group [batch][chunks][G][2], per channel [batch][chunks][2][C]
   int64_t rows, chunk_rows, ldx, ldy;
   int32_t batch, C, G, cpg, act, chunks;
+  int32_t slices, width;  // cluster kernels: slices of an image, channels of one
   float eps;
   int* err;  // cleared by the first kernel of a call (none of them waits)
 };
 
 struct Plan {
+  bool cluster[2];  // forward, backward
+  int ctas[2], width[2];
+  int64_t cta_rows[2];
   int chunks;
   int64_t chunk_rows;
   size_t pg_floats, pc_floats;
 };
 
+// Shared memory of a cluster kernel: `tensors` vectors per thread and row pass, the
+// row threads' sums, per-channel sums, per-group results (two buffers).
+size_t cluster_smem(int width, int groups, int vec, int64_t cta_rows, int tensors) {
+  const int cols = width / vec, rows_t = kThreads / cols;
+  const int64_t iters = (cta_rows + rows_t - 1) / rows_t;
+  if (iters > 64) return SIZE_MAX;
+  return (size_t)iters * kThreads * 16 * tensors + (size_t)2 * vec * kThreads * 4 + (size_t)2 * width * 4 +
+         (size_t)4 * groups * 4;
+}
+
 Plan make_plan(const sd_group_norm_cfg& c) {
   Plan p;
-  // enough CTAs to fill the GPU, at least 16 rows in each
+  memset(&p, 0, sizeof(p));
+  const int vec = c.dtype == SD_DTYPE_F32 ? 4 : 8, size = 16 / vec;
+  const int cpg = c.channels / c.groups;
+  const bool wide = c.channels % vec == 0 && c.ld_x % vec == 0 && c.ld_y % vec == 0;
+  const int unit = std::lcm(cpg, vec);  // narrowest slice of whole groups and whole vectors
+  for (int back = 0; back < 2 && wide && c.channels % unit == 0; ++back) {
+    const int n = c.channels / unit;
+    double best = 0;
+    for (int k = 1; k <= n; ++k) {
+      if (n % k) continue;
+      const int width = unit * k, cols = width / vec;
+      // slices of 64 bytes and more: narrower ones waste parts of sectors
+      if (cols > kThreads || (width * size < 64 && k < n)) continue;
+      const int rows_t = kThreads / cols;
+      for (int ctas = 1; ctas <= kMaxCluster; ctas *= 2) {
+        const int64_t rows = (c.rows + ctas - 1) / ctas;
+        if (ctas > 1 && rows < rows_t) break;
+        if (cluster_smem(width, width / cpg, vec, rows, 1 + back) > kClusterSmem) continue;
+        // passes over a thread's rows in all waves, and about four passes' worth of
+        // latency for the sums and the cluster's two barriers per wave
+        const int64_t total = (int64_t)c.batch * (n / k) * ctas;
+        const double cost = (double)((total + kSms - 1) / kSms) * ((rows + rows_t - 1) / rows_t + 4.0);
+        if (!p.cluster[back] || cost < best) {
+          best = cost;
+          p.cluster[back] = true;
+          p.ctas[back] = ctas;
+          p.width[back] = width;
+          p.cta_rows[back] = rows;
+        }
+      }
+    }
+    // A whole image in few CTAs (long rows, wide groups) leaves most of the GPU idle:
+    // then the two kernels' second read costs less.
+    if (p.cluster[back]) {
+      const int64_t total = (int64_t)c.batch * (c.channels / p.width[back]) * p.ctas[back];
+      const int64_t vecs = (int64_t)c.batch * c.rows * (c.channels / vec);
+      if (total * 3 < kSms && vecs > (int64_t)kThreads * kSms) p.cluster[back] = false;
+    }
+  }
+  // two CTAs per SM in all, four rows or more for each thread
+  const int cols = std::max(1, std::min(kThreads, c.channels / (wide ? vec : 1)));
+  const int64_t least = 4 * (int64_t)(kThreads / cols);
   int64_t n = (kTargetCtas + c.batch - 1) / c.batch;
-  if (n > kMaxChunks) n = kMaxChunks;
-  if (n > (c.rows + 15) / 16) n = (c.rows + 15) / 16;
-  if (n < 1) n = 1;
+  n = std::min<int64_t>(std::min<int64_t>(n, kMaxChunks), (c.rows + least - 1) / least);
+  n = std::max<int64_t>(n, 1);
   p.chunk_rows = (c.rows + n - 1) / n;
   p.chunks = (int)((c.rows + p.chunk_rows - 1) / p.chunk_rows);
-  p.pg_floats = (size_t)c.batch * p.chunks * c.groups * 2;
-  p.pc_floats = (size_t)c.batch * p.chunks * c.channels * 2;
+  p.pg_floats = p.cluster[0] && p.cluster[1] ? 0 : (size_t)c.batch * p.chunks * c.groups * 2;
+  p.pc_floats = (size_t)c.batch * (p.cluster[1] ? 1 : p.chunks) * c.channels * 2;
   return p;
 }
 
-template <typename T, int V>
-struct Row {
-  uint4 raw;
-  float f[V];
-};
-
 // V channels at p (16-byte aligned when V > 1).
 template <typename T, int V>
-__device__ __forceinline__ void load_v(const T* p, float (&f)[V]) {
-  if constexpr (V == 1) {
-    f[0] = Elem<T>::to_f(*p);
-  } else {
-    unpack_vec<T, V>(*reinterpret_cast<const uint4*>(p), f);
-  }
+struct Raw {
+  uint4 v;
+};
+template <typename T>
+struct Raw<T, 1> {
+  T v;
+};
+template <typename T, int V>
+__device__ __forceinline__ Raw<T, V> load_raw(const T* p) {
+  Raw<T, V> r;
+  if constexpr (V == 1)
+    r.v = *p;
+  else
+    r.v = *reinterpret_cast<const uint4*>(p);
+  return r;
+}
+template <typename T, int V>
+__device__ __forceinline__ void to_float(const Raw<T, V>& r, float (&f)[V]) {
+  if constexpr (V == 1)
+    f[0] = Elem<T>::to_f(r.v);
+  else
+    unpack_vec<T, V>(r.v, f);
 }
 template <typename T, int V>
 __device__ __forceinline__ void store_v(T* p, const float (&f)[V]) {
@@ -88,6 +163,114 @@ __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
+}
+
+// Pairwise arithmetic on V channels (packed FP32 for even V).
+template <int V>
+__device__ __forceinline__ void v_add(const float (&x)[V], const float (&y)[V], float (&o)[V]) {
+  if constexpr (V % 2) {
+    o[0] = x[0] + y[0];
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; j += 2) add2(x[j], x[j + 1], y[j], y[j + 1], o[j], o[j + 1]);
+  }
+}
+template <int V>
+__device__ __forceinline__ void v_mul(const float (&x)[V], const float (&y)[V], float (&o)[V]) {
+  if constexpr (V % 2) {
+    o[0] = x[0] * y[0];
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; j += 2) mul2(x[j], x[j + 1], y[j], y[j + 1], o[j], o[j + 1]);
+  }
+}
+template <int V>
+__device__ __forceinline__ void v_fma(const float (&x)[V], const float (&y)[V], const float (&z)[V], float (&o)[V]) {
+  if constexpr (V % 2) {
+    o[0] = fmaf(x[0], y[0], z[0]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; j += 2) fma2v(x[j], x[j + 1], y[j], y[j + 1], z[j], z[j + 1], o[j], o[j + 1]);
+  }
+}
+
+// Per-channel terms of the V channels a thread owns: z = (x + nm) * sc + be, where
+// nm = -mean and sc = rstd * gamma.
+template <int V>
+struct Cols {
+  float nm[V], sc[V], be[V];
+};
+template <typename T, int V>
+__device__ __forceinline__ void load_affine(const GnArgs& a, int c, Cols<V>& t) {
+  const T *gamma = static_cast<const T*>(a.gamma), *beta = static_cast<const T*>(a.beta);
+#pragma unroll
+  for (int j = 0; j < V; ++j) t.sc[j] = 1.f, t.be[j] = 0.f;
+  if (gamma) to_float<T, V>(load_raw<T, V>(gamma + c), t.sc);
+  if (beta) to_float<T, V>(load_raw<T, V>(beta + c), t.be);
+}
+// The first group of a thread's V channels and, where groups are narrower than the
+// vector, each channel's own: one division per thread.
+struct Groups {
+  int g, left, cpg;  // group of the next channel, channels of it left
+  __device__ __forceinline__ Groups(int c, int per) : g(c / per), left(per - c % per), cpg(per) {}
+  __device__ __forceinline__ int next() {
+    const int r = g;
+    if (--left == 0) {
+      ++g;
+      left = cpg;
+    }
+    return r;
+  }
+};
+// Takes mean and rstd pairs of the channels' groups into
+// the terms; rs receives rstd.
+template <int V>
+__device__ __forceinline__ void add_stats(const float* st, int c, int cpg, Cols<V>& t, float (&rs)[V]) {
+  Groups gr(c, cpg);
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int g = gr.next();
+    t.nm[j] = -st[2 * g];
+    rs[j] = st[2 * g + 1];
+    t.sc[j] *= rs[j];
+  }
+}
+template <int V>
+__device__ __forceinline__ void normalise(const Cols<V>& t, float (&f)[V], int act) {
+  v_add<V>(f, t.nm, f);
+  v_fma<V>(f, t.sc, t.be, f);
+  act_vec<V>(f, act);
+}
+// f = x -> x - mean, d = dy -> dz
+template <int V>
+__device__ __forceinline__ void grad_terms(const Cols<V>& t, float (&f)[V], float (&d)[V], int act) {
+  v_add<V>(f, t.nm, f);
+  if (act != SD_ACT_NONE) {
+    float z[V], a[V];
+    v_fma<V>(f, t.sc, t.be, z);
+    act_grad_vec<V>(z, d, a, act);
+  }
+}
+// dx = rstd (gamma dz - m1 - xh m2) = sc dz + b2 (x - mean) + b1
+template <int V>
+struct GradCols {
+  float b1[V], b2[V];
+};
+template <int V>
+__device__ __forceinline__ void grad_cols(const float* mu, int c, int cpg, const float (&rs)[V],
+                                          GradCols<V>& o) {
+  Groups gr(c, cpg);
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int g = gr.next();
+    o.b1[j] = -rs[j] * mu[2 * g];
+    o.b2[j] = -rs[j] * rs[j] * mu[2 * g + 1];
+  }
+}
+template <int V>
+__device__ __forceinline__ void grad_out(const Cols<V>& t, const GradCols<V>& k, float (&f)[V], const float (&d)[V]) {
+  v_fma<V>(f, k.b2, k.b1, f);
+  v_fma<V>(d, t.sc, f, f);
 }
 
 // Adds the per-thread sums s0, s1 of V channels over the CTA's row threads, in
@@ -107,14 +290,312 @@ __device__ __forceinline__ void reduce_rows(float* red, float* ch, int C, int c_
   for (int i = threadIdx.x; i < 2 * V * cols_t; i += kThreads) {
     const int j = i / cols_t, t = i % cols_t;
     float a = 0.f;
+#pragma unroll 8
     for (int y = 0; y < rows_t; ++y) a += red[(y * 2 * V + j) * cols_t + t];
     ch[(j >= V ? C : 0) + c_first + t * V + (j >= V ? j - V : j)] = a;
   }
 }
 
+// ------------------------------------------------------------------ one slice per cluster
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// p[i] of CTA `rank` of the cluster
+__device__ __forceinline__ float peer_float(const float* p, uint32_t rank) {
+  uint32_t a;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+
+struct Slice {
+  int64_t n, r0, r1;
+  int c0, tx, ty, cols, rows_t;
+  bool active;
+};
+__device__ __forceinline__ Slice my_slice(const GnArgs& a, int vec, uint32_t rank, uint32_t ctas) {
+  Slice s;
+  const int64_t cl = blockIdx.x / ctas;
+  s.n = cl / a.slices;
+  s.c0 = (int)(cl % a.slices) * a.width;
+  s.r0 = min(a.rows, rank * a.chunk_rows);
+  s.r1 = min(a.rows, s.r0 + a.chunk_rows);
+  s.cols = a.width / vec;
+  s.rows_t = kThreads / s.cols;
+  s.tx = threadIdx.x % s.cols;
+  s.ty = threadIdx.x / s.cols;
+  s.active = s.ty < s.rows_t;
+  return s;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) gn_cluster_fwd_kernel(const __grid_constant__ GnArgs a) {
+  constexpr int V = kVec<T>;
+  extern __shared__ __align__(16) uint8_t smem[];
+  const uint32_t rank = cluster_rank(), ctas = cluster_size();
+  const Slice s = my_slice(a, V, rank, ctas);
+  const int iters = (int)((a.chunk_rows + s.rows_t - 1) / s.rows_t), groups = a.width / a.cpg;
+  uint4* tile = reinterpret_cast<uint4*>(smem);                       // [iters][threads]
+  float* red = reinterpret_cast<float*>(tile + (size_t)iters * kThreads);
+  float* ch = red + 2 * V * kThreads;                                 // [2][width]
+  float* part = ch + 2 * a.width;                                     // [groups][2] mean, squared deviations
+  float* res = part + 2 * groups;                                     // [groups][2] mean, rstd
+  const int c = s.c0 + s.tx * V;
+  Cols<V> t;
+  pdl_wait();
+  pdl_trigger();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.err = 0;
+  const T* x = static_cast<const T*>(a.x) + s.n * a.rows * a.ldx;
+  const T* first = x + s.r0 * a.ldx + s.c0;
+  const bool some = s.r0 < s.r1;
+  if (s.active) load_affine<T, V>(a, c, t);
+  float k[V], s0[V], s1[V];
+  Groups gk(s.tx * V, a.cpg);
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int g = gk.next();
+    k[j] = some && s.active ? -Elem<T>::to_f(first[g * a.cpg]) : 0.f;
+    s0[j] = s1[j] = 0.f;
+  }
+  if (s.active) {
+    const T* p = x + c;
+    constexpr int U = 4;
+    int it = 0;
+    for (int64_t r = s.r0 + s.ty; r < s.r1; r += U * s.rows_t, it += U) {
+      uint4 raw[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (r + u * s.rows_t < s.r1) raw[u] = *reinterpret_cast<const uint4*>(p + (r + u * s.rows_t) * a.ldx);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (r + u * s.rows_t >= s.r1) break;
+        tile[(it + u) * kThreads + threadIdx.x] = raw[u];
+        float f[V];
+        unpack_vec<T, V>(raw[u], f);
+        v_add<V>(f, k, f);
+        v_add<V>(s0, f, s0);
+        v_fma<V>(f, f, s1, s1);
+      }
+    }
+  }
+  reduce_rows<V>(red, ch, a.width, 0, s.tx, s.ty, s.cols, s.rows_t, s.active, s0, s1);
+  __syncthreads();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int g = warp; g < groups; g += kThreads / 32) {
+    float sum = 0.f, sq = 0.f;
+    for (int i = lane; i < a.cpg; i += 32) {
+      sum += ch[g * a.cpg + i];
+      sq += ch[a.width + g * a.cpg + i];
+    }
+    sum = warp_sum(sum);
+    sq = warp_sum(sq);
+    if (lane == 0) {
+      const float d = some ? sum / ((float)(s.r1 - s.r0) * a.cpg) : 0.f;
+      part[2 * g] = (some ? Elem<T>::to_f(first[g * a.cpg]) : 0.f) + d;
+      part[2 * g + 1] = fmaxf(sq - sum * d, 0.f);
+    }
+  }
+  cluster_sync();
+  for (int g = threadIdx.x; g < groups; g += kThreads) {
+    float m = 0.f, q = 0.f;
+    float pm[kMaxCluster], w[kMaxCluster];
+#pragma unroll
+    for (int i = 0; i < kMaxCluster; ++i) {
+      pm[i] = w[i] = 0.f;
+      if (i < (int)ctas) {
+        const int64_t lo = min(a.rows, i * a.chunk_rows), hi = min(a.rows, lo + a.chunk_rows);
+        w[i] = (float)(hi - lo) / (float)a.rows;
+        pm[i] = peer_float(part + 2 * g, i);
+        q += peer_float(part + 2 * g + 1, i);
+        m += w[i] * pm[i];
+      }
+    }
+    q /= (float)a.rows * a.cpg;
+#pragma unroll
+    for (int i = 0; i < kMaxCluster; ++i) q += w[i] * (pm[i] - m) * (pm[i] - m);
+    const float rstd = 1.f / sqrtf(q + a.eps);
+    res[2 * g] = m;
+    res[2 * g + 1] = rstd;
+    if (a.stats && rank == 0) {
+      float* o = a.stats + (s.n * a.G + s.c0 / a.cpg + g) * 2;
+      o[0] = m;
+      o[1] = rstd;
+    }
+  }
+  __syncthreads();
+  if (s.active) {
+    float rs[V];
+    add_stats<V>(res, s.tx * V, a.cpg, t, rs);
+    T* y = static_cast<T*>(a.out) + s.n * a.rows * a.ldy + c;
+    int it = 0;
+#pragma unroll 2
+    for (int64_t r = s.r0 + s.ty; r < s.r1; r += s.rows_t, ++it) {
+      float f[V];
+      unpack_vec<T, V>(tile[it * kThreads + threadIdx.x], f);
+      normalise<V>(t, f, a.act);
+      *reinterpret_cast<uint4*>(y + r * a.ldy) = pack_vec<T, V>(f);
+    }
+  }
+  cluster_sync();  // a CTA's sums stay readable until all have read them
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) gn_cluster_bwd_kernel(const __grid_constant__ GnArgs a) {
+  constexpr int V = kVec<T>;
+  extern __shared__ __align__(16) uint8_t smem[];
+  const uint32_t rank = cluster_rank(), ctas = cluster_size();
+  const Slice s = my_slice(a, V, rank, ctas);
+  const int iters = (int)((a.chunk_rows + s.rows_t - 1) / s.rows_t), groups = a.width / a.cpg;
+  uint4* tx_ = reinterpret_cast<uint4*>(smem);           // [iters][threads] x
+  uint4* td = tx_ + (size_t)iters * kThreads;            // dy
+  float* red = reinterpret_cast<float*>(td + (size_t)iters * kThreads);
+  float* ch = red + 2 * V * kThreads;                    // [2][width] sum dz, sum dz * xh of this CTA
+  float* part = ch + 2 * a.width;                        // [groups][2] the same weighted by gamma
+  float* res = part + 2 * groups;                        // [groups][2] mean(u), mean(u * xh)
+  const int c = s.c0 + s.tx * V;
+  pdl_wait();
+  pdl_trigger();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.err = 0;
+  const T* x = static_cast<const T*>(a.x) + s.n * a.rows * a.ldx + c;
+  const T* dy = static_cast<const T*>(a.dy) + s.n * a.rows * a.ldy + c;
+  const T* gamma = static_cast<const T*>(a.gamma);
+  Cols<V> t;
+  float s0[V], s1[V], rs[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) s0[j] = s1[j] = rs[j] = 0.f;
+  if (s.active) {
+    load_affine<T, V>(a, c, t);
+    add_stats<V>(a.stats + s.n * a.G * 2, c, a.cpg, t, rs);
+    constexpr int U = 2;
+    int it = 0;
+    for (int64_t r = s.r0 + s.ty; r < s.r1; r += U * s.rows_t, it += U) {
+      uint4 rx[U], rd[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (r + u * s.rows_t < s.r1) {
+          rx[u] = *reinterpret_cast<const uint4*>(x + (r + u * s.rows_t) * a.ldx);
+          rd[u] = *reinterpret_cast<const uint4*>(dy + (r + u * s.rows_t) * a.ldy);
+        }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (r + u * s.rows_t >= s.r1) break;
+        tx_[(it + u) * kThreads + threadIdx.x] = rx[u];
+        td[(it + u) * kThreads + threadIdx.x] = rd[u];
+        float f[V], d[V];
+        unpack_vec<T, V>(rx[u], f);
+        unpack_vec<T, V>(rd[u], d);
+        grad_terms<V>(t, f, d, a.act);
+        v_add<V>(s0, d, s0);
+        v_fma<V>(d, f, s1, s1);
+      }
+    }
+  }
+  v_mul<V>(s1, rs, s1);  // sum dz (x - mean) -> sum dz * xh
+  reduce_rows<V>(red, ch, a.width, 0, s.tx, s.ty, s.cols, s.rows_t, s.active, s0, s1);
+  __syncthreads();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int g = warp; g < groups; g += kThreads / 32) {
+    float sum = 0.f, q = 0.f;
+    for (int i = lane; i < a.cpg; i += 32) {
+      const int cc = g * a.cpg + i;
+      const float w = gamma ? Elem<T>::to_f(gamma[s.c0 + cc]) : 1.f;
+      sum += w * ch[cc];
+      q += w * ch[a.width + cc];
+    }
+    sum = warp_sum(sum);
+    q = warp_sum(q);
+    if (lane == 0) {
+      part[2 * g] = sum;
+      part[2 * g + 1] = q;
+    }
+  }
+  cluster_sync();
+  const float inv = 1.f / ((float)a.rows * a.cpg);
+  for (int i = threadIdx.x; i < 2 * groups; i += kThreads) {
+    float v = 0.f;
+    for (uint32_t k = 0; k < ctas; ++k) v += peer_float(part + i, k);
+    res[i] = v * inv;
+  }
+  if (a.dgamma || a.dbeta) {
+    // the image's channel sums, a share of the channels per CTA; of several images they
+    // are joined by a kernel of their own
+    for (int i = rank * kThreads + threadIdx.x; i < 2 * a.width; i += ctas * kThreads) {
+      float v = 0.f;
+      for (uint32_t k = 0; k < ctas; ++k) v += peer_float(ch + i, k);
+      const bool second = i >= a.width;
+      const int cc = s.c0 + (second ? i - a.width : i);
+      if (a.batch > 1)
+        a.pc[(s.n * 2 + second) * a.C + cc] = v;
+      else if (float* o = second ? a.dgamma : a.dbeta)
+        o[cc] = v;
+    }
+  }
+  __syncthreads();
+  if (s.active) {
+    GradCols<V> k;
+    grad_cols<V>(res, s.tx * V, a.cpg, rs, k);
+    T* dx = static_cast<T*>(a.out) + s.n * a.rows * a.ldx + c;
+    int it = 0;
+#pragma unroll 2
+    for (int64_t r = s.r0 + s.ty; r < s.r1; r += s.rows_t, ++it) {
+      float f[V], d[V];
+      unpack_vec<T, V>(tx_[it * kThreads + threadIdx.x], f);
+      unpack_vec<T, V>(td[it * kThreads + threadIdx.x], d);
+      grad_terms<V>(t, f, d, a.act);
+      grad_out<V>(t, k, f, d);
+      *reinterpret_cast<uint4*>(dx + r * a.ldx) = pack_vec<T, V>(f);
+    }
+  }
+  cluster_sync();  // a CTA's sums stay readable until all have read them
+}
+
+// dgamma and dbeta from per-channel parts [parts][2][C], 32 channels per CTA.
+__device__ __forceinline__ void join_params(const GnArgs& a, int64_t parts, int block) {
+  __shared__ float part[2][kThreads];
+  const int c = block * 32 + (threadIdx.x & 31), slice = threadIdx.x >> 5;
+  float s = 0.f, q = 0.f;
+  if (c < a.C) {
+#pragma unroll 4
+    for (int64_t p = slice; p < parts; p += kThreads / 32) {
+      s += a.pc[p * 2 * a.C + c];
+      q += a.pc[p * 2 * a.C + a.C + c];
+    }
+  }
+  part[0][threadIdx.x] = s;
+  part[1][threadIdx.x] = q;
+  __syncthreads();
+  if (slice == 0 && c < a.C) {
+    for (int i = 1; i < kThreads / 32; ++i) {
+      s += part[0][i * 32 + threadIdx.x];
+      q += part[1][i * 32 + threadIdx.x];
+    }
+    if (a.dbeta) a.dbeta[c] = s;
+    if (a.dgamma) a.dgamma[c] = q;
+  }
+}
+__global__ void __launch_bounds__(kThreads) gn_param_join_kernel(const __grid_constant__ GnArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  join_params(a, a.batch, blockIdx.x);
+}
+
+// ------------------------------------------------------------------ two kernels
+
 // Shares of the forward statistics: (mean, sum of squared deviations) per group.
 template <typename T, int V>
-__global__ void __launch_bounds__(kThreads) gn_stats_share_kernel(const __grid_constant__ GnArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) gn_stats_share_kernel(const __grid_constant__ GnArgs a) {
   extern __shared__ float ch[];  // [2][C]
   __shared__ float red[2 * V * kThreads];
   pdl_wait();
@@ -132,24 +613,32 @@ __global__ void __launch_bounds__(kThreads) gn_stats_share_kernel(const __grid_c
     const bool active = ty < rows_t;
     const int c = (c0 + tx) * V;
     float k[V], s0[V], s1[V];
+    Groups gk(c, a.cpg);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      k[j] = Elem<T>::to_f(first[(c + j) / a.cpg * a.cpg]);
+      const int g = gk.next();
+      k[j] = active ? -Elem<T>::to_f(first[g * a.cpg]) : 0.f;
       s0[j] = s1[j] = 0.f;
     }
     if (active) {
+      constexpr int U = 8;
       const T* p = x + c;
-#pragma unroll 4
-      for (int64_t r = r0 + ty; r < r1; r += rows_t) {
+      int64_t r = r0 + ty;
+      auto add = [&](const Raw<T, V>& raw) {
         float f[V];
-        load_v<T, V>(p + r * a.ldx, f);
+        to_float<T, V>(raw, f);
+        v_add<V>(f, k, f);
+        v_add<V>(s0, f, s0);
+        v_fma<V>(f, f, s1, s1);
+      };
+      for (; r + (U - 1) * rows_t < r1; r += U * rows_t) {
+        Raw<T, V> raw[U];
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const float d = f[j] - k[j];
-          s0[j] += d;
-          s1[j] = fmaf(d, d, s1[j]);
-        }
+        for (int u = 0; u < U; ++u) raw[u] = load_raw<T, V>(p + (r + u * rows_t) * a.ldx);
+#pragma unroll
+        for (int u = 0; u < U; ++u) add(raw[u]);
       }
+      for (; r < r1; r += rows_t) add(load_raw<T, V>(p + r * a.ldx));
     }
     reduce_rows<V>(red, ch, a.C, c0 * V, tx, ty, cols_t, rows_t, active, s0, s1);
   }
@@ -175,7 +664,7 @@ __global__ void __launch_bounds__(kThreads) gn_stats_share_kernel(const __grid_c
 
 // y = act(z) from the joined shares; each CTA joins its image's shares itself.
 template <typename T, int V>
-__global__ void __launch_bounds__(kThreads) gn_apply_kernel(const __grid_constant__ GnArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) gn_apply_kernel(const __grid_constant__ GnArgs a) {
   extern __shared__ float gs[];  // [G][2] mean, rstd
   pdl_wait();
   pdl_trigger();
@@ -216,27 +705,36 @@ __global__ void __launch_bounds__(kThreads) gn_apply_kernel(const __grid_constan
   const int64_t r0 = chunk * a.chunk_rows, r1 = min(a.rows, r0 + a.chunk_rows);
   const T* x = static_cast<const T*>(a.x) + n * a.rows * a.ldx;
   T* y = static_cast<T*>(a.out) + n * a.rows * a.ldy;
-  const T *gamma = static_cast<const T*>(a.gamma), *beta = static_cast<const T*>(a.beta);
   const int cols = a.C / V;
   for (int c0 = 0; c0 < cols; c0 += kThreads) {
     const int cols_t = min(kThreads, cols - c0), rows_t = kThreads / cols_t;
     const int tx = threadIdx.x % cols_t, ty = threadIdx.x / cols_t;
     if (ty >= rows_t) continue;
     const int c = (c0 + tx) * V;
-    float m[V], sc[V], sh[V];
+    Cols<V> t;
+    float rs[V];
+    load_affine<T, V>(a, c, t);
+    add_stats<V>(gs, c, a.cpg, t, rs);
+    // several rows are read before the first is written: y may be x, so the compiler
+    // would not move a read across a write
+    constexpr int U = 4;
+    int64_t r = r1 - 1 - ty;
+    for (; r - (U - 1) * rows_t >= r0; r -= U * rows_t) {
+      Raw<T, V> raw[U];
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int g = (c + j) / a.cpg;
-      m[j] = gs[2 * g];
-      sc[j] = gs[2 * g + 1] * (gamma ? Elem<T>::to_f(gamma[c + j]) : 1.f);
-      sh[j] = beta ? Elem<T>::to_f(beta[c + j]) : 0.f;
+      for (int u = 0; u < U; ++u) raw[u] = load_raw<T, V>(x + (r - u * rows_t) * a.ldx + c);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float f[V];
+        to_float<T, V>(raw[u], f);
+        normalise<V>(t, f, a.act);
+        store_v<T, V>(y + (r - u * rows_t) * a.ldy + c, f);
+      }
     }
-#pragma unroll 4
-    for (int64_t r = r1 - 1 - ty; r >= r0; r -= rows_t) {
+    for (; r >= r0; r -= rows_t) {
       float f[V];
-      load_v<T, V>(x + r * a.ldx + c, f);
-#pragma unroll
-      for (int j = 0; j < V; ++j) f[j] = act_f(fmaf(f[j] - m[j], sc[j], sh[j]), a.act);
+      to_float<T, V>(load_raw<T, V>(x + r * a.ldx + c), f);
+      normalise<V>(t, f, a.act);
       store_v<T, V>(y + r * a.ldy + c, f);
     }
   }
@@ -256,7 +754,7 @@ __global__ void __launch_bounds__(kThreads) gn_grad_share_kernel(const __grid_co
   const int64_t r0 = chunk * a.chunk_rows, r1 = min(a.rows, r0 + a.chunk_rows);
   const T* x = static_cast<const T*>(a.x) + n * a.rows * a.ldx;
   const T* dy = static_cast<const T*>(a.dy) + n * a.rows * a.ldy;
-  const T *gamma = static_cast<const T*>(a.gamma), *beta = static_cast<const T*>(a.beta);
+  const T* gamma = static_cast<const T*>(a.gamma);
   const float* stats = a.stats + n * a.G * 2;
   const int cols = a.C / V;
   for (int c0 = 0; c0 < cols; c0 += kThreads) {
@@ -264,32 +762,36 @@ __global__ void __launch_bounds__(kThreads) gn_grad_share_kernel(const __grid_co
     const int tx = threadIdx.x % cols_t, ty = threadIdx.x / cols_t;
     const bool active = ty < rows_t;
     const int c = (c0 + tx) * V;
-    float m[V], rs[V], ga[V], be[V], s0[V], s1[V];
+    float s0[V], s1[V];
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int g = (c + j) / a.cpg;
-      m[j] = stats[2 * g];
-      rs[j] = stats[2 * g + 1];
-      ga[j] = gamma ? Elem<T>::to_f(gamma[c + j]) : 1.f;
-      be[j] = beta ? Elem<T>::to_f(beta[c + j]) : 0.f;
-      s0[j] = s1[j] = 0.f;
-    }
+    for (int j = 0; j < V; ++j) s0[j] = s1[j] = 0.f;
     if (active) {
-#pragma unroll 2
-      for (int64_t r = r0 + ty; r < r1; r += rows_t) {
+      Cols<V> t;
+      float rs[V];
+      load_affine<T, V>(a, c, t);
+      add_stats<V>(stats, c, a.cpg, t, rs);
+      constexpr int U = 4;
+      int64_t r = r0 + ty;
+      auto add = [&](const Raw<T, V>& rx, const Raw<T, V>& rd) {
         float f[V], d[V];
-        load_v<T, V>(x + r * a.ldx + c, f);
-        load_v<T, V>(dy + r * a.ldy + c, d);
+        to_float<T, V>(rx, f);
+        to_float<T, V>(rd, d);
+        grad_terms<V>(t, f, d, a.act);
+        v_add<V>(s0, d, s0);
+        v_fma<V>(d, f, s1, s1);
+      };
+      for (; r + (U - 1) * rows_t < r1; r += U * rows_t) {
+        Raw<T, V> rx[U], rd[U];
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const float xh = (f[j] - m[j]) * rs[j];
-          float act, slope;
-          act_grad_f(fmaf(xh, ga[j], be[j]), a.act, act, slope);
-          const float dz = d[j] * slope;
-          s0[j] += dz;
-          s1[j] = fmaf(dz, xh, s1[j]);
+        for (int u = 0; u < U; ++u) {
+          rx[u] = load_raw<T, V>(x + (r + u * rows_t) * a.ldx + c);
+          rd[u] = load_raw<T, V>(dy + (r + u * rows_t) * a.ldy + c);
         }
+#pragma unroll
+        for (int u = 0; u < U; ++u) add(rx[u], rd[u]);
       }
+      for (; r < r1; r += rows_t) add(load_raw<T, V>(x + r * a.ldx + c), load_raw<T, V>(dy + r * a.ldy + c));
+      v_mul<V>(s1, rs, s1);  // sum dz (x - mean) -> sum dz * xh
     }
     reduce_rows<V>(red, ch, a.C, c0 * V, tx, ty, cols_t, rows_t, active, s0, s1);
   }
@@ -326,27 +828,7 @@ __global__ void __launch_bounds__(kThreads) gn_grad_apply_kernel(const __grid_co
   pdl_trigger();
   const int64_t shares = (int64_t)a.batch * a.chunks;
   if (blockIdx.x >= shares) {
-    __shared__ float part[2][kThreads];
-    const int c = (int)(blockIdx.x - shares) * 32 + (threadIdx.x & 31), slice = threadIdx.x >> 5;
-    float s = 0.f, q = 0.f;
-    if (c < a.C) {
-#pragma unroll 4
-      for (int64_t p = slice; p < shares; p += kThreads / 32) {
-        s += a.pc[p * 2 * a.C + c];
-        q += a.pc[p * 2 * a.C + a.C + c];
-      }
-    }
-    part[0][threadIdx.x] = s;
-    part[1][threadIdx.x] = q;
-    __syncthreads();
-    if (slice == 0 && c < a.C) {
-      for (int i = 1; i < kThreads / 32; ++i) {
-        s += part[0][i * 32 + threadIdx.x];
-        q += part[1][i * 32 + threadIdx.x];
-      }
-      if (a.dbeta) a.dbeta[c] = s;
-      if (a.dgamma) a.dgamma[c] = q;
-    }
+    join_params(a, shares, (int)(blockIdx.x - shares));
     return;
   }
   const int64_t n = blockIdx.x / a.chunks;
@@ -375,7 +857,6 @@ __global__ void __launch_bounds__(kThreads) gn_grad_apply_kernel(const __grid_co
   const T* x = static_cast<const T*>(a.x) + n * a.rows * a.ldx;
   const T* dy = static_cast<const T*>(a.dy) + n * a.rows * a.ldy;
   T* dx = static_cast<T*>(a.out) + n * a.rows * a.ldx;
-  const T *gamma = static_cast<const T*>(a.gamma), *beta = static_cast<const T*>(a.beta);
   const float* stats = a.stats + n * a.G * 2;
   const int cols = a.C / V;
   for (int c0 = 0; c0 < cols; c0 += kThreads) {
@@ -383,33 +864,38 @@ __global__ void __launch_bounds__(kThreads) gn_grad_apply_kernel(const __grid_co
     const int tx = threadIdx.x % cols_t, ty = threadIdx.x / cols_t;
     if (ty >= rows_t) continue;
     const int c = (c0 + tx) * V;
-    float m[V], rs[V], ga[V], be[V], m1[V], m2[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int g = (c + j) / a.cpg;
-      m[j] = stats[2 * g];
-      rs[j] = stats[2 * g + 1];
-      ga[j] = gamma ? Elem<T>::to_f(gamma[c + j]) : 1.f;
-      be[j] = beta ? Elem<T>::to_f(beta[c + j]) : 0.f;
-      m1[j] = gs[2 * g];
-      m2[j] = gs[2 * g + 1];
-    }
-#pragma unroll 2
-    for (int64_t r = r1 - 1 - ty; r >= r0; r -= rows_t) {
+    Cols<V> t;
+    float rs[V];
+    GradCols<V> k;
+    load_affine<T, V>(a, c, t);
+    add_stats<V>(stats, c, a.cpg, t, rs);
+    grad_cols<V>(gs, c, a.cpg, rs, k);
+    auto put = [&](const Raw<T, V>& rx, const Raw<T, V>& rd, int64_t r) {
       float f[V], d[V];
-      load_v<T, V>(x + r * a.ldx + c, f);
-      load_v<T, V>(dy + r * a.ldy + c, d);
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const float xh = (f[j] - m[j]) * rs[j];
-        float act, slope;
-        act_grad_f(fmaf(xh, ga[j], be[j]), a.act, act, slope);
-        f[j] = rs[j] * (d[j] * slope * ga[j] - m1[j] - xh * m2[j]);
-      }
+      to_float<T, V>(rx, f);
+      to_float<T, V>(rd, d);
+      grad_terms<V>(t, f, d, a.act);
+      grad_out<V>(t, k, f, d);
       store_v<T, V>(dx + r * a.ldx + c, f);
+    };
+    constexpr int U = 2;  // reads before writes, as above
+    int64_t r = r1 - 1 - ty;
+    for (; r - (U - 1) * rows_t >= r0; r -= U * rows_t) {
+      Raw<T, V> rx[U], rd[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        rx[u] = load_raw<T, V>(x + (r - u * rows_t) * a.ldx + c);
+        rd[u] = load_raw<T, V>(dy + (r - u * rows_t) * a.ldy + c);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) put(rx[u], rd[u], r - u * rows_t);
     }
+    for (; r >= r0; r -= rows_t)
+      put(load_raw<T, V>(x + r * a.ldx + c), load_raw<T, V>(dy + r * a.ldy + c), r);
   }
 }
+
+// ------------------------------------------------------------------ host side
 
 sd_status check(const sd_group_norm_cfg* c) {
   if (!c) return SD_ERR_NULL_ARG;
@@ -419,18 +905,59 @@ sd_status check(const sd_group_norm_cfg* c) {
   if (c->channels > kMaxChannels || c->dtype < SD_DTYPE_BF16 || c->dtype > SD_DTYPE_F32 || c->act < SD_ACT_NONE ||
       c->act > SD_ACT_GELU)
     return SD_ERR_UNSUPPORTED;
-  // element counts within 48 bits, CTA counts within a grid's x extent
+  // element counts within 63 bits, CTA counts within a grid's x extent
   const int64_t ld = c->ld_x > c->ld_y ? c->ld_x : c->ld_y;
-  if (c->rows > (int64_t)1 << 40 || ld > (int64_t)1 << 24 || c->batch > 1 << 22) return SD_ERR_UNSUPPORTED;
+  if (c->rows > (int64_t)1 << 36 || ld > (int64_t)1 << 24 || c->batch > 1 << 18) return SD_ERR_UNSUPPORTED;
   return SD_OK;
 }
 
+cudaError_t launch_cluster(void (*kernel)(GnArgs), unsigned grid, unsigned ctas, size_t smem, cudaStream_t st,
+                           const GnArgs& a) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ctas;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+template <typename T>
+sd_status run_cluster(const sd_group_norm_cfg& c, GnArgs& a, const Plan& p, int back, const Device& dev,
+                      cudaStream_t st) {
+  a.width = p.width[back];
+  a.slices = c.channels / a.width;
+  a.chunk_rows = p.cta_rows[back];
+  const size_t smem = cluster_smem(a.width, a.width / a.cpg, kVec<T>, a.chunk_rows, 1 + back);
+  const unsigned ctas = (unsigned)p.ctas[back], grid = (unsigned)(c.batch * a.slices) * ctas;
+  const double bytes = (double)c.batch * c.rows * c.channels * sizeof(T) * (2 + back);
+  if (!back) {
+    OP_TRY((allow_smem<gn_cluster_fwd_kernel<T>>(kClusterSmem, dev.index)));
+    sdp::Scope sc("gn_cluster_fwd", sdp::F_GN_APPLY, 0, bytes, st);
+    return launched(launch_cluster(gn_cluster_fwd_kernel<T>, grid, ctas, smem, st, a));
+  }
+  OP_TRY((allow_smem<gn_cluster_bwd_kernel<T>>(kClusterSmem, dev.index)));
+  const bool more = c.batch > 1 && (a.dgamma || a.dbeta);
+  sdp::Scope sc("gn_cluster_bwd", sdp::F_GN_APPLY, 0, bytes, st, more ? 2 : 1);
+  OP_TRY(launched(launch_cluster(gn_cluster_bwd_kernel<T>, grid, ctas, smem, st, a)));
+  if (!more) return SD_OK;
+  return launched(launch_pdl(gn_param_join_kernel, dim3((c.channels + 31) / 32), dim3(kThreads), 0, st, a));
+}
+
 template <typename T, int V>
-sd_status run(const sd_group_norm_cfg& c, GnArgs& a, const Plan& p, bool grad, const Device& dev, cudaStream_t st) {
+sd_status run_pair(const sd_group_norm_cfg& c, GnArgs& a, const Plan& p, int back, const Device& dev, cudaStream_t st) {
   const size_t sums = (size_t)2 * c.channels * sizeof(float), gsum = (size_t)2 * c.groups * sizeof(float);
   const unsigned ctas = (unsigned)(c.batch * (int64_t)p.chunks);
   const double e = sizeof(T), n = (double)c.batch * c.rows * c.channels;
-  if (!grad) {
+  if (!back) {
     OP_TRY((allow_smem<gn_stats_share_kernel<T, V>>(2 * kMaxChannels * sizeof(float), dev.index)));
     OP_TRY((allow_smem<gn_apply_kernel<T, V>>(2 * kMaxChannels * sizeof(float), dev.index)));
     {
@@ -452,20 +979,20 @@ sd_status run(const sd_group_norm_cfg& c, GnArgs& a, const Plan& p, bool grad, c
 }
 
 template <typename T>
-sd_status run_type(const sd_group_norm_cfg& c, GnArgs& a, const Plan& p, bool grad, const Device& dev,
-                   cudaStream_t st) {
+sd_status run_type(const sd_group_norm_cfg& c, GnArgs& a, const Plan& p, int back, const Device& dev, cudaStream_t st) {
+  if (p.cluster[back]) return run_cluster<T>(c, a, p, back, dev, st);
   // 16-byte accesses when every row of every tensor starts on a 16-byte boundary
   const int v = kVec<T>;
-  if (c.channels % v == 0 && a.ldx % v == 0 && a.ldy % v == 0) return run<T, kVec<T>>(c, a, p, grad, dev, st);
-  return run<T, 1>(c, a, p, grad, dev, st);
+  if (c.channels % v == 0 && a.ldx % v == 0 && a.ldy % v == 0) return run_pair<T, kVec<T>>(c, a, p, back, dev, st);
+  return run_pair<T, 1>(c, a, p, back, dev, st);
 }
 
-sd_status dispatch(const sd_group_norm_cfg& c, GnArgs& a, const Plan& p, bool grad, cudaStream_t st) {
+sd_status dispatch(const sd_group_norm_cfg& c, GnArgs& a, const Plan& p, int back, cudaStream_t st) {
   Device dev;
   OP_TRY(current_device(&dev));
-  if (c.dtype == SD_DTYPE_BF16) return run_type<__nv_bfloat16>(c, a, p, grad, dev, st);
-  if (c.dtype == SD_DTYPE_F16) return run_type<__half>(c, a, p, grad, dev, st);
-  return run_type<float>(c, a, p, grad, dev, st);
+  if (c.dtype == SD_DTYPE_BF16) return run_type<__nv_bfloat16>(c, a, p, back, dev, st);
+  if (c.dtype == SD_DTYPE_F16) return run_type<__half>(c, a, p, back, dev, st);
+  return run_type<float>(c, a, p, back, dev, st);
 }
 
 void fill(const sd_group_norm_cfg& c, const Plan& p, void* ws, GnArgs* a) {
@@ -487,6 +1014,10 @@ void fill(const sd_group_norm_cfg& c, const Plan& p, void* ws, GnArgs* a) {
   a->pc = reinterpret_cast<float*>(w + up256(p.pg_floats * sizeof(float)));
 }
 
+size_t space(const Plan& p) {
+  return kOpHeader + up256(p.pg_floats * sizeof(float)) + up256(p.pc_floats * sizeof(float));
+}
+
 }  // namespace
 }  // namespace sdo
 
@@ -497,8 +1028,7 @@ extern "C" {
 size_t sd_group_norm_workspace_size(const sd_group_norm_cfg* cfg) {
   if (check(cfg) != SD_OK) return 0;
   if (cfg->batch == 0 || cfg->rows == 0) return kOpHeader;
-  const Plan p = make_plan(*cfg);
-  return kOpHeader + up256(p.pg_floats * sizeof(float)) + up256(p.pc_floats * sizeof(float));
+  return space(make_plan(*cfg));
 }
 
 sd_status sd_group_norm_fwd(const sd_group_norm_cfg* cfg, const void* x, const void* gamma, const void* beta, void* y,
@@ -508,8 +1038,8 @@ sd_status sd_group_norm_fwd(const sd_group_norm_cfg* cfg, const void* x, const v
   if (!x || !y) return SD_ERR_NULL_ARG;
   if (misaligned(x) || misaligned(gamma) || misaligned(beta) || misaligned(y) || misaligned(stats))
     return SD_ERR_MISALIGNED;
-  OP_TRY(check_workspace(sd_group_norm_workspace_size(cfg), workspace, ws_bytes));
   const Plan p = make_plan(*cfg);
+  OP_TRY(check_workspace(space(p), workspace, ws_bytes));
   GnArgs a;
   fill(*cfg, p, workspace, &a);
   a.x = x;
@@ -517,7 +1047,7 @@ sd_status sd_group_norm_fwd(const sd_group_norm_cfg* cfg, const void* x, const v
   a.beta = beta;
   a.out = y;
   a.stats = stats;
-  return dispatch(*cfg, a, p, false, (cudaStream_t)stream);
+  return dispatch(*cfg, a, p, 0, (cudaStream_t)stream);
 }
 
 sd_status sd_group_norm_bwd(const sd_group_norm_cfg* cfg, const void* x, const void* gamma, const void* beta,
@@ -536,8 +1066,8 @@ sd_status sd_group_norm_bwd(const sd_group_norm_cfg* cfg, const void* x, const v
     return SD_OK;
   }
   if (!x || !stats || !dy || !dx) return SD_ERR_NULL_ARG;
-  OP_TRY(check_workspace(sd_group_norm_workspace_size(cfg), workspace, ws_bytes));
   const Plan p = make_plan(*cfg);
+  OP_TRY(check_workspace(space(p), workspace, ws_bytes));
   GnArgs a;
   fill(*cfg, p, workspace, &a);
   a.x = x;
@@ -548,7 +1078,7 @@ sd_status sd_group_norm_bwd(const sd_group_norm_cfg* cfg, const void* x, const v
   a.out = dx;
   a.dgamma = dgamma;
   a.dbeta = dbeta;
-  return dispatch(*cfg, a, p, true, (cudaStream_t)stream);
+  return dispatch(*cfg, a, p, 1, (cudaStream_t)stream);
 }
 
 }  // extern "C"
