@@ -19,11 +19,12 @@
 //                    transposed copy of anything is made
 // Few CTAs and a long walk: the walk is split and FP32 parts are joined in order.
 //
-// 576 threads, one CTA per SM: warps 0-15 turn scores into P and dS (four warps per
+// 608 threads, one CTA per SM: warps 0-15 turn scores into P and dS (four warps per
 // TMEM lane quarter, 32 of the columns each: with eight warps of 64 columns a tile took
-// 1.8 times as long, the warps waiting for instructions and for one another), warp 16
-// loads by TMA, one thread of warp 17 issues the products: S of the next tile runs
-// beside dS of this one. P and dS
+// 1.2 to 1.4 times as long), warp 16 loads by TMA, one thread of warp 17 issues the
+// products around S and P, one of warp 18 those around dP and dS: beside sixteen busy
+// warps a thread issues one product in 80 to 100 cycles, so that one thread for all
+// five was what the others waited for. S of the next tile runs beside dS of this one. P and dS
 // are rounded to the inputs' type (the tensor core takes no other); everything else is
 // FP32. For FP16 inputs P carries a factor 2^shift (taken out of the results again)
 // that keeps the small probabilities of long sequences above FP16's subnormals.
@@ -38,8 +39,8 @@
 namespace sdo {
 namespace {
 
-constexpr int kThreads = 576;
-constexpr int kCompute = 512;   // threads of the computing warps
+constexpr int kThreads = 608;
+constexpr int kComputeWarps = 16;
 constexpr int kSms = 148;
 constexpr int kMaxSplits = 32;
 
@@ -204,7 +205,7 @@ __device__ __forceinline__ void score_grads(const uint32_t (&r)[16], const float
   }
 }
 template <typename T>
-__device__ __forceinline__ void pack16(const float* f, uint32_t (&pk)[8]) {
+__device__ __forceinline__ void pack16(const float* f, uint32_t* pk) {
 #pragma unroll
   for (int u = 0; u < 8; ++u) pk[u] = Elem<T>::pack(f[2 * u], f[2 * u + 1]);
 }
@@ -246,6 +247,23 @@ __device__ __forceinline__ void store_row(uint32_t tacc, int side, bool have, bo
   }
 }
 
+// Tensor memory of both kernels: two score regions of 128 columns, two accumulators, and
+// the packed P and dS that the products take as A operands.
+//   head_dim <= 64: accumulators of 64 columns leave room for P and dS of their own, so
+//     the scores of the next step are issued before this step's sums
+//   head_dim <= 128: P and dS lie over their scores, each warp's 32 columns packed into the
+//     first 16 of them, so that no warp writes where another still reads
+template <int NB>
+struct Tmem {
+  static constexpr bool kApart = NB == 1;
+  static constexpr uint32_t kS = 0, kDp = 128, kAcc0 = 256, kAcc1 = NB == 1 ? 320 : 384;
+  static constexpr uint32_t kP = NB == 1 ? 384 : kS, kDs = NB == 1 ? 448 : kDp;
+  // first packed column of scores [16 k, +16)
+  static constexpr __host__ __device__ uint32_t packed(uint32_t k) {
+    return NB == 1 ? 8 * k : (k >> 1) * 32 + (k & 1) * 8;
+  }
+};
+
 constexpr size_t kTailBytes = kDocRing * 512 + kRing * sizeof(Record) + 512;  // documents, records, barriers
 
 template <int NB>
@@ -253,21 +271,26 @@ constexpr size_t kDkvSmem = 1024 + (size_t)6 * NB * kBlockBytes + 2048 + kTailBy
 template <int NB>
 constexpr size_t kDqSmem = 1024 + (size_t)6 * NB * kBlockBytes + 2048 + kTailBytes;
 
-// d = x y^T over the head dimension, both K-major.
-__device__ __forceinline__ void issue_scores(uint32_t d, uint32_t x0, uint32_t y0, int nd, uint32_t idesc, uint64_t* bar) {
-  for (int n = 0; n < nd; ++n) {
-    const uint32_t o = (n >> 2) * kBlockBytes + (n & 3) * 32;
-    umma_bf16(d, umma_desc_k_sw128(x0 + o), umma_desc_k_sw128(y0 + o), idesc, n > 0);
+// d = x y^T over the head dimension (nd steps of 16), both K-major; x and y as desc_k().
+template <int NB>
+__device__ __forceinline__ void issue_scores(uint32_t d, uint32_t x, uint32_t y, int nd, uint32_t idesc, uint64_t* bar) {
+  mma_ss<false>(d, x, y, idesc);
+#pragma unroll
+  for (int n = 1; n < 4 * NB; ++n) {
+    const uint32_t o = (n >> 2) * (kBlockBytes >> 4) + (n & 3) * 2;
+    if (n < nd) mma_ss<true>(d, x + o, y + o, idesc);
   }
   umma_commit(bar);
 }
-// d += x y, x packed over a score region (32 columns of scores hold their 16 packed ones in
-// their first half), y 128 rows MN-major.
-__device__ __forceinline__ void issue_sum(uint32_t d, uint32_t x, uint32_t y0, uint32_t idesc, bool more) {
+// d = or += x y, x packed P or dS, y 128 rows MN-major as desc_mn().
+template <int NB>
+__device__ __forceinline__ void issue_sum(uint32_t d, uint32_t x, uint32_t y, uint32_t idesc, bool more) {
+  if (more)
+    mma_ts<true>(d, x, y, idesc);
+  else
+    mma_ts<false>(d, x, y, idesc);
 #pragma unroll
-  for (int k = 0; k < 8; ++k)
-    umma_ts(d, x + (k >> 1) * 32 + (k & 1) * 8, umma_desc_mn(y0 + k * 2048, kBlockBytes), idesc,
-            (more || k > 0) ? 1u : 0u);
+  for (int k = 1; k < 8; ++k) mma_ts<true>(d, x + Tmem<NB>::packed(k), y + k * 128, idesc);
 }
 
 // The walk of a dkv CTA over (head of the group, query tile).
@@ -308,9 +331,6 @@ struct HeadWalk {
   }
 };
 
-// TMEM: S^T [0,128), dP^T [128,256), dK [256,384), dV [384,512). P^T and dS^T lie over
-// their scores, each warp's 32 columns packed into the first 16 of them, so that no warp
-// writes where another still reads.
 template <typename T, int NB, bool SHAPED>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_dkv_kernel(const __grid_constant__ GradMaps maps, const __grid_constant__ GradArgs g) {
@@ -336,9 +356,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* p_full = bars + 8;
   uint64_t* ds_full = bars + 9;
   uint64_t* rec_full = bars + 10;   // [kRing]
-  uint64_t* rec_empty = bars + 14;  // [kRing], the computing warps and the MMA warp
+  uint64_t* rec_empty = bars + 14;  // [kRing], the computing warps and the two MMA warps
   uint64_t* doc_full = bars + 18;   // [kDocRing]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 18 + kDocRing);
+  uint64_t* pv_done = bars + 18 + kDocRing;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 19 + kDocRing);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const RecordRing ring{recs, rec_full, rec_empty, abort_flag, a.err};
   const DocRing docs{sdocs, doc_full, abort_flag, a.err};
@@ -352,7 +373,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kDocRing; ++i) mbar_init(&doc_full[i], 1);
-    for (int i = 0; i < 18; ++i) mbar_init(bars + i, i >= 14 ? 17 : i == 8 || i == 9 ? kCompute : 1);
+    for (int i = 0; i < 18; ++i) {
+      const bool both = i == 3 || i == 4 || i == 7;  // released by both MMA warps
+      mbar_init(bars + i, i >= 14 ? kComputeWarps + 2 : i == 8 || i == 9 ? kComputeWarps : both ? 2 : 1);
+    }
+    mbar_init(pv_done, 1);
     *abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&maps.q);
@@ -365,7 +390,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const uint32_t tS = tmem, tDp = tmem + 128, tDk = tmem + 256, tDv = tmem + 384;
+  using Tm = Tmem<NB>;
+  const uint32_t tS = tmem + Tm::kS, tDp = tmem + Tm::kDp, tDk = tmem + Tm::kAcc0, tDv = tmem + Tm::kAcc1;
+  const uint32_t tP = tmem + Tm::kP, tDs = tmem + Tm::kDs;
   pdl_wait();
   pdl_trigger();
 
@@ -403,46 +430,43 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = __shfl_sync(0xffffffffu, ok, 0);
     }
     if (lane == 0 && ok) ring.end(t);
-  } else if (warp == 17) {
+  } else if (warp >= 17) {
+    // warp 17: S^T = K Q^T and dV += P^T dO; warp 18: dP^T = V dO^T and dK += dS^T Q
+    const bool ds = warp == 18;
     const int nd = (a.D + 15) >> 4;
     const uint32_t id_s = idesc_f16(128, 128, f16, false, false);
     const uint32_t id_o = idesc_f16(128, nd * 16, f16, false, true);
-    const uint32_t k0 = smem_u32(sK), v0 = smem_u32(sV), q0 = smem_u32(sQ), d0 = smem_u32(sDo);
+    constexpr uint32_t kStage = kBytes >> 4;  // from one stage's descriptor to the other's
+    const uint32_t x0 = desc_k(smem_u32(ds ? sV : sK)), y0 = desc_k(smem_u32(ds ? sDo : sQ));
+    const uint32_t y0t = desc_mn(smem_u32(ds ? sQ : sDo), kBlockBytes);
+    const uint32_t tScore = ds ? tDp : tS, tOp = ds ? tDs : tP, tAcc = ds ? tDk : tDv;
+    uint64_t* const score_full = ds ? dp_full : s_full;
+    uint64_t* const op_full = ds ? ds_full : p_full;
+    auto next_scores = [&](int tt) {
+      if (!mbar_wait(&q_full[tt & 1], (tt >> 1) & 1, abort_flag, a.err)) return false;
+      tc_fence_after();
+      issue_scores<NB>(tScore, x0, y0 + (tt & 1) * kStage, nd, id_s, score_full);
+      return true;
+    };
     bool ok = true;
     int t = 0;
     bool have = ring.get(0).x >= 0;
-    if (have && lane == 0) {
-      ok = mbar_wait(kv_full, 0, abort_flag, a.err) && mbar_wait(&q_full[0], 0, abort_flag, a.err);
-      if (ok) {
-        tc_fence_after();
-        issue_scores(tS, k0, q0, nd, id_s, s_full);
-        issue_scores(tDp, v0, d0, nd, id_s, dp_full);
-      }
-    }
+    if (have && lane == 0) ok = mbar_wait(kv_full, 0, abort_flag, a.err) && next_scores(0);
     ok = __shfl_sync(0xffffffffu, ok, 0);
     for (; have && ok; ++t) {
       const bool more = ring.get(t + 1).x >= 0;
       if (lane == 0) {
-        const int s = t & 1, s1 = s ^ 1;
-        ok = mbar_wait(p_full, t & 1, abort_flag, a.err);
+        ok = mbar_wait(op_full, t & 1, abort_flag, a.err);
+        tc_fence_after();
+        if (Tm::kApart && ok && more) ok = next_scores(t + 1);
         if (ok) {
-          tc_fence_after();
-          issue_sum(tDv, tS, d0 + s * kBytes, id_o, t > 0);
+          issue_sum<NB>(tAcc, tOp, y0t + (t & 1) * kStage, id_o, t > 0);
+          umma_commit(&q_empty[t & 1]);
+          if (Tm::kApart && !ds) umma_commit(pv_done);
+          if (!more) umma_commit(acc_done);
         }
-        if (ok && more && (ok = mbar_wait(&q_full[s1], ((t + 1) >> 1) & 1, abort_flag, a.err))) {
-          tc_fence_after();
-          issue_scores(tS, k0, q0 + s1 * kBytes, nd, id_s, s_full);  // over P^T, whose product was issued before
-        }
-        ok = ok && mbar_wait(ds_full, t & 1, abort_flag, a.err);
-        if (ok) {
-          tc_fence_after();
-          issue_sum(tDk, tDp, q0 + s * kBytes, id_o, t > 0);
-          umma_commit(&q_empty[s]);
-          if (more)
-            issue_scores(tDp, v0, d0 + s1 * kBytes, nd, id_s, dp_full);
-          else
-            umma_commit(acc_done);
-        }
+        // over P^T or dS^T, whose product was issued before
+        if (!Tm::kApart && ok && more) ok = next_scores(t + 1);
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
       have = more;
@@ -452,6 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = q4 * 32 + lane, j = j0 + row;
     const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
     const uint32_t tSr = tS + lane_off + c0, tDpr = tDp + lane_off + c0;
+    const uint32_t tPr = tP + lane_off + Tm::packed(c0 / 16), tDsr = tDs + lane_off + Tm::packed(c0 / 16);
     ScoreTerms st;
     st.to = kTile;
     st.doc = a.k_doc && j < a.Nk ? a.k_doc[(int64_t)b * a.Nk + j] : 0;
@@ -478,9 +503,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       tc_fence_after();
       float pf[32];
+      uint32_t pk[16];
 #pragma unroll
       for (int e = 0; e < 32; e += 16) {
-        uint32_t q[16], pk[8];
+        uint32_t q[16];
         float nl[16], p[16];
         tmem_ld_x16(tSr + e, q);
 #pragma unroll
@@ -496,17 +522,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           probabilities<SHAPED, false>(a, st, q, c0 + e, nl, p, pf + e);
         else
           probabilities<SHAPED, true>(a, st, q, c0 + e, nl, p, pf + e);
-        pack16<T>(p, pk);
-        tmem_st_x8(tSr + e / 2, pk);  // over scores already read
+        pack16<T>(p, pk + e / 2);
+        if (!Tm::kApart) tmem_st_x8(tPr + e / 2, pk + e / 2);  // over scores already read
+      }
+      if (Tm::kApart) {
+        // P's columns are free once the last step's product is done
+        if (t > 0 && !(alive = mbar_wait_all(pv_done, (t - 1) & 1, abort_flag, a.err))) break;
+        tc_fence_after();
+        tmem_st_x16(tPr, pk);
       }
       tmem_store_wait();
       tc_fence_before();
-      mbar_arrive(p_full);
+      mbar_arrive_warp(p_full);
       if (!(alive = mbar_wait_all(dp_full, t & 1, abort_flag, a.err))) break;
       tc_fence_after();
 #pragma unroll
       for (int e = 0; e < 32; e += 16) {
-        uint32_t q[16], pk[8];
+        uint32_t q[16];
         float nd[16], ds[16];
         tmem_ld_x16(tDpr + e, q);
 #pragma unroll
@@ -522,12 +554,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           score_grads<false>(q, nd, pf + e, ds);
         else
           score_grads<true>(q, nd, pf + e, ds);
-        pack16<T>(ds, pk);
-        tmem_st_x8(tDpr + e / 2, pk);
+        pack16<T>(ds, pk + e / 2);
+        if (!Tm::kApart) tmem_st_x8(tDsr + e / 2, pk + e / 2);
+      }
+      if (Tm::kApart) {
+        // dS's columns are free once the last step's dS product is done
+        if (t > 0 && !(alive = mbar_wait_all(&q_empty[s ^ 1], ((t - 1) >> 1) & 1, abort_flag, a.err))) break;
+        tc_fence_after();
+        tmem_st_x16(tDsr, pk);
       }
       tmem_store_wait();
       tc_fence_before();
-      mbar_arrive(ds_full);
+      mbar_arrive_warp(ds_full);
       ring.done(t);
     }
     if (alive && t > 0) alive = mbar_wait_all(acc_done, 0, abort_flag, a.err);
@@ -621,7 +659,6 @@ __device__ __noinline__ void store_dq(const GradArgs& g, int b, int h, int i, in
   }
 }
 
-// TMEM: S [0,128) with P over it, dP [128,256) with dS over it, dS K [256,384), P K [384,512).
 // CTAs take over units as in the forward kernel; t counts steps and n units with steps.
 template <typename T, int NB, bool SHAPED>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -649,11 +686,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* p_full = bars + 9;
   uint64_t* ds_full = bars + 10;
   uint64_t* rec_full = bars + 11;   // [kRing]
-  uint64_t* rec_empty = bars + 15;  // [kRing], the computing warps and the MMA warp
+  uint64_t* rec_empty = bars + 15;  // [kRing], the computing warps and the two MMA warps
   uint64_t* next_bar = bars + 19;
   uint8_t* next_unit = reinterpret_cast<uint8_t*>(bars + 20);  // 16 bytes
   uint64_t* doc_full = bars + 22;  // [kDocRing]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 22 + kDocRing);
+  uint64_t* pv_done = bars + 22 + kDocRing;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 23 + kDocRing);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const RecordRing ring{recs, rec_full, rec_empty, abort_flag, a.err};
   const DocRing docs{sdocs, doc_full, abort_flag, a.err};
@@ -661,7 +699,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kDocRing; ++i) mbar_init(&doc_full[i], 1);
-    for (int i = 0; i < 20; ++i) mbar_init(bars + i, i == 9 || i == 10 ? kCompute : i >= 15 && i < 19 ? 17 : 1);
+    for (int i = 0; i < 20; ++i) {
+      const bool both = i == 1 || i == 4 || i == 5 || i == 8;  // released by both MMA warps
+      mbar_init(bars + i, i == 9 || i == 10 ? kComputeWarps : i >= 15 && i < 19 ? kComputeWarps + 2 : both ? 2 : 1);
+    }
+    mbar_init(pv_done, 1);
     *abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&maps.q);
@@ -674,7 +716,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const uint32_t tS = tmem, tDp = tmem + 128, tDq = tmem + 256, tPk = tmem + 384;
+  using Tm = Tmem<NB>;
+  const uint32_t tS = tmem + Tm::kS, tDp = tmem + Tm::kDp, tDq = tmem + Tm::kAcc0, tPk = tmem + Tm::kAcc1;
+  const uint32_t tP = tmem + Tm::kP, tDs = tmem + Tm::kDs;
   pdl_wait();
   pdl_trigger();
 
@@ -741,26 +785,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = __shfl_sync(0xffffffffu, ok, 0);
     }
     if (lane == 0 && ok) ring.end(r);
-  } else if (warp == 17) {
+  } else if (warp >= 17) {
+    // warp 17: S = Q K^T and the sum of P K; warp 18: dP = dO V^T and the sum of dS K.
+    // Steps follow one another across units: while one is summed, the scores of the next
+    // are issued, whichever unit it belongs to. Only one record is looked ahead: one
+    // without a tile is not waited past, since the ring moves on only with this step.
+    const bool ds = warp == 18;
     const int nd = (a.D + 15) >> 4;
     const uint32_t id_s = idesc_f16(128, 128, f16, false, false);
     const uint32_t id_o = idesc_f16(128, nd * 16, f16, false, true);
-    const uint32_t q0 = smem_u32(sQ), d0 = smem_u32(sDo), k0 = smem_u32(sK), v0 = smem_u32(sV);
-    // steps follow one another across units: while one is summed, the scores of the next
-    // are issued, whichever unit it belongs to. Only one record is looked ahead: one
-    // without a tile is not waited past, since the ring moves on only with this step.
+    constexpr uint32_t kStage = kBytes >> 4;  // from one stage's descriptor to the other's
+    const uint32_t x0 = desc_k(smem_u32(ds ? sDo : sQ)), y0 = desc_k(smem_u32(ds ? sV : sK));
+    const uint32_t k0t = desc_mn(smem_u32(sK), kBlockBytes);
+    const uint32_t tScore = ds ? tDp : tS, tOp = ds ? tDs : tP, tAcc = ds ? tDq : tPk;
+    uint64_t* const score_full = ds ? dp_full : s_full;
+    uint64_t* const op_full = ds ? ds_full : p_full;
     int n = -1, t = 0;
     bool ok = true, issued = false;
-    auto s_of = [&](int tt, int nn, bool fst) {
-      if (fst && !mbar_wait(q_full, nn & 1, abort_flag, a.err)) return false;
+    // the scores of step tt of unit nn
+    auto next_scores = [&](int tt, int nn, int flags) {
+      if ((flags & kFirst) && !mbar_wait(q_full, nn & 1, abort_flag, a.err)) return false;
       if (!mbar_wait(&kv_full[tt & 1], (tt >> 1) & 1, abort_flag, a.err)) return false;
       tc_fence_after();
-      issue_scores(tS, q0, k0 + (tt & 1) * kBytes, nd, id_s, s_full);
-      return true;
-    };
-    auto dp_of = [&](int tt, int flags) {
-      issue_scores(tDp, d0, v0 + (tt & 1) * kBytes, nd, id_s, dp_full);
+      issue_scores<NB>(tScore, x0, y0 + (tt & 1) * kStage, nd, id_s, score_full);
       if (flags & kLast) umma_commit(q_empty);
+      return true;
     };
     int2 cur = ring.get(0);  // tile, flags
     for (int r = 1; !(cur.y & kEnd) && ok; ++r) {
@@ -772,26 +821,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool more = nx.x >= 0;
       if (!issued) {
         if (cur.y & kFirst) ++n;
-        if (lane == 0 && (ok = s_of(t, n, cur.y & kFirst))) dp_of(t, cur.y);
+        if (lane == 0) ok = next_scores(t, n, cur.y);
       }
       if (more && (nx.y & kFirst)) ++n;
       if (lane == 0 && ok) {
-        const int s = t & 1;
-        const bool sum = !(cur.y & kFirst);
-        ok = mbar_wait(p_full, t & 1, abort_flag, a.err);
+        ok = mbar_wait(op_full, t & 1, abort_flag, a.err);
+        tc_fence_after();
+        if (Tm::kApart && ok && more) ok = next_scores(t + 1, n, nx.y);
         if (ok) {
-          tc_fence_after();
-          issue_sum(tPk, tS, k0 + s * kBytes, id_o, sum);
-        }
-        if (ok && more) ok = s_of(t + 1, n, nx.y & kFirst);
-        ok = ok && mbar_wait(ds_full, t & 1, abort_flag, a.err);
-        if (ok) {
-          tc_fence_after();
-          issue_sum(tDq, tDp, k0 + s * kBytes, id_o, sum);
-          umma_commit(&kv_empty[s]);
+          issue_sum<NB>(tAcc, tOp, k0t + (t & 1) * kStage, id_o, !(cur.y & kFirst));
+          umma_commit(&kv_empty[t & 1]);
+          if (Tm::kApart && !ds) umma_commit(pv_done);
           if (cur.y & kLast) umma_commit(acc_done);
-          if (more) dp_of(t + 1, nx.y);
         }
+        // over P or dS, whose product was issued before
+        if (!Tm::kApart && ok && more) ok = next_scores(t + 1, n, nx.y);
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
       issued = more;
@@ -803,6 +847,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = q4 * 32 + lane;
     const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
     const uint32_t tSr = tS + lane_off + c0, tDpr = tDp + lane_off + c0;
+    const uint32_t tPr = tP + lane_off + Tm::packed(c0 / 16), tDsr = tDs + lane_off + Tm::packed(c0 / 16);
     int t = 0, n = 0;
     bool alive = true;
     ScoreTerms st;
@@ -842,9 +887,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // P, and the cap's slope as FP16 pairs (in [0, 1]: off by 2^-12, below dS's own rounding)
         float p[32];
         [[maybe_unused]] uint32_t fac[SHAPED ? 16 : 1];
+        uint32_t pk[16];
 #pragma unroll
         for (int e = 0; e < 32; e += 16) {
-          uint32_t q[16], pk[8];
+          uint32_t q[16];
           float nl[16], pf[16];
           tmem_ld_x16(tSr + e, q);
 #pragma unroll
@@ -854,8 +900,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             probabilities<SHAPED, false>(a, st, q, c0 + e, nl, p + e, pf, SHAPED ? fac + e / 2 : nullptr);
           else
             probabilities<SHAPED, true>(a, st, q, c0 + e, nl, p + e, pf, SHAPED ? fac + e / 2 : nullptr);
-          pack16<T>(pf, pk);
-          tmem_st_x8(tSr + e / 2, pk);  // over scores already read
+          pack16<T>(pf, pk + e / 2);
+          if (!Tm::kApart) tmem_st_x8(tPr + e / 2, pk + e / 2);  // over scores already read
+        }
+        if (Tm::kApart) {
+          // P's columns are free once the last step's product is done
+          if (t > 0 && !(alive = mbar_wait_all(pv_done, (t - 1) & 1, abort_flag, a.err))) break;
+          tc_fence_after();
+          tmem_st_x16(tPr, pk);
         }
         if (!whole && j0 + kTile > nk && nk < a.Nk) {
           // keys behind the last one count as zeros in the sums, whatever they hold (S of this tile is done)
@@ -871,12 +923,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tmem_store_wait();
         tc_fence_before();
-        mbar_arrive(p_full);
+        mbar_arrive_warp(p_full);
         if (!(alive = mbar_wait_all(dp_full, t & 1, abort_flag, a.err))) break;
         tc_fence_after();
 #pragma unroll
         for (int e = 0; e < 32; e += 16) {
-          uint32_t q[16], pk[8];
+          uint32_t q[16];
           float nd[16], ds[16];
           tmem_ld_x16(tDpr + e, q);
 #pragma unroll
@@ -894,12 +946,18 @@ __global__ void __launch_bounds__(kThreads, 1)
               mul2(ds[y], ds[y + 1], Elem<__half>::lo(fac[(e + y) / 2]), Elem<__half>::hi(fac[(e + y) / 2]), ds[y],
                    ds[y + 1]);
           }
-          pack16<T>(ds, pk);
-          tmem_st_x8(tDpr + e / 2, pk);
+          pack16<T>(ds, pk + e / 2);
+          if (!Tm::kApart) tmem_st_x8(tDsr + e / 2, pk + e / 2);
+        }
+        if (Tm::kApart) {
+          // dS's columns are free once the last step's dS product is done
+          if (t > 0 && !(alive = mbar_wait_all(&kv_empty[(t - 1) & 1], ((t - 1) >> 1) & 1, abort_flag, a.err))) break;
+          tc_fence_after();
+          tmem_st_x16(tDsr, pk);
         }
         tmem_store_wait();
         tc_fence_before();
-        mbar_arrive(ds_full);
+        mbar_arrive_warp(ds_full);
         ++t;
       }
       if (flags & kLast) {

@@ -41,7 +41,7 @@ namespace sdo {
 namespace {
 
 constexpr int kThreads = 320;
-constexpr int kSoftmax = 256;   // threads of the softmax warps
+constexpr int kSoftmaxWarps = 8;
 constexpr int kSms = 148;
 constexpr int kMaxSplits = 64;
 
@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kDocRing; ++i) mbar_init(&doc_full[i], 1);
-    for (int i = 0; i < 25; ++i) mbar_init(bars + i, i == 14 || i == 15 ? kSoftmax : i >= 20 && i < 24 ? 9 : 1);
+    for (int i = 0; i < 25; ++i) mbar_init(bars + i, i == 14 || i == 15 ? kSoftmaxWarps : i >= 20 && i < 24 ? 9 : 1);
     *abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&maps.q);
@@ -273,15 +273,19 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int nd = (a.D + 15) >> 4;  // head dimension in steps of 16
     const uint32_t id_s = idesc_f16(128, 128, f16, false, false);
     const uint32_t id_o = idesc_f16(128, nd * 16, f16, false, true);
+    constexpr uint32_t kStage = Sh::kBytes >> 4;  // from one stage's descriptor to the next's
+    const uint32_t q0 = desc_k(smem_u32(sQ)), k0 = desc_k(smem_u32(sK)), v0t = desc_mn(smem_u32(sV), kBlockBytes);
     auto issue_s = [&](int t, int n, bool first, bool last) {
       const int s = t % KS, sq = n % KS;
       if (first && !mbar_wait(&q_full[sq], (n / KS) & 1, abort_flag, a.err)) return false;
       if (!mbar_wait(&k_full[s], (t / KS) & 1, abort_flag, a.err)) return false;
       tc_fence_after();
-      const uint32_t q0 = smem_u32(sQ + sq * Sh::kBytes), k0 = smem_u32(sK + s * Sh::kBytes);
-      for (int d = 0; d < nd; ++d) {
-        const uint32_t o = (d >> 2) * kBlockBytes + (d & 3) * 32;
-        umma_bf16(tS, umma_desc_k_sw128(q0 + o), umma_desc_k_sw128(k0 + o), id_s, d > 0);
+      const uint32_t q = q0 + sq * kStage, k = k0 + s * kStage;
+      mma_ss<false>(tS, q, k, id_s);
+#pragma unroll
+      for (int d = 1; d < 4 * NB; ++d) {
+        const uint32_t o = (d >> 2) * (kBlockBytes >> 4) + (d & 3) * 2;
+        if (d < nd) mma_ss<true>(tS, q + o, k + o, id_s);
       }
       umma_commit(&k_empty[s]);
       umma_commit(s_full);
@@ -293,10 +297,13 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (!mbar_wait(p_full, t & 1, abort_flag, a.err)) return false;
       if (!mbar_wait(&v_full[s], (t / KS) & 1, abort_flag, a.err)) return false;
       tc_fence_after();
-      const uint32_t v0 = smem_u32(sV + s * Sh::kBytes);
+      const uint32_t v = v0t + s * kStage;
+      if (first)
+        mma_ts<false>(tO, tP, v, id_o);
+      else
+        mma_ts<true>(tO, tP, v, id_o);
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        umma_ts(tO, tP + 8 * k, umma_desc_mn(v0 + k * 2048, kBlockBytes), id_o, (!first || k > 0) ? 1u : 0u);
+      for (int k = 1; k < 8; ++k) mma_ts<true>(tO, tP + 8 * k, v + k * 128, id_o);
       umma_commit(&v_empty[s]);
       umma_commit(pv_done);
       return true;
@@ -383,11 +390,11 @@ __global__ void __launch_bounds__(kThreads, 2)
         tc_fence_after();
         if (!work) {
           // a warp without rows only keeps the barriers going (its rows of P and O are never read)
-          if (NB == 1) mbar_arrive(s_free);
+          if (NB == 1) mbar_arrive_warp(s_free);
           if (!whole && !(alive = prepare_masks())) break;
           // not ahead of the working warps by more than this tile: their arrivals share a phase
           if (!first && !(alive = mbar_wait_all(pv_done, (t - 1) & 1, abort_flag, a.err))) break;
-          mbar_arrive(p_full);
+          mbar_arrive_warp(p_full);
         } else {
           uint32_t sv[64];
           tmem_ld_32x32b_x32(tSr, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
@@ -396,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           tmem_ld_wait_regs(*reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
           if constexpr (NB == 1) {
             tc_fence_before();
-            mbar_arrive(s_free);
+            mbar_arrive_warp(s_free);
           }
           if constexpr (SHAPED) {
             if (a.cap_out != 0.f) {
@@ -510,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           tmem_st_x32(tPr, pk);
           tmem_store_wait();
           tc_fence_before();
-          mbar_arrive(p_full);
+          mbar_arrive_warp(p_full);
         }
         ++t;
       }
@@ -647,20 +654,21 @@ FwdPlan plan_forward(const sd_attention_cfg& c) {
   p.items = (int64_t)c.batch * c.kv_heads * p.qtiles;
   // Time in key tiles of one SM for 1, 2, ... splits of every item. Two CTAs share an SM
   // and take turns (measured: 1.2 us a tile and SM at head_dim 64, 1.5 at 128, 0.8 more for
-  // capped or biased scores; a CTA alone needs 1.25 of that). Units start longest first, so
+  // capped or biased scores; a CTA alone needs 1.25 or 1.8 of that). Units start longest first, so
   // the last ones end about half the longest unit's tiles after the average; parts cost
   // one more launch and their FP32 rows, written and joined at 1.3 TB/s.
   const double nq = c.q_len, nk = c.k_len;
   const double seen = !c.causal ? 1.0 : nq <= nk ? 1.0 - nq / (2.0 * std::max(nk, 1.0)) : nk / (2.0 * nq);
   const double total = (double)p.items * p.ktiles * seen / kSms;
   const double tile_us = (c.head_dim <= 64 ? 1.2 : 1.5) + (c.softcap > 0.f ? 0.8 : 0.0);
+  const double alone = c.head_dim <= 64 ? 1.25 : 1.8;
   const double rows = (double)c.batch * c.heads * nq;
   double best = 0;
   p.splits = 1;
   for (int s = 1; s <= std::min(kMaxSplits, std::max(p.ktiles, 1)); ++s) {
     // one more tile's time for beginning and ending a unit
     const double units = (double)p.items * s, longest = 1 + (p.ktiles + s - 1) / s;
-    double t = units <= kSms ? 1.25 * longest : std::max(total + units / kSms + 0.5 * longest, 1.25 * longest);
+    double t = units <= kSms ? alone * longest : std::max(total + units / kSms + 0.5 * longest, alone * longest);
     if (s > 1) t += (3.0 + rows * s * (c.head_dim + 2) * 8.0 / 1.3e6) / tile_us;
     if (s == 1 || t < best) {
       best = t;

@@ -54,6 +54,41 @@ __device__ __forceinline__ void umma_ts(uint32_t tmem_d, uint32_t tmem_a, uint64
       : "memory");
 }
 
+// The issuing thread builds every operand descriptor itself, and its instructions, not
+// the tensor core, bounded products of small tiles. So the constant upper half of a
+// descriptor stays apart and a step along an operand is one 32-bit addition:
+//   lower half: address / 16, and the distance of 64-element MN blocks / 16 (MN-major)
+//   upper half: 1024 bytes between groups of 8 rows, version, 128-byte swizzle
+// 16 reduction elements further: +2 K-major (within 64 of them), +128 MN-major.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_k(uint32_t smem_addr) { return (smem_addr >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t desc_mn(uint32_t smem_addr, uint32_t block_bytes) {
+  return (smem_addr >> 4) | ((block_bytes >> 4) << 16);
+}
+// D[tmem] = or += A[smem] B[smem]^T
+template <bool ADD>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%1, %4};\n\t"
+      "mov.b64 b, {%2, %4};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(kDescHi), "n"(ADD ? 1 : 0)
+      : "memory");
+}
+// The same with A in tensor memory.
+template <bool ADD>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t tmem_a, uint32_t b_lo, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "mov.b64 b, {%2, %4};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d),
+      "r"(tmem_a), "r"(b_lo), "r"(idesc), "r"(kDescHi), "n"(ADD ? 1 : 0)
+      : "memory");
+}
+
 __device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
@@ -118,6 +153,13 @@ __device__ __forceinline__ int asked_unit(const void* result16) {
       : "r"(smem_u32(result16))
       : "memory");
   return taken ? (int)x : -1;
+}
+
+// One arrival for a whole warp, after all its lanes' writes (an arrival of every thread
+// of many warps would queue on the barrier's word for longer than a tile's arithmetic).
+__device__ __forceinline__ void mbar_arrive_warp(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
 // A bounded wait whose answer is the same for the whole warp (TMEM accesses are warp-collective).
