@@ -29,11 +29,17 @@
 namespace sdo {
 namespace {
 
-constexpr int kThreads = 320;     // warp 0 TMA, warp 1 MMA, warps 2-9 epilogue
-constexpr int kEpiThreads = 256;
+// Warp 0 TMA, warp 1 MMA, the others epilogue: sixteen for the forward gate, whose
+// activation bounded it with eight (29 us instead of 22 at 9216 x 320 x 1280), eight
+// elsewhere (the backward gate holds more per thread).
+template <int EPI>
+constexpr int kEpiWarps = EPI == 1 ? 16 : 8;
+template <int EPI>
+constexpr int kThreads = 64 + 32 * kEpiWarps<EPI>;
 constexpr int kSubA = 128 * 64 * 2;  // one CTA's 128 rows x 64 reduction elements
 constexpr int kRingBytes = 196608;
-constexpr int kSmemBytes = 1024 + kRingBytes + 256 + 2 * 256 * 4;
+constexpr int kColBytes = 2 * 4 * 256 * 2 * 4;  // EPI_GATE_GRAD: column sums [2][4 row quarters][2][256]
+constexpr int kSmemBytes = 1024 + kRingBytes + 256 + 2 * 256 * 4 + kColBytes;
 constexpr int kPairs = 74;        // CTA pairs the plan assumes (148 SMs)
 constexpr int kMaxSplits = 16;
 constexpr size_t kSplitBytes = size_t(64) << 20;
@@ -41,7 +47,7 @@ constexpr size_t kSplitBytes = size_t(64) << 20;
 enum Epi { EPI_PLAIN = 0, EPI_GATE = 1, EPI_GATE_GRAD = 2 };
 
 struct FfMaps {
-  CUtensorMap a, b;
+  CUtensorMap a, b, pre;
 };
 
 struct FfArgs {
@@ -60,36 +66,78 @@ struct FfArgs {
   void* pre;              // EPI_GATE: [M][2N] out or null; EPI_GATE_GRAD: [M][2N] in
   void* dpre;             // EPI_GATE_GRAD: [M][2N] out
   float* partial;         // EPI_PLAIN with splits: [splits][M][N]
+  float* colsum;          // EPI_GATE_GRAD: [M / 128][2N] column sums of dpre, or null
   int* err;
   int32_t clear_err;
 };
 
-// 32 FP32 values to 32 consecutive elements of T, `n` of them inside (n a multiple of 8).
+// 16 FP32 values to 16 consecutive elements of T, and back; n as below.
 template <typename T>
-__device__ __forceinline__ void store32(T* p, const float (&f)[32], int n) {
+__device__ __forceinline__ void store16(T* p, const float (&f)[16], int n, bool wide) {
+  uint32_t w[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (8 * i < n)
-      *reinterpret_cast<uint4*>(p + 8 * i) =
-          make_uint4(Elem<T>::pack(f[8 * i], f[8 * i + 1]), Elem<T>::pack(f[8 * i + 2], f[8 * i + 3]),
-                     Elem<T>::pack(f[8 * i + 4], f[8 * i + 5]), Elem<T>::pack(f[8 * i + 6], f[8 * i + 7]));
+  for (int j = 0; j < 8; ++j) w[j] = Elem<T>::pack(f[2 * j], f[2 * j + 1]);
+  if (wide && n >= 16) {
+    st_global_v8(p, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
+  } else {
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    if (n > 8) *reinterpret_cast<uint4*>(p + 8) = make_uint4(w[4], w[5], w[6], w[7]);
   }
 }
 template <typename T>
-__device__ __forceinline__ void load32(const T* p, uint32_t (&r)[16], int n) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint4 v = 8 * i < n ? *reinterpret_cast<const uint4*>(p + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
-    r[4 * i] = v.x;
-    r[4 * i + 1] = v.y;
-    r[4 * i + 2] = v.z;
-    r[4 * i + 3] = v.w;
+__device__ __forceinline__ void load16(const T* p, uint32_t (&r)[8], int n, bool wide) {
+  if (wide && n >= 16) {
+    ld_global_v8(p, r);
+  } else {
+    const uint4 a = *reinterpret_cast<const uint4*>(p);
+    const uint4 b = n > 8 ? *reinterpret_cast<const uint4*>(p + 8) : make_uint4(0u, 0u, 0u, 0u);
+    r[0] = a.x;
+    r[1] = a.y;
+    r[2] = a.z;
+    r[3] = a.w;
+    r[4] = b.x;
+    r[5] = b.y;
+    r[6] = b.z;
+    r[7] = b.w;
   }
+}
+// Sums of 16 columns over the warp's 32 rows (one row per lane): lanes 2j and 2j + 1 get
+// column j. Halves of the columns change places, so it takes 16 exchanges, not 80.
+__device__ __forceinline__ float column_sum16(float (&a)[16], int lane) {
+#pragma unroll
+  for (int w = 8; w > 0; w >>= 1) {
+    const bool up = lane & (2 * w);
+#pragma unroll
+    for (int i = 0; i < w; ++i) {
+      const float send = up ? a[i] : a[i + w], keep = up ? a[i + w] : a[i];
+      a[i] = keep + __shfl_xor_sync(0xffffffffu, send, 2 * w);
+    }
+  }
+  return a[0] + __shfl_xor_sync(0xffffffffu, a[0], 1);
 }
 
+// 32 FP32 values to 32 consecutive elements of T, `n` of them inside (n a multiple of 8).
+// A thread stores a row piece of its own, so a warp's instruction touches 32 rows: 32-byte
+// accesses where rows start on 32-byte boundaries (`wide`) fill whole sectors.
+template <typename T>
+__device__ __forceinline__ void store32(T* p, const float (&f)[32], int n, bool wide) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint32_t w[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = Elem<T>::pack(f[16 * i + 2 * j], f[16 * i + 2 * j + 1]);
+    if (wide && 16 * i + 16 <= n) {
+      st_global_v8(p + 16 * i, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
+    } else {
+      if (16 * i < n) *reinterpret_cast<uint4*>(p + 16 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+      if (16 * i + 8 < n) *reinterpret_cast<uint4*>(p + 16 * i + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+  }
+}
 template <typename T, int EPI>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<EPI>, 1)
     ff_gemm_kernel(const __grid_constant__ FfMaps maps, const __grid_constant__ FfArgs args) {
+  constexpr int kEpiThreads = 32 * kEpiWarps<EPI>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + kRingBytes);  // [stages <= 8]
@@ -99,6 +147,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float* ecols = reinterpret_cast<float*>(smem + kRingBytes + 256);  // [2][256]
+  float* csums = ecols + 512;                                        // [2][4][2][256]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = pair_rank();
@@ -142,6 +191,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int n0 = (rest % args.tiles_n) * args.step_n;
         const int brow = EPI == EPI_GATE ? (rank ? args.gate_row + n0 : n0) : n0 + (int)rank * half;
         const int hi = min(args.kb, (z + 1) * args.kb_split);
+        if (EPI == EPI_GATE_GRAD) {
+          // the epilogue's v and z of this tile, on their way to L2 during its main loop
+          for (int c = 0; c < args.bn && n0 + c < args.N; c += 64) {
+            tma_prefetch_2d(&maps.pre, n0 + c, m0);
+            tma_prefetch_2d(&maps.pre, args.N + n0 + c, m0);
+          }
+        }
         for (int kb = z * args.kb_split; kb < hi; kb += 2) {
           if (q >= (uint32_t)stages && !mbar_wait(&empty[s], ph ^ 1, abort_flag, args.err)) {
             ok = false;
@@ -175,8 +231,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
-      // encoded descriptor steps of 16 reduction elements: 32 bytes K-major, 2048 bytes MN-major
-      const uint64_t a_step = args.a_mn ? 128 : 2, b_step = args.b_mn ? 128 : 2;
+      // descriptor steps of 16 reduction elements: 32 bytes K-major, 2048 bytes MN-major
+      const uint32_t a_step = args.a_mn ? 128 : 2, b_step = args.b_mn ? 128 : 2;
+      const uint32_t a0 = smem_u32(smem), b0 = a0 + kSubA;
+      const uint32_t a_base = args.a_mn ? desc_mn(a0, 8192) : desc_k(a0);
+      const uint32_t b_base = args.b_mn ? desc_mn(b0, 8192) : desc_k(b0);
       int s = 0, it = 0;
       uint32_t ph = 0;
       bool ok = true;
@@ -196,12 +255,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           tc_fence_after();
           const int nsub = min(2, hi - kb);
           for (int h = 0; h < nsub; ++h) {
-            const uint32_t a = smem_u32(smem + s * stage_bytes + h * sub_bytes);
-            const uint64_t adesc = args.a_mn ? umma_desc_mn(a, 8192) : umma_desc_k_sw128(a);
-            const uint64_t bdesc = args.b_mn ? umma_desc_mn(a + kSubA, 8192) : umma_desc_k_sw128(a + kSubA);
+            const uint32_t o = (uint32_t)(s * stage_bytes + h * sub_bytes) >> 4;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              pair_umma(tacc, adesc + k * a_step, bdesc + k * b_step, args.idesc, acc);
+              pair_mma(tacc, a_base + o + k * a_step, b_base + o + k * b_step, args.idesc, acc);
               acc = 1;
             }
           }
@@ -226,6 +283,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     T* const pre = static_cast<T*>(args.pre);
     T* const dpre = static_cast<T*>(args.dpre);
     float* const partial = args.partial;
+    const bool wide = N % 16 == 0 && ((reinterpret_cast<uintptr_t>(out) | reinterpret_cast<uintptr_t>(pre) |
+                                       reinterpret_cast<uintptr_t>(dpre)) & 31) == 0;
     int it = 0;
     for (int u = pair; u < args.units; u += npairs, ++it) {
       const int z = u % args.splits, rest = u / args.splits;
@@ -247,84 +306,140 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         asm volatile("bar.sync 2, %0;" ::"n"(kEpiThreads) : "memory");
       }
+      const bool in = grow < M;
+      // the saved v and z of this row's first chunk while the main loop runs, each further
+      // chunk's while the one before is computed
+      [[maybe_unused]] uint32_t pv[2][8], pz[2][8];
+      auto load_pre = [&](int c, uint32_t (&v)[8], uint32_t (&z)[8]) {
+        const int left = N - (n0 + c);
+        if (in && c < step_n && left > 0) {
+          load16<T>(pre + grow * 2 * N + n0 + c, v, left, wide);
+          load16<T>(pre + grow * 2 * N + N + n0 + c, z, left, wide);
+        }
+      };
+      if (EPI == EPI_GATE_GRAD) load_pre(half * 16, pv[0], pz[0]);
       if (!mbar_wait_all(&acc_full[b], (it >> 1) & 1, abort_flag, args.err)) break;
       tc_fence_after();
       const uint32_t tacc = tmem + (uint32_t)(b * 256) + lane_off;
-      const bool in = grow < M;
-      for (int c = half * 32; c < step_n; c += 64) {
-        const int left = N - (n0 + c);  // columns of this chunk inside the output
-        if (left <= 0) break;
-        uint32_t r[32];
-        tmem_ld_32x32b_x32(tacc + c, r);
-        float f[32];
-        if (EPI == EPI_GATE) {
-          uint32_t r2[32];
-          tmem_ld_32x32b_x32(tacc + step_n + c, r2);
-          tmem_ld_wait_regs(r);
-          tmem_ld_wait_regs(r2);
-          float g[32];
+      if constexpr (EPI == EPI_GATE_GRAD) {
+        float* const cs = csums + b * 2048 + q4 * 512;
+        auto chunk = [&](int c, uint32_t (&v)[8], uint32_t (&z)[8], uint32_t (&v2)[8], uint32_t (&z2)[8]) {
+          const int left = N - (n0 + c);
+          uint32_t r[16];
+          tmem_ld_x16(tacc + c, r);
+          load_pre(c + 32, v2, z2);
+          tmem_ld_wait_16(r);
+          float f[16], dz[16], h[16];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
+          for (int i = 0; i < 16; i += 8) {
+            float zv[8], d[8], a8[8];
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) {
+              const int w = (i + j) / 2;
+              zv[j] = Elem<T>::lo(z[w]);
+              zv[j + 1] = Elem<T>::hi(z[w]);
+              // dz = dh v act'(z)
+              mul2(__uint_as_float(r[i + j]), __uint_as_float(r[i + j + 1]), Elem<T>::lo(v[w]), Elem<T>::hi(v[w]), d[j],
+                   d[j + 1]);
+            }
+            act_grad_vec<8>(zv, d, a8, act);
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) {
+              const int w = (i + j) / 2;
+              dz[i + j] = d[j];
+              dz[i + j + 1] = d[j + 1];
+              mul2(__uint_as_float(r[i + j]), __uint_as_float(r[i + j + 1]), a8[j], a8[j + 1], f[i + j], f[i + j + 1]);
+              mul2(Elem<T>::lo(v[w]), Elem<T>::hi(v[w]), a8[j], a8[j + 1], h[i + j], h[i + j + 1]);
+            }
+          }
+          if (in) {
+            store16<T>(dpre + grow * 2 * N + n0 + c, f, left, wide);
+            store16<T>(dpre + grow * 2 * N + N + n0 + c, dz, left, wide);
+            if (out) store16<T>(out + grow * N + n0 + c, h, left, wide);
+          }
+          if (args.colsum) {
+            if (!in) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) f[i] = dz[i] = 0.f;
+            }
+            const float sv = column_sum16(f, lane), sz = column_sum16(dz, lane);
+            if (!(lane & 1)) {
+              cs[c + (lane >> 1)] = sv;
+              cs[256 + c + (lane >> 1)] = sz;
+            }
+          }
+        };
+        for (int c = half * 16; c < step_n && n0 + c < N; c += 64) {
+          chunk(c, pv[0], pz[0], pv[1], pz[1]);
+          if (c + 32 < step_n && n0 + c + 32 < N) chunk(c + 32, pv[1], pz[1], pv[0], pz[0]);
+        }
+      }
+      if constexpr (EPI == EPI_GATE) {
+        for (int c = half * 16; c < step_n; c += 64) {
+          const int left = N - (n0 + c);  // columns of this chunk inside the output
+          if (left <= 0) break;
+          uint32_t r[16], r2[16];
+          tmem_ld_x16(tacc + c, r);
+          tmem_ld_x16(tacc + step_n + c, r2);
+          tmem_ld_wait_16(r);
+          tmem_ld_wait_16(r2);
+          float f[16], g[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
             f[i] = __uint_as_float(r[i]);
             g[i] = __uint_as_float(r2[i]);
           }
           if (bias) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              f[i] += ecol[c + i];
-              g[i] += ecol[step_n + c + i];
+            for (int i = 0; i < 16; i += 4) {
+              const float4 bv = *reinterpret_cast<const float4*>(ecol + c + i);
+              const float4 bz = *reinterpret_cast<const float4*>(ecol + step_n + c + i);
+              add2(f[i], f[i + 1], bv.x, bv.y, f[i], f[i + 1]);
+              add2(f[i + 2], f[i + 3], bv.z, bv.w, f[i + 2], f[i + 3]);
+              add2(g[i], g[i + 1], bz.x, bz.y, g[i], g[i + 1]);
+              add2(g[i + 2], g[i + 3], bz.z, bz.w, g[i + 2], g[i + 3]);
             }
           }
           if (pre && in) {
-            store32<T>(pre + grow * 2 * N + n0 + c, f, left);
-            store32<T>(pre + grow * 2 * N + N + n0 + c, g, left);
+            store16<T>(pre + grow * 2 * N + n0 + c, f, left, wide);
+            store16<T>(pre + grow * 2 * N + N + n0 + c, g, left, wide);
           }
+          act_vec<16>(g, act);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) f[i] *= act_f(g[i], act);
-          if (in) store32<T>(out + grow * N + n0 + c, f, left);
-        } else if (EPI == EPI_GATE_GRAD) {
-          uint32_t v[16], zz[16];
-          if (in) {
-            load32<T>(pre + grow * 2 * N + n0 + c, v, left);
-            load32<T>(pre + grow * 2 * N + N + n0 + c, zz, left);
-          }
+          for (int i = 0; i < 16; i += 2) mul2(f[i], f[i + 1], g[i], g[i + 1], f[i], f[i + 1]);
+          if (in) store16<T>(out + grow * N + n0 + c, f, left, wide);
+        }
+      }
+      if constexpr (EPI == EPI_PLAIN) {
+        for (int c = half * 32; c < step_n; c += 64) {
+          const int left = N - (n0 + c);  // columns of this chunk inside the output
+          if (left <= 0) break;
+          uint32_t r[32];
+          tmem_ld_32x32b_x32(tacc + c, r);
           tmem_ld_wait_regs(r);
-          float dz[32], h[32];
-          if (in) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const float vv = i & 1 ? Elem<T>::hi(v[i >> 1]) : Elem<T>::lo(v[i >> 1]);
-              const float zv = i & 1 ? Elem<T>::hi(zz[i >> 1]) : Elem<T>::lo(zz[i >> 1]);
-              float a, d;
-              act_grad_f(zv, act, a, d);
-              const float dh = __uint_as_float(r[i]);
-              f[i] = dh * a;
-              dz[i] = dh * vv * d;
-              h[i] = vv * a;
-            }
-            store32<T>(dpre + grow * 2 * N + n0 + c, f, left);
-            store32<T>(dpre + grow * 2 * N + N + n0 + c, dz, left);
-            if (out) store32<T>(out + grow * N + n0 + c, h, left);
-          }
-        } else {
-          tmem_ld_wait_regs(r);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(r[i]);
           if (partial) {
             if (in) {
+              // N is a multiple of 8 and the parts start on 256 bytes: whole 32-byte sectors
               float* p = partial + ((int64_t)z * M + grow) * N + n0 + c;
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                if (4 * i < left)
-                  __stcg(reinterpret_cast<float4*>(p + 4 * i),
-                         make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]));
+              for (int i = 0; i < 4; ++i)
+                if (8 * i < left)
+                  st_global_v8(p + 8 * i, r[8 * i], r[8 * i + 1], r[8 * i + 2], r[8 * i + 3], r[8 * i + 4],
+                               r[8 * i + 5], r[8 * i + 6], r[8 * i + 7]);
             }
           } else {
+            float f[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(r[i]);
             if (bias) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) f[i] += ecol[c + i];
+              for (int i = 0; i < 32; i += 4) {
+                const float4 bv = *reinterpret_cast<const float4*>(ecol + c + i);
+                add2(f[i], f[i + 1], bv.x, bv.y, f[i], f[i + 1]);
+                add2(f[i + 2], f[i + 3], bv.z, bv.w, f[i + 2], f[i + 3]);
+              }
             }
-            if (in) store32<T>(out + grow * N + n0 + c, f, left);
+            if (in) store32<T>(out + grow * N + n0 + c, f, left, wide);
           }
         }
       }
@@ -333,6 +448,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       tc_fence_before();
       asm volatile("bar.sync 3, %0;" ::"n"(kEpiThreads) : "memory");
       if (et == 0) pair_arrive(empty_addr[b]);
+      if (EPI == EPI_GATE_GRAD && args.colsum && et < step_n && n0 + et < N && grow - row < M) {
+        // the four row quarters in order; this buffer is written again two tiles from now
+        const float* c = csums + b * 2048 + et;
+        float* o = args.colsum + (grow - row) / 128 * 2 * N + n0 + et;
+        o[0] = (c[0] + c[512]) + (c[1024] + c[1536]);
+        o[N] = (c[256] + c[768]) + (c[1280] + c[1792]);
+      }
     }
   }
 
@@ -340,6 +462,156 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   pair_sync();
   tc_fence_after();
   if (warp == 1) pair_tmem_dealloc(tmem, 512);
+}
+
+// ------------------------------------------------------------------ few tokens
+// Bound by reading the weights: a warp per weight row (or a few, which share the
+// tokens' values), each lane 16 bytes at a time, several loads under way, FP32 sums
+// joined across the warp.
+constexpr int kSmallThreads = 256;
+constexpr int kSmallTokens = 4;  // 5 to 8 tokens took 29 to 30 us at 1280 x 5120, the tensor cores 24
+
+// acc[r][m] += row r's 8 weights times token m's 8 values (even and odd elements apart as
+// packed FP32 where there are several tokens). All tokens' values are asked for at once
+// and without a branch, else their latencies would add up: rows past the last token
+// repeat it and are not stored.
+template <typename T, int MT, int R>
+__device__ __forceinline__ void dot_step(const uint4 (&w)[R], const T* x, int64_t ld, int M, bool in,
+                                         float (&acc)[R][MT][2]) {
+  uint4 xv[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+    xv[m] = in ? *reinterpret_cast<const uint4*>(x + min(m, M - 1) * ld) : make_uint4(0u, 0u, 0u, 0u);
+  float f[R][8];
+#pragma unroll
+  for (int r = 0; r < R; ++r) unpack_vec<T, 8>(w[r], f[r]);
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    float v[8];
+    unpack_vec<T, 8>(xv[m], v);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if constexpr (MT == 1) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[r][m][j & 1] = fmaf(f[r][j], v[j], acc[r][m][j & 1]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; j += 2)
+          fma2v(f[r][j], f[r][j + 1], v[j], v[j + 1], acc[r][m][0], acc[r][m][1], acc[r][m][0], acc[r][m][1]);
+      }
+    }
+  }
+}
+__device__ __forceinline__ float lane_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// h = v act(z) (and pre = [v | z]): a warp reads the value and gate rows of C hidden columns.
+template <typename T, int MT, int C>
+__global__ void __launch_bounds__(kSmallThreads) ff_small_up_kernel(const T* __restrict__ x, const T* __restrict__ w1,
+                                                                    const T* __restrict__ b1, T* __restrict__ pre,
+                                                                    T* __restrict__ h, int M, int D, int F, int act,
+                                                                    int* err) {
+  constexpr int R = 2 * C;
+  pdl_wait();
+  pdl_trigger();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *err = 0;
+  const int lane = threadIdx.x & 31;
+  const int j0 = (blockIdx.x * (kSmallThreads / 32) + (threadIdx.x >> 5)) * C;  // F is a multiple of C
+  if (j0 >= F) return;
+  const uint4* w[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+    w[r] = reinterpret_cast<const uint4*>(w1 + (int64_t)((r < C ? 0 : F) + j0 + r % C) * D);
+  float acc[R][MT][2];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) acc[r][m][0] = acc[r][m][1] = 0.f;
+  constexpr int U = 8 / R;
+  for (int i0 = lane; i0 < D / 8; i0 += 32 * U) {
+    uint4 v[U][R];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        v[u][r] = i0 + 32 * u < D / 8 ? __ldg(w[r] + i0 + 32 * u) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      dot_step<T, MT, R>(v[u], x + (int64_t)(i0 + 32 * u) * 8, D, M, i0 + 32 * u < D / 8, acc);
+  }
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int j = j0 + c;
+    const float bv = b1 ? Elem<T>::to_f(b1[j]) : 0.f, bz = b1 ? Elem<T>::to_f(b1[F + j]) : 0.f;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const float v = lane_sum(acc[c][m][0] + acc[c][m][1]) + bv;
+      const float z = lane_sum(acc[C + c][m][0] + acc[C + c][m][1]) + bz;
+      if (m < M && lane == 0) {
+        h[(int64_t)m * F + j] = Elem<T>::from_f(v * act_f(z, act));
+        if (pre) {
+          pre[(int64_t)m * 2 * F + j] = Elem<T>::from_f(v);
+          pre[(int64_t)m * 2 * F + F + j] = Elem<T>::from_f(z);
+        }
+      }
+    }
+  }
+}
+
+// y = h w2^T + b2: four warps share the rows of R output columns, a quarter of the
+// reduction each. The first weights are asked for before the wait for h: no kernel of the
+// call writes them, and the kernel before this one started only after everything ahead
+// of the call had finished.
+template <typename T, int MT, int R>
+__global__ void __launch_bounds__(kSmallThreads) ff_small_down_kernel(const T* __restrict__ h, const T* __restrict__ w2,
+                                                                      const T* __restrict__ b2, T* __restrict__ y, int M,
+                                                                      int F, int N) {
+  __shared__ float red[kSmallThreads / 32][R][MT];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp & 3;
+  const int n0 = (blockIdx.x * (kSmallThreads / 128) + (warp >> 2)) * R;  // N is a multiple of R
+  const int per = (F / 8 + 3) / 4, lo = part * per, hi = n0 < N ? min(F / 8, lo + per) : 0;
+  const uint4* w = reinterpret_cast<const uint4*>(w2 + (int64_t)min(n0, N - R) * F);
+  const int64_t row = F / 8;
+  float acc[R][MT][2];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) acc[r][m][0] = acc[r][m][1] = 0.f;
+  constexpr int U = 5;
+  uint4 v[U][R];
+  auto ask = [&](int i0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        v[u][r] = i0 + 32 * u < hi ? __ldg(w + r * row + i0 + 32 * u) : make_uint4(0u, 0u, 0u, 0u);
+  };
+  ask(lo + lane);
+  pdl_wait();
+  pdl_trigger();
+  for (int i0 = lo + lane; i0 < hi; i0 += 32 * U) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      dot_step<T, MT, R>(v[u], h + (int64_t)(i0 + 32 * u) * 8, F, M, i0 + 32 * u < hi, acc);
+    ask(i0 + 32 * U);
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const float s = lane_sum(acc[r][m][0] + acc[r][m][1]);
+      if (lane == 0) red[warp][r][m] = s;
+    }
+  __syncthreads();
+  if (part == 0 && n0 < N && lane < R * MT) {
+    const int r = lane / MT, m = lane % MT;
+    float s = red[warp][r][m];
+    for (int p = 1; p < 4; ++p) s += red[warp + p][r][m];
+    if (m < M) y[(int64_t)m * N + n0 + r] = Elem<T>::from_f(s + (b2 ? Elem<T>::to_f(b2[n0 + r]) : 0.f));
+  }
 }
 
 // out = sum of the splits (in order) + bias, 8 columns per thread.
@@ -353,7 +625,7 @@ __global__ void __launch_bounds__(256) ff_join_kernel(const float* __restrict__ 
     float f[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) f[j] = 0.f;
-#pragma unroll 4
+#pragma unroll 8
     for (int z = 0; z < splits; ++z) {
       const float4* p = reinterpret_cast<const float4*>(partial + z * stride + i * 8);
       const float4 u = __ldcg(p), w = __ldcg(p + 1);
@@ -376,38 +648,27 @@ __global__ void __launch_bounds__(256) ff_join_kernel(const float* __restrict__ 
   }
 }
 
-// Column sums of up to two [rows][n] matrices (db1 and db2 in one launch): a CTA
-// sums 256 columns over a share of the rows into FP32 shares; a second kernel adds
-// the shares in order.
-struct ColSum {
-  const void* m[2];
-  void* out[2];
-  float* part[2];  // [chunks][n]
-  int32_t n[2], blocks[2];
-  int64_t rows, chunk_rows;
-  int32_t chunks;
-};
-
+// Column sums of dy [rows][n] for db2: a CTA sums 256 columns over a share of the rows
+// into an FP32 part.
 template <typename T>
-__global__ void __launch_bounds__(256) ff_colsum_kernel(const __grid_constant__ ColSum a) {
+__global__ void __launch_bounds__(256) ff_colsum_kernel(const T* __restrict__ m, int n, int64_t rows, int64_t chunk_rows,
+                                                        float* __restrict__ part, int* clear_err) {
   __shared__ float red[8][256];
   pdl_wait();
   pdl_trigger();
-  const int which = (int)blockIdx.x >= a.blocks[0];
-  const int n = a.n[which];
-  const int c0 = ((int)blockIdx.x - (which ? a.blocks[0] : 0)) * 256;
+  if (clear_err && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *clear_err = 0;
+  const int c0 = (int)blockIdx.x * 256;
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
   const int c = c0 + tx * 8;
-  const int64_t r0 = blockIdx.y * a.chunk_rows, r1 = min(a.rows, r0 + a.chunk_rows);
+  const int64_t r0 = blockIdx.y * chunk_rows, r1 = min(rows, r0 + chunk_rows);
   float s[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) s[j] = 0.f;
   if (c < n) {
-    const T* m = static_cast<const T*>(a.m[which]) + c;
 #pragma unroll 4
     for (int64_t r = r0 + ty; r < r1; r += 8) {
       float f[8];
-      unpack_vec<T, 8>(*reinterpret_cast<const uint4*>(m + r * n), f);
+      unpack_vec<T, 8>(*reinterpret_cast<const uint4*>(m + r * n + c), f);
 #pragma unroll
       for (int j = 0; j < 8; ++j) s[j] += f[j];
     }
@@ -419,22 +680,38 @@ __global__ void __launch_bounds__(256) ff_colsum_kernel(const __grid_constant__ 
     float t = 0.f;
 #pragma unroll
     for (int y = 0; y < 8; ++y) t += red[y][threadIdx.x];
-    a.part[which][(int64_t)blockIdx.y * n + c0 + threadIdx.x] = t;
+    part[(int64_t)blockIdx.y * n + c0 + threadIdx.x] = t;
   }
 }
 
+// db1 and db2 from their parts, 32 columns per CTA: eight slices of the parts, then the
+// slices in order.
+struct BiasJoin {
+  const float* part[2];  // [parts][n]
+  void* out[2];
+  int32_t n[2], blocks[2];
+  int64_t parts[2];
+};
 template <typename T>
-__global__ void __launch_bounds__(256) ff_colsum_join_kernel(const __grid_constant__ ColSum a) {
+__global__ void __launch_bounds__(256) ff_bias_join_kernel(const __grid_constant__ BiasJoin a) {
+  __shared__ float red[8][32];
   pdl_wait();
   pdl_trigger();
   const int which = (int)blockIdx.x >= a.blocks[0];
-  const int n = a.n[which];
-  const int c = ((int)blockIdx.x - (which ? a.blocks[0] : 0)) * 256 + threadIdx.x;
-  if (c >= n) return;
+  const int n = a.n[which], tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+  const int c = ((int)blockIdx.x - (which ? a.blocks[0] : 0)) * 32 + tx;
   float s = 0.f;
+  if (c < n) {
 #pragma unroll 8
-  for (int p = 0; p < a.chunks; ++p) s += a.part[which][(int64_t)p * n + c];
-  static_cast<T*>(a.out[which])[c] = Elem<T>::from_f(s);
+    for (int64_t p = ty; p < a.parts[which]; p += 8) s += a.part[which][p * n + c];
+  }
+  red[ty][tx] = s;
+  __syncthreads();
+  if (ty == 0 && c < n) {
+#pragma unroll
+    for (int y = 1; y < 8; ++y) s += red[y][tx];
+    static_cast<T*>(a.out[which])[c] = Elem<T>::from_f(s);
+  }
 }
 
 // ------------------------------------------------------------------ host side
@@ -450,12 +727,12 @@ struct Plan {
 };
 
 // Tile width and number of splits with the least predicted time, in cycles of one
-// SM: a 64-wide block costs the slower of its MMAs (2 bn cycles, 4 x 54 at least)
+// SM: a 64-wide block costs the slower of its MMAs (2 bn cycles, 4 x 80 to issue them)
 // and its operands' arrival (50 bytes a cycle), a tile about 1500 cycles more for
 // filling the pipeline and its last epilogue, and a split product the writing and
 // joining of its FP32 parts.
 Plan plan_product(const Product& p) {
-  const int widths[] = {256, 224, 192, 160, 128, 96, 64};
+  const int widths[] = {256, 192, 160, 128, 96, 64};
   const int64_t kb = (p.K + 63) / 64, pairs_m = (p.M + 255) / 256;
   Plan best{0, 1, 0};
   double best_cost = 0;
@@ -463,14 +740,16 @@ Plan plan_product(const Product& p) {
     if (p.gated && bn % 64) continue;  // each half whole 32-column chunks
     const int step = p.gated ? bn / 2 : bn;
     const int64_t tiles = pairs_m * ((p.N + step - 1) / step);
-    for (int sp = 1; sp <= (p.may_split ? kMaxSplits : 1); ++sp) {
+    // more splits than fill the GPU twice only cost
+    const int most = !p.may_split ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>(kMaxSplits, 2 * kPairs / tiles));
+    for (int sp = 1; sp <= most; ++sp) {
       int64_t per = (kb + sp - 1) / sp;
       per = (per + 1) / 2 * 2;
       if (sp > 1 && ((kb + per - 1) / per != sp || per < 4)) continue;
       if (sp > 1 && (size_t)sp * p.M * p.N * 4 > kSplitBytes) break;
       const int64_t rounds = (tiles * sp + kPairs - 1) / kPairs;
       const double b_bytes = p.b_mn ? (bn / 2 + 63) / 64 * 8192.0 : bn * 64.0;
-      const double block = std::max(std::max(2.0 * bn, 216.0), (kSubA + b_bytes) / 50.0);
+      const double block = std::max(std::max(2.0 * bn, 320.0), (kSubA + b_bytes) / 50.0);
       double cost = rounds * (per * block + 1500.0);
       if (sp > 1) cost += 4000.0 + 1.9 * 2.0 * sp * p.M * p.N * 4 / 4000.0;
       if (best.bn == 0 || cost < best_cost) {
@@ -510,6 +789,12 @@ sd_status product(Call& c, const char* name, const Product& p, const void* A, co
   const int64_t sa[1] = {(int64_t)da[0]}, sb[1] = {(int64_t)db[0]};
   const uint32_t ba[2] = {64, p.a_mn ? 64u : 128u}, bb[2] = {64, p.b_mn ? 64u : (uint32_t)g.bn / 2};
   if (!encode_map(&maps.a, f16, A, 2, da, sa, ba) || !encode_map(&maps.b, f16, B, 2, db, sb, bb)) return SD_ERR_LAUNCH;
+  if (EPI == EPI_GATE_GRAD) {
+    const uint64_t dp[2] = {2 * (uint64_t)p.N, M};
+    const int64_t sp[1] = {2 * (int64_t)p.N};
+    const uint32_t bp[2] = {64, 128};
+    if (!encode_map(&maps.pre, f16, a.pre, 2, dp, sp, bp)) return SD_ERR_LAUNCH;
+  }
   a.M = (int32_t)p.M;
   a.N = p.N;
   a.kb = (int32_t)((p.K + 63) / 64);
@@ -542,11 +827,12 @@ sd_status product(Call& c, const char* name, const Product& p, const void* A, co
   const double flops = 2.0 * p.M * p.N * p.K * (p.gated ? 2 : 1);
   const double bytes = 2.0 * (p.M * (double)p.K + p.K * (double)rows_b + p.M * (double)p.N);
   sdp::Scope sc(name, sdp::F_GEMM, flops, bytes, c.st, g.splits > 1 ? 2 : 1);
-  OP_TRY(launched(launch_pdl(ff_gemm_kernel<T, EPI>, dim3(2 * pairs), dim3(kThreads), kSmemBytes, c.st, maps, a)));
+  OP_TRY(launched(launch_pdl(ff_gemm_kernel<T, EPI>, dim3(2 * pairs), dim3(kThreads<EPI>), kSmemBytes, c.st, maps, a)));
   if (g.splits == 1) return SD_OK;
   const int64_t vecs = p.M * p.N / 8;
-  const unsigned blocks = (unsigned)std::min<int64_t>((vecs + 255) / 256, (int64_t)c.dev.sms * 8);
-  return launched(launch_pdl(ff_join_kernel<T>, dim3(blocks), dim3(256), 0, c.st, (const float*)c.partial, g.splits,
+  const int threads = vecs < 256 * (int64_t)c.dev.sms ? 64 : 256;  // few vectors: over all SMs
+  const unsigned blocks = (unsigned)std::min<int64_t>((vecs + threads - 1) / threads, (int64_t)c.dev.sms * 8);
+  return launched(launch_pdl(ff_join_kernel<T>, dim3(blocks), dim3(threads), 0, c.st, (const float*)c.partial, g.splits,
                              p.M, p.N, static_cast<const T*>(bias), static_cast<T*>(a.out)));
 }
 
@@ -569,7 +855,7 @@ Product p_dw1(const sd_gated_ff_cfg& c) { return {2 * (int64_t)c.d_hidden, c.tok
 Product p_dw2(const sd_gated_ff_cfg& c) { return {c.d_out, c.tokens, c.d_hidden, false, true, true, true}; }
 
 struct Space {
-  size_t h, dpre, partial, colsum, total;
+  size_t h, dpre, partial, colsum, colsum2, total;
   int chunks;
 };
 Space plan_space(const sd_gated_ff_cfg& c) {
@@ -580,15 +866,42 @@ Space plan_space(const sd_gated_ff_cfg& c) {
   size_t parts = 0;
   for (const Product& p : {p_down(c), p_dx(c), p_dw1(c), p_dw2(c)}) parts = std::max(parts, split_bytes(p));
   s.colsum = s.partial + up256(parts);
-  const int blocks = (2 * c.d_hidden + 255) / 256 + (c.d_out + 255) / 256;
+  // db1: a part for every 128 tokens; db2: enough parts to fill the GPU
+  const int blocks = (c.d_out + 255) / 256;
   s.chunks = (int)std::max<int64_t>(1, std::min<int64_t>((c.tokens + 63) / 64, (592 + blocks - 1) / blocks));
-  s.total = s.colsum + up256((size_t)s.chunks * (2 * (size_t)c.d_hidden + c.d_out) * 4);
+  s.colsum2 = s.colsum + up256((size_t)((c.tokens + 127) / 128) * 2 * c.d_hidden * 4);
+  s.total = s.colsum2 + up256((size_t)s.chunks * c.d_out * 4);
   return s;
+}
+
+template <typename T, int MT>
+sd_status forward_small(Call& c, const Space& s, uint8_t* ws, const void* w1, const void* b1, const void* w2,
+                        const void* b2, const void* x, void* pre, void* y) {
+  // one token: as many warps as can be; more: rows that share the tokens' values
+  constexpr int C = MT == 1 ? 1 : 2, R = MT == 1 ? 1 : 2;
+  const sd_gated_ff_cfg& g = *c.cfg;
+  const int M = (int)g.tokens, D = g.d_in, F = g.d_hidden, N = g.d_out;
+  const auto t = [](const void* p) { return static_cast<const T*>(p); };
+  T* h = reinterpret_cast<T*>(ws + s.h);
+  {
+    const int per = kSmallThreads / 32 * C;
+    sdp::Scope sc("ff_small_up", sdp::F_GEMV, 4.0 * M * D * F, 4.0 * D * F, c.st);
+    OP_TRY(launched(launch_pdl(ff_small_up_kernel<T, MT, C>, dim3((unsigned)((F + per - 1) / per)), dim3(kSmallThreads), 0,
+                               c.st, t(x), t(w1), t(b1), static_cast<T*>(pre), h, M, D, F, (int)g.act, c.err)));
+  }
+  const int per = kSmallThreads / 128 * R;
+  sdp::Scope sc("ff_small_down", sdp::F_GEMV, 2.0 * M * N * F, 2.0 * N * F, c.st);
+  return launched(launch_pdl(ff_small_down_kernel<T, MT, R>, dim3((unsigned)((N + per - 1) / per)), dim3(kSmallThreads), 0,
+                             c.st, (const T*)h, t(w2), t(b2), static_cast<T*>(y), M, F, N));
 }
 
 template <typename T>
 sd_status forward(Call& c, const Space& s, uint8_t* ws, const void* w1, const void* b1, const void* w2, const void* b2,
                   const void* x, void* pre, void* y) {
+  // up to kSmallTokens tokens the weights' bytes are all that counts (see the kernels)
+  if (c.cfg->tokens == 1) return forward_small<T, 1>(c, s, ws, w1, b1, w2, b2, x, pre, y);
+  if (c.cfg->tokens == 2) return forward_small<T, 2>(c, s, ws, w1, b1, w2, b2, x, pre, y);
+  if (c.cfg->tokens <= kSmallTokens) return forward_small<T, kSmallTokens>(c, s, ws, w1, b1, w2, b2, x, pre, y);
   FfArgs a;
   memset(&a, 0, sizeof(a));
   a.bias = b1;
@@ -611,6 +924,7 @@ sd_status backward(Call& c, const Space& s, uint8_t* ws, const void* w1, const v
     a.pre = const_cast<void*>(pre);
     a.dpre = ws + s.dpre;
     a.out = dw2 ? ws + s.h : nullptr;
+    a.colsum = db1 ? reinterpret_cast<float*>(ws + s.colsum) : nullptr;
     OP_TRY((product<T, EPI_GATE_GRAD>(c, "ff_dh_gate", p_dh(g), dy, w2, a)));
   }
   memset(&a, 0, sizeof(a));
@@ -626,28 +940,30 @@ sd_status backward(Call& c, const Space& s, uint8_t* ws, const void* w1, const v
     a.out = dw2;
     OP_TRY((product<T, EPI_PLAIN>(c, "ff_dw2", p_dw2(g), dy, ws + s.h, a)));
   }
+  if (db2) {
+    const int64_t rows = (g.tokens + s.chunks - 1) / s.chunks;
+    sdp::Scope sc("ff_colsum", sdp::F_OTHER, 0, 2.0 * g.tokens * g.d_out, c.st);
+    OP_TRY(launched(launch_pdl(ff_colsum_kernel<T>, dim3((g.d_out + 255) / 256, (unsigned)((g.tokens + rows - 1) / rows)),
+                               dim3(256), 0, c.st, static_cast<const T*>(dy), g.d_out, g.tokens, rows,
+                               reinterpret_cast<float*>(ws + s.colsum2), c.first ? c.err : nullptr)));
+    c.first = false;
+  }
   if (db1 || db2) {
-    ColSum cs;
-    memset(&cs, 0, sizeof(cs));
-    float* part = reinterpret_cast<float*>(ws + s.colsum);
-    cs.m[0] = ws + s.dpre;
-    cs.m[1] = dy;
-    cs.out[0] = db1;
-    cs.out[1] = db2;
-    cs.part[0] = part;
-    cs.part[1] = part + (size_t)s.chunks * 2 * g.d_hidden;
-    cs.n[0] = 2 * g.d_hidden;
-    cs.n[1] = g.d_out;
-    cs.blocks[0] = db1 ? (cs.n[0] + 255) / 256 : 0;
-    cs.blocks[1] = db2 ? (cs.n[1] + 255) / 256 : 0;
-    cs.rows = g.tokens;
-    cs.chunk_rows = (g.tokens + s.chunks - 1) / s.chunks;
-    cs.chunks = (int)((g.tokens + cs.chunk_rows - 1) / cs.chunk_rows);
-    const unsigned blocks = (unsigned)(cs.blocks[0] + cs.blocks[1]);
-    const double bytes = 2.0 * g.tokens * ((db1 ? cs.n[0] : 0) + (db2 ? cs.n[1] : 0));
-    sdp::Scope sc("ff_colsum", sdp::F_OTHER, 0, bytes, c.st, 2);
-    OP_TRY(launched(launch_pdl(ff_colsum_kernel<T>, dim3(blocks, cs.chunks), dim3(256), 0, c.st, cs)));
-    OP_TRY(launched(launch_pdl(ff_colsum_join_kernel<T>, dim3(blocks), dim3(256), 0, c.st, cs)));
+    BiasJoin j;
+    memset(&j, 0, sizeof(j));
+    const int64_t rows = (g.tokens + s.chunks - 1) / s.chunks;
+    j.part[0] = reinterpret_cast<const float*>(ws + s.colsum);
+    j.part[1] = reinterpret_cast<const float*>(ws + s.colsum2);
+    j.out[0] = db1;
+    j.out[1] = db2;
+    j.n[0] = 2 * g.d_hidden;
+    j.n[1] = g.d_out;
+    j.parts[0] = (g.tokens + 127) / 128;
+    j.parts[1] = (g.tokens + rows - 1) / rows;
+    for (int i = 0; i < 2; ++i) j.blocks[i] = j.out[i] ? (j.n[i] + 31) / 32 : 0;
+    sdp::Scope sc("ff_bias_join", sdp::F_OTHER, 0, 4.0 * (j.parts[0] * j.n[0] + j.parts[1] * j.n[1]), c.st);
+    OP_TRY(launched(
+        launch_pdl(ff_bias_join_kernel<T>, dim3((unsigned)(j.blocks[0] + j.blocks[1])), dim3(256), 0, c.st, j)));
   }
   return SD_OK;
 }

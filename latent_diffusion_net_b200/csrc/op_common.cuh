@@ -141,6 +141,29 @@ __device__ __forceinline__ void mul2(float a0, float a1, float b0, float b1, flo
       : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
 }
 
+// normal_cdf of two values, the same arithmetic in packed FP32.
+__device__ __forceinline__ void normal_cdf2(float z0, float z1, float& c0, float& c1, float& e0, float& e1) {
+  float t0, t1, w0, w1, q0, q1;
+  fma2v(fabsf(z0), fabsf(z1), 0.35355339f, 0.35355339f, 1.f, 1.f, t0, t1);
+  t0 = fast_rcp(t0);
+  t1 = fast_rcp(t1);
+  mul2(z0, z1, z0, z1, e0, e1);
+  mul2(e0, e1, -0.5f * kLog2e, -0.5f * kLog2e, e0, e1);
+  e0 = fast_ex2(e0);
+  e1 = fast_ex2(e1);
+  fma2v(t0, t1, 0.04765096f, 0.04765096f, -0.19102928f, -0.19102928f, w0, w1);
+  fma2v(w0, w1, t0, t1, 0.21266575f, 0.21266575f, w0, w1);
+  fma2v(w0, w1, t0, t1, 0.0058340114f, 0.0058340114f, w0, w1);
+  fma2v(w0, w1, t0, t1, 0.14584327f, 0.14584327f, w0, w1);
+  fma2v(w0, w1, t0, t1, 0.13779275f, 0.13779275f, w0, w1);
+  fma2v(w0, w1, t0, t1, 0.14124271f, 0.14124271f, w0, w1);
+  mul2(w0, w1, t0, t1, w0, w1);
+  mul2(w0, w1, e0, e1, w0, w1);
+  fma2v(w0, w1, -1.f, -1.f, 1.f, 1.f, q0, q1);
+  c0 = z0 < 0.f ? w0 : q0;
+  c1 = z1 < 0.f ? w1 : q1;
+}
+
 // The activations on V values at once: the same arithmetic as act_f and act_grad_f
 // with the multiply-adds as packed pairs (half the instructions); the activation is
 // chosen once for all V.
@@ -160,7 +183,11 @@ __device__ __forceinline__ void act_vec(float (&z)[V], int act) {
     }
   } else if (act == SD_ACT_GELU) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) z[j] = act_f(z[j], SD_ACT_GELU);
+    for (int j = 0; j < V; j += 2) {
+      float c0, c1, e0, e1;
+      normal_cdf2(z[j], z[j + 1], c0, c1, e0, e1);
+      mul2(z[j], z[j + 1], c0, c1, z[j], z[j + 1]);
+    }
   }
 }
 // d *= act'(z); a = act(z) (both may be unused)
@@ -189,10 +216,13 @@ __device__ __forceinline__ void act_grad_vec(const float (&z)[V], float (&d)[V],
     }
   } else if (act == SD_ACT_GELU) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      float s;
-      act_grad_f(z[j], SD_ACT_GELU, a[j], s);
-      d[j] *= s;
+    for (int j = 0; j < V; j += 2) {
+      float c0, c1, e0, e1;
+      normal_cdf2(z[j], z[j + 1], c0, c1, e0, e1);
+      mul2(z[j], z[j + 1], c0, c1, a[j], a[j + 1]);
+      mul2(e0, e1, 0.39894228040143268f, 0.39894228040143268f, e0, e1);
+      fma2v(z[j], z[j + 1], e0, e1, c0, c1, c0, c1);
+      mul2(d[j], d[j + 1], c0, c1, d[j], d[j + 1]);
     }
   } else {
 #pragma unroll
