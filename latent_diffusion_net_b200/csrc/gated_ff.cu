@@ -318,7 +318,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<EPI>, 1)
         }
       };
       if (EPI == EPI_GATE_GRAD) load_pre(half * 16, pv[0], pz[0]);
-      if (!mbar_wait_all(&acc_full[b], (it >> 1) & 1, abort_flag, args.err)) break;
+      if (!mbar_wait_all(&acc_full[b], (it >> 1) & 1, abort_flag, args.err)) {
+        // other warps may have got through, and wait for this one at the barriers
+        asm volatile("bar.sync 3, %0;" ::"n"(kEpiThreads) : "memory");
+        continue;
+      }
       tc_fence_after();
       const uint32_t tacc = tmem + (uint32_t)(b * 256) + lane_off;
       if constexpr (EPI == EPI_GATE_GRAD) {

@@ -15,6 +15,9 @@
 //       the second joins the shares and walks the same rows from their end, so that
 //       it finds the rows that the first one read last still in L2
 // Sums are joined in a fixed order, so results repeat bit for bit.
+// Measured (BF16, SiLU): 768 x 768 x 128 forward 89 us, 302 MB of x and y at 3.4 TB/s (x is
+// read twice, in part from L2); 4 x 9216 rows x 320 forward 22 us, gradients 31 us;
+// 144 rows x 1280 forward 7.6 us, which is launch, cluster barriers and two latencies.
 //
 // A thread owns one 16-byte vector of channels for all its rows (channel terms
 // stay in registers, a warp reads whole sectors whatever C/G is); sums are FP32
@@ -34,9 +37,8 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kMaxChannels = 8192;  // per-channel sums of a CTA: 64 KB of shared memory
-constexpr int kMaxChunks = 320;     // shares of one image (two CTAs for each of 148 SMs, and some)
-constexpr int kTargetCtas = 296;
 constexpr int kSms = 148;
+constexpr int kMaxChunks = 160;  // shares of one image: kSms up to a multiple of 32
 constexpr int kMaxCluster = 8;
 constexpr size_t kClusterSmem = 220 * 1024;
 
@@ -45,7 +47,7 @@ struct GnArgs {
   void* out;  // y or dx
   float* stats;
   float *dgamma, *dbeta;
-  float *pg, *pc;  // shares: per group [batch][chunks][G][2], per channel [batch][chunks][2][C]
+  float *pg, *pc;  // shares: per group [batch][G][chunks][2], per channel [batch][chunks][2][C]
   int64_t rows, chunk_rows, ldx, ldy;
   int32_t batch, C, G, cpg, act, chunks;
   int32_t slices, width;  // cluster kernels: slices of an image, channels of one
@@ -57,8 +59,8 @@ struct Plan {
   bool cluster[2];  // forward, backward
   int ctas[2], width[2];
   int64_t cta_rows[2];
-  int chunks;
-  int64_t chunk_rows;
+  int chunks[2];
+  int64_t chunk_rows[2];
   size_t pg_floats, pc_floats;
 };
 
@@ -81,7 +83,7 @@ Plan make_plan(const sd_group_norm_cfg& c) {
   const int unit = std::lcm(cpg, vec);  // narrowest slice of whole groups and whole vectors
   for (int back = 0; back < 2 && wide && c.channels % unit == 0; ++back) {
     const int n = c.channels / unit;
-    double best = 0;
+    double best = 0;  // in passes, see below
     for (int k = 1; k <= n; ++k) {
       if (n % k) continue;
       const int width = unit * k, cols = width / vec;
@@ -92,10 +94,13 @@ Plan make_plan(const sd_group_norm_cfg& c) {
         const int64_t rows = (c.rows + ctas - 1) / ctas;
         if (ctas > 1 && rows < rows_t) break;
         if (cluster_smem(width, width / cpg, vec, rows, 1 + back) > kClusterSmem) continue;
-        // passes over a thread's rows in all waves, and about four passes' worth of
-        // latency for the sums and the cluster's two barriers per wave
-        const int64_t total = (int64_t)c.batch * (n / k) * ctas;
-        const double cost = (double)((total + kSms - 1) / kSms) * ((rows + rows_t - 1) / rows_t + 4.0);
+        // Measured: a wave of clusters takes about 7 us and 0.5 us (0.75 us for gradients)
+        // for each pass of its threads over their rows, more where a row of the slice
+        // is few sectors, so that the parts outside it count (80 bytes: a third). One CTA
+        // fits on an SM, and of larger clusters fewer fit on the GPU.
+        const int64_t total = (int64_t)c.batch * (n / k) * ctas, room = ctas <= 2 ? 148 : ctas == 4 ? 132 : 120;
+        const double part = 1 + 24.0 / (width * size);
+        const double cost = (double)((total + room - 1) / room) * ((rows + rows_t - 1) / rows_t * part + 12);
         if (!p.cluster[back] || cost < best) {
           best = cost;
           p.cluster[back] = true;
@@ -105,24 +110,28 @@ Plan make_plan(const sd_group_norm_cfg& c) {
         }
       }
     }
-    // A whole image in few CTAs (long rows, wide groups) leaves most of the GPU idle:
-    // then the two kernels' second read costs less.
+    // The two kernels, measured: 14 us and 0.5 us per MB of x, gradients 10.5 us and
+    // 0.93 us per MB. (16 x 256 rows x 1280: 14 us in clusters, 21 in two kernels; 2 x 16384 x
+    // 320: 35 and 25.)
     if (p.cluster[back]) {
-      const int64_t total = (int64_t)c.batch * (c.channels / p.width[back]) * p.ctas[back];
-      const int64_t vecs = (int64_t)c.batch * c.rows * (c.channels / vec);
-      if (total * 3 < kSms && vecs > (int64_t)kThreads * kSms) p.cluster[back] = false;
+      const double mb = 1e-6 * c.batch * c.rows * c.channels * size;
+      if (best * (back ? 0.7 : 0.5) > (back ? 10.5 + 0.93 * mb : 14 + 0.5 * mb)) p.cluster[back] = false;
     }
   }
-  // two CTAs per SM in all, four rows or more for each thread
-  const int cols = std::max(1, std::min(kThreads, c.channels / (wide ? vec : 1)));
-  const int64_t least = 4 * (int64_t)(kThreads / cols);
-  int64_t n = (kTargetCtas + c.batch - 1) / c.batch;
-  n = std::min<int64_t>(std::min<int64_t>(n, kMaxChunks), (c.rows + least - 1) / least);
-  n = std::max<int64_t>(n, 1);
-  p.chunk_rows = (c.rows + n - 1) / n;
-  p.chunks = (int)((c.rows + p.chunk_rows - 1) / p.chunk_rows);
-  p.pg_floats = p.cluster[0] && p.cluster[1] ? 0 : (size_t)c.batch * p.chunks * c.groups * 2;
-  p.pc_floats = (size_t)c.batch * (p.cluster[1] ? 1 : p.chunks) * c.channels * 2;
+  for (int back = 0; back < 2; ++back) {
+    // one wave of CTAs, four rows or more for each thread. Two CTAs per SM have too few
+    // registers for the loads under way (9216 x 320 x 4 forward: 31 us, one CTA 26), and a
+    // second wave pays the joins again (gradients: 41 us, 31 in one).
+    const int cols = std::max(1, std::min(kThreads, c.channels / (wide ? vec : 1)));
+    const int64_t least = 4 * (int64_t)(kThreads / cols);
+    int64_t n = kSms / c.batch;
+    n = std::max<int64_t>(std::min<int64_t>(n, (c.rows + least - 1) / least), 1);
+    p.chunk_rows[back] = (c.rows + n - 1) / n;
+    p.chunks[back] = (int)((c.rows + p.chunk_rows[back] - 1) / p.chunk_rows[back]);
+    if (!p.cluster[back])
+      p.pg_floats = std::max(p.pg_floats, (size_t)c.batch * p.chunks[back] * c.groups * 2);
+  }
+  p.pc_floats = (size_t)c.batch * (p.cluster[1] ? 1 : p.chunks[1]) * c.channels * 2;
   return p;
 }
 
@@ -297,6 +306,8 @@ __device__ __forceinline__ void reduce_rows(float* red, float* ch, int C, int c_
 }
 
 // ------------------------------------------------------------------ one slice per cluster
+// All of a thread's rows are asked for ahead (16 forward, 8 of both tensors backward)
+// straight into shared memory: with four in registers 4 x 9216 x 320 took 30 us, so 22.
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -318,6 +329,22 @@ __device__ __forceinline__ float peer_float(const float* p, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
   return v;
+}
+
+// 16 bytes from global to shared memory, without a register; a thread reads back only what
+// it asked for itself, so its own wait suffices.
+__device__ __forceinline__ void copy_async(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Rows that a thread takes of first, first + step, ... below end (a CTA's share: below 2^31).
+__device__ __forceinline__ int thread_rows(int64_t first, int64_t end, int step) {
+  return first < end ? ((int)(end - first) + step - 1) / step : 0;
 }
 
 struct Slice {
@@ -360,34 +387,35 @@ __global__ void __launch_bounds__(kThreads) gn_cluster_fwd_kernel(const __grid_c
   const T* x = static_cast<const T*>(a.x) + s.n * a.rows * a.ldx;
   const T* first = x + s.r0 * a.ldx + s.c0;
   const bool some = s.r0 < s.r1;
-  if (s.active) load_affine<T, V>(a, c, t);
   float k[V], s0[V], s1[V];
-  Groups gk(s.tx * V, a.cpg);
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const int g = gk.next();
-    k[j] = some && s.active ? -Elem<T>::to_f(first[g * a.cpg]) : 0.f;
-    s0[j] = s1[j] = 0.f;
-  }
+  for (int j = 0; j < V; ++j) s0[j] = s1[j] = 0.f;
   if (s.active) {
-    const T* p = x + c;
-    constexpr int U = 4;
-    int it = 0;
-    for (int64_t r = s.r0 + s.ty; r < s.r1; r += U * s.rows_t, it += U) {
-      uint4 raw[U];
+    constexpr int kAhead = 16;
+    const int n = thread_rows(s.r0 + s.ty, s.r1, s.rows_t);
+    const int64_t step = s.rows_t * a.ldx;
+    const T* p = x + (s.r0 + s.ty) * a.ldx + c;
+    uint4* own = tile + threadIdx.x;
+    for (int i = 0; i < kAhead; ++i, p += step) {
+      if (i < n) copy_async(own + i * kThreads, p);
+      copy_commit();
+    }
+    load_affine<T, V>(a, c, t);
+    Groups gk(s.tx * V, a.cpg);
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (r + u * s.rows_t < s.r1) raw[u] = *reinterpret_cast<const uint4*>(p + (r + u * s.rows_t) * a.ldx);
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (r + u * s.rows_t >= s.r1) break;
-        tile[(it + u) * kThreads + threadIdx.x] = raw[u];
-        float f[V];
-        unpack_vec<T, V>(raw[u], f);
-        v_add<V>(f, k, f);
-        v_add<V>(s0, f, s0);
-        v_fma<V>(f, f, s1, s1);
-      }
+    for (int j = 0; j < V; ++j) {
+      const int g = gk.next();
+      k[j] = some ? -Elem<T>::to_f(first[g * a.cpg]) : 0.f;
+    }
+    for (int i = 0; i < n; ++i, p += step) {
+      copy_wait<kAhead - 1>();
+      float f[V];
+      unpack_vec<T, V>(own[i * kThreads], f);
+      if (i + kAhead < n) copy_async(own + (i + kAhead) * kThreads, p);
+      copy_commit();
+      v_add<V>(f, k, f);
+      v_add<V>(s0, f, s0);
+      v_fma<V>(f, f, s1, s1);
     }
   }
   reduce_rows<V>(red, ch, a.width, 0, s.tx, s.ty, s.cols, s.rows_t, s.active, s0, s1);
@@ -476,30 +504,32 @@ __global__ void __launch_bounds__(kThreads) gn_cluster_bwd_kernel(const __grid_c
 #pragma unroll
   for (int j = 0; j < V; ++j) s0[j] = s1[j] = rs[j] = 0.f;
   if (s.active) {
+    constexpr int kAhead = 8;
+    const int n = thread_rows(s.r0 + s.ty, s.r1, s.rows_t);
+    const int64_t step_x = s.rows_t * a.ldx, step_y = s.rows_t * a.ldy;
+    const T *px = x + (s.r0 + s.ty) * a.ldx, *pd = dy + (s.r0 + s.ty) * a.ldy;
+    uint4 *own_x = tx_ + threadIdx.x, *own_d = td + threadIdx.x;
+    auto ask = [&](int i) {
+      if (i < n) {
+        copy_async(own_x + i * kThreads, px);
+        copy_async(own_d + i * kThreads, pd);
+      }
+      copy_commit();
+      px += step_x;
+      pd += step_y;
+    };
+    for (int i = 0; i < kAhead; ++i) ask(i);
     load_affine<T, V>(a, c, t);
     add_stats<V>(a.stats + s.n * a.G * 2, c, a.cpg, t, rs);
-    constexpr int U = 2;
-    int it = 0;
-    for (int64_t r = s.r0 + s.ty; r < s.r1; r += U * s.rows_t, it += U) {
-      uint4 rx[U], rd[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (r + u * s.rows_t < s.r1) {
-          rx[u] = *reinterpret_cast<const uint4*>(x + (r + u * s.rows_t) * a.ldx);
-          rd[u] = *reinterpret_cast<const uint4*>(dy + (r + u * s.rows_t) * a.ldy);
-        }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (r + u * s.rows_t >= s.r1) break;
-        tx_[(it + u) * kThreads + threadIdx.x] = rx[u];
-        td[(it + u) * kThreads + threadIdx.x] = rd[u];
-        float f[V], d[V];
-        unpack_vec<T, V>(rx[u], f);
-        unpack_vec<T, V>(rd[u], d);
-        grad_terms<V>(t, f, d, a.act);
-        v_add<V>(s0, d, s0);
-        v_fma<V>(d, f, s1, s1);
-      }
+    for (int i = 0; i < n; ++i) {
+      copy_wait<kAhead - 1>();
+      float f[V], d[V];
+      unpack_vec<T, V>(own_x[i * kThreads], f);
+      unpack_vec<T, V>(own_d[i * kThreads], d);
+      ask(i + kAhead);
+      grad_terms<V>(t, f, d, a.act);
+      v_add<V>(s0, d, s0);
+      v_fma<V>(d, f, s1, s1);
     }
   }
   v_mul<V>(s1, rs, s1);  // sum dz (x - mean) -> sum dz * xh
@@ -595,7 +625,7 @@ __global__ void __launch_bounds__(kThreads) gn_param_join_kernel(const __grid_co
 
 // Shares of the forward statistics: (mean, sum of squared deviations) per group.
 template <typename T, int V>
-__global__ void __launch_bounds__(kThreads, 2) gn_stats_share_kernel(const __grid_constant__ GnArgs a) {
+__global__ void __launch_bounds__(kThreads) gn_stats_share_kernel(const __grid_constant__ GnArgs a) {
   extern __shared__ float ch[];  // [2][C]
   __shared__ float red[2 * V * kThreads];
   pdl_wait();
@@ -622,23 +652,23 @@ __global__ void __launch_bounds__(kThreads, 2) gn_stats_share_kernel(const __gri
     }
     if (active) {
       constexpr int U = 8;
-      const T* p = x + c;
-      int64_t r = r0 + ty;
-      auto add = [&](const Raw<T, V>& raw) {
-        float f[V];
-        to_float<T, V>(raw, f);
-        v_add<V>(f, k, f);
-        v_add<V>(s0, f, s0);
-        v_fma<V>(f, f, s1, s1);
-      };
-      for (; r + (U - 1) * rows_t < r1; r += U * rows_t) {
+      const T* p = x + (r0 + ty) * a.ldx + c;
+      const int64_t step = rows_t * a.ldx;
+      for (int left = thread_rows(r0 + ty, r1, rows_t); left > 0; left -= U, p += U * step) {
         Raw<T, V> raw[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) raw[u] = load_raw<T, V>(p + (r + u * rows_t) * a.ldx);
+        for (int u = 0; u < U; ++u)
+          if (u < left) raw[u] = load_raw<T, V>(p + u * step);
 #pragma unroll
-        for (int u = 0; u < U; ++u) add(raw[u]);
+        for (int u = 0; u < U; ++u) {
+          if (u >= left) break;
+          float f[V];
+          to_float<T, V>(raw[u], f);
+          v_add<V>(f, k, f);
+          v_add<V>(s0, f, s0);
+          v_fma<V>(f, f, s1, s1);
+        }
       }
-      for (; r < r1; r += rows_t) add(load_raw<T, V>(p + r * a.ldx));
     }
     reduce_rows<V>(red, ch, a.C, c0 * V, tx, ty, cols_t, rows_t, active, s0, s1);
   }
@@ -655,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, 2) gn_stats_share_kernel(const __gri
     q = warp_sum(q);
     if (lane == 0) {
       const float d = s * inv;
-      float* o = a.pg + ((int64_t)blockIdx.x * a.G + g) * 2;
+      float* o = a.pg + ((n * a.G + g) * a.chunks + chunk) * 2;
       o[0] = Elem<T>::to_f(first[g * a.cpg]) + d;
       o[1] = fmaxf(q - s * d, 0.f);
     }
@@ -664,7 +694,7 @@ __global__ void __launch_bounds__(kThreads, 2) gn_stats_share_kernel(const __gri
 
 // y = act(z) from the joined shares; each CTA joins its image's shares itself.
 template <typename T, int V>
-__global__ void __launch_bounds__(kThreads, 2) gn_apply_kernel(const __grid_constant__ GnArgs a) {
+__global__ void __launch_bounds__(kThreads) gn_apply_kernel(const __grid_constant__ GnArgs a) {
   extern __shared__ float gs[];  // [G][2] mean, rstd
   pdl_wait();
   pdl_trigger();
@@ -679,7 +709,7 @@ __global__ void __launch_bounds__(kThreads, 2) gn_apply_kernel(const __grid_cons
 #pragma unroll
     for (int i = 0; i < kMaxChunks / 32; ++i) {
       const int p = i * 32 + lane;
-      s[i] = p < a.chunks ? pg[(int64_t)p * a.G + g] : make_float2(0.f, 0.f);
+      s[i] = p < a.chunks ? pg[(int64_t)g * a.chunks + p] : make_float2(0.f, 0.f);
       cnt[i] = p < a.chunks ? (float)(min(a.rows, (p + 1) * a.chunk_rows) - p * a.chunk_rows) / (float)a.rows : 0.f;
       m += cnt[i] * s[i].x;
     }
@@ -717,25 +747,23 @@ __global__ void __launch_bounds__(kThreads, 2) gn_apply_kernel(const __grid_cons
     add_stats<V>(gs, c, a.cpg, t, rs);
     // several rows are read before the first is written: y may be x, so the compiler
     // would not move a read across a write
-    constexpr int U = 4;
-    int64_t r = r1 - 1 - ty;
-    for (; r - (U - 1) * rows_t >= r0; r -= U * rows_t) {
+    constexpr int U = 8;
+    const int64_t last = r1 - 1 - ty, step_x = rows_t * a.ldx, step_y = rows_t * a.ldy;
+    const T* p = x + last * a.ldx + c;
+    T* o = y + last * a.ldy + c;
+    for (int left = thread_rows(r0 + ty, r1, rows_t); left > 0; left -= U, p -= U * step_x, o -= U * step_y) {
       Raw<T, V> raw[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) raw[u] = load_raw<T, V>(x + (r - u * rows_t) * a.ldx + c);
+      for (int u = 0; u < U; ++u)
+        if (u < left) raw[u] = load_raw<T, V>(p - u * step_x);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
+        if (u >= left) break;
         float f[V];
         to_float<T, V>(raw[u], f);
         normalise<V>(t, f, a.act);
-        store_v<T, V>(y + (r - u * rows_t) * a.ldy + c, f);
+        store_v<T, V>(o - u * step_y, f);
       }
-    }
-    for (; r >= r0; r -= rows_t) {
-      float f[V];
-      to_float<T, V>(load_raw<T, V>(x + r * a.ldx + c), f);
-      normalise<V>(t, f, a.act);
-      store_v<T, V>(y + r * a.ldy + c, f);
     }
   }
 }
@@ -771,26 +799,27 @@ __global__ void __launch_bounds__(kThreads) gn_grad_share_kernel(const __grid_co
       load_affine<T, V>(a, c, t);
       add_stats<V>(stats, c, a.cpg, t, rs);
       constexpr int U = 4;
-      int64_t r = r0 + ty;
-      auto add = [&](const Raw<T, V>& rx, const Raw<T, V>& rd) {
-        float f[V], d[V];
-        to_float<T, V>(rx, f);
-        to_float<T, V>(rd, d);
-        grad_terms<V>(t, f, d, a.act);
-        v_add<V>(s0, d, s0);
-        v_fma<V>(d, f, s1, s1);
-      };
-      for (; r + (U - 1) * rows_t < r1; r += U * rows_t) {
+      const int64_t step_x = rows_t * a.ldx, step_y = rows_t * a.ldy;
+      const T *px = x + (r0 + ty) * a.ldx + c, *pd = dy + (r0 + ty) * a.ldy + c;
+      for (int left = thread_rows(r0 + ty, r1, rows_t); left > 0; left -= U, px += U * step_x, pd += U * step_y) {
         Raw<T, V> rx[U], rd[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          rx[u] = load_raw<T, V>(x + (r + u * rows_t) * a.ldx + c);
-          rd[u] = load_raw<T, V>(dy + (r + u * rows_t) * a.ldy + c);
-        }
+        for (int u = 0; u < U; ++u)
+          if (u < left) {
+            rx[u] = load_raw<T, V>(px + u * step_x);
+            rd[u] = load_raw<T, V>(pd + u * step_y);
+          }
 #pragma unroll
-        for (int u = 0; u < U; ++u) add(rx[u], rd[u]);
+        for (int u = 0; u < U; ++u) {
+          if (u >= left) break;
+          float f[V], d[V];
+          to_float<T, V>(rx[u], f);
+          to_float<T, V>(rd[u], d);
+          grad_terms<V>(t, f, d, a.act);
+          v_add<V>(s0, d, s0);
+          v_fma<V>(d, f, s1, s1);
+        }
       }
-      for (; r < r1; r += rows_t) add(load_raw<T, V>(x + r * a.ldx + c), load_raw<T, V>(dy + r * a.ldy + c));
       v_mul<V>(s1, rs, s1);  // sum dz (x - mean) -> sum dz * xh
     }
     reduce_rows<V>(red, ch, a.C, c0 * V, tx, ty, cols_t, rows_t, active, s0, s1);
@@ -812,7 +841,7 @@ __global__ void __launch_bounds__(kThreads) gn_grad_share_kernel(const __grid_co
     s = warp_sum(s);
     q = warp_sum(q);
     if (lane == 0) {
-      float* o = a.pg + ((int64_t)blockIdx.x * a.G + g) * 2;
+      float* o = a.pg + ((n * a.G + g) * a.chunks + chunk) * 2;
       o[0] = s;
       o[1] = q;
     }
@@ -841,7 +870,7 @@ __global__ void __launch_bounds__(kThreads) gn_grad_apply_kernel(const __grid_co
 #pragma unroll
     for (int i = 0; i < kMaxChunks / 32; ++i) {
       const int p = i * 32 + lane;
-      const float2 v = p < a.chunks ? pg[(int64_t)p * a.G + g] : make_float2(0.f, 0.f);
+      const float2 v = p < a.chunks ? pg[(int64_t)g * a.chunks + p] : make_float2(0.f, 0.f);
       s += v.x;
       q += v.y;
     }
@@ -870,28 +899,30 @@ __global__ void __launch_bounds__(kThreads) gn_grad_apply_kernel(const __grid_co
     load_affine<T, V>(a, c, t);
     add_stats<V>(stats, c, a.cpg, t, rs);
     grad_cols<V>(gs, c, a.cpg, rs, k);
-    auto put = [&](const Raw<T, V>& rx, const Raw<T, V>& rd, int64_t r) {
-      float f[V], d[V];
-      to_float<T, V>(rx, f);
-      to_float<T, V>(rd, d);
-      grad_terms<V>(t, f, d, a.act);
-      grad_out<V>(t, k, f, d);
-      store_v<T, V>(dx + r * a.ldx + c, f);
-    };
     constexpr int U = 2;  // reads before writes, as above
-    int64_t r = r1 - 1 - ty;
-    for (; r - (U - 1) * rows_t >= r0; r -= U * rows_t) {
+    const int64_t last = r1 - 1 - ty, step_x = rows_t * a.ldx, step_y = rows_t * a.ldy;
+    const T *px = x + last * a.ldx + c, *pd = dy + last * a.ldy + c;
+    T* o = dx + last * a.ldx + c;
+    for (int left = thread_rows(r0 + ty, r1, rows_t); left > 0;
+         left -= U, px -= U * step_x, pd -= U * step_y, o -= U * step_x) {
       Raw<T, V> rx[U], rd[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        rx[u] = load_raw<T, V>(x + (r - u * rows_t) * a.ldx + c);
-        rd[u] = load_raw<T, V>(dy + (r - u * rows_t) * a.ldy + c);
-      }
+      for (int u = 0; u < U; ++u)
+        if (u < left) {
+          rx[u] = load_raw<T, V>(px - u * step_x);
+          rd[u] = load_raw<T, V>(pd - u * step_y);
+        }
 #pragma unroll
-      for (int u = 0; u < U; ++u) put(rx[u], rd[u], r - u * rows_t);
+      for (int u = 0; u < U; ++u) {
+        if (u >= left) break;
+        float f[V], d[V];
+        to_float<T, V>(rx[u], f);
+        to_float<T, V>(rd[u], d);
+        grad_terms<V>(t, f, d, a.act);
+        grad_out<V>(t, k, f, d);
+        store_v<T, V>(o - u * step_x, f);
+      }
     }
-    for (; r >= r0; r -= rows_t)
-      put(load_raw<T, V>(x + r * a.ldx + c), load_raw<T, V>(dy + r * a.ldy + c), r);
   }
 }
 
@@ -955,7 +986,7 @@ sd_status run_cluster(const sd_group_norm_cfg& c, GnArgs& a, const Plan& p, int 
 template <typename T, int V>
 sd_status run_pair(const sd_group_norm_cfg& c, GnArgs& a, const Plan& p, int back, const Device& dev, cudaStream_t st) {
   const size_t sums = (size_t)2 * c.channels * sizeof(float), gsum = (size_t)2 * c.groups * sizeof(float);
-  const unsigned ctas = (unsigned)(c.batch * (int64_t)p.chunks);
+  const unsigned ctas = (unsigned)(c.batch * (int64_t)p.chunks[back]);
   const double e = sizeof(T), n = (double)c.batch * c.rows * c.channels;
   if (!back) {
     OP_TRY((allow_smem<gn_stats_share_kernel<T, V>>(2 * kMaxChannels * sizeof(float), dev.index)));
@@ -995,7 +1026,7 @@ sd_status dispatch(const sd_group_norm_cfg& c, GnArgs& a, const Plan& p, int bac
   return run_type<float>(c, a, p, back, dev, st);
 }
 
-void fill(const sd_group_norm_cfg& c, const Plan& p, void* ws, GnArgs* a) {
+void fill(const sd_group_norm_cfg& c, const Plan& p, int back, void* ws, GnArgs* a) {
   memset(a, 0, sizeof(*a));
   a->batch = c.batch;
   a->rows = c.rows;
@@ -1006,8 +1037,8 @@ void fill(const sd_group_norm_cfg& c, const Plan& p, void* ws, GnArgs* a) {
   a->eps = c.eps;
   a->ldx = c.ld_x ? c.ld_x : c.channels;
   a->ldy = c.ld_y ? c.ld_y : c.channels;
-  a->chunks = p.chunks;
-  a->chunk_rows = p.chunk_rows;
+  a->chunks = p.chunks[back];
+  a->chunk_rows = p.chunk_rows[back];
   a->err = static_cast<int*>(ws);
   uint8_t* w = static_cast<uint8_t*>(ws) + kOpHeader;
   a->pg = reinterpret_cast<float*>(w);
@@ -1041,7 +1072,7 @@ sd_status sd_group_norm_fwd(const sd_group_norm_cfg* cfg, const void* x, const v
   const Plan p = make_plan(*cfg);
   OP_TRY(check_workspace(space(p), workspace, ws_bytes));
   GnArgs a;
-  fill(*cfg, p, workspace, &a);
+  fill(*cfg, p, 0, workspace, &a);
   a.x = x;
   a.gamma = gamma;
   a.beta = beta;
@@ -1069,7 +1100,7 @@ sd_status sd_group_norm_bwd(const sd_group_norm_cfg* cfg, const void* x, const v
   const Plan p = make_plan(*cfg);
   OP_TRY(check_workspace(space(p), workspace, ws_bytes));
   GnArgs a;
-  fill(*cfg, p, workspace, &a);
+  fill(*cfg, p, 1, workspace, &a);
   a.x = x;
   a.gamma = gamma;
   a.beta = beta;
