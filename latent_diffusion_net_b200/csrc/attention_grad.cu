@@ -48,7 +48,6 @@ struct GradArgs {
   AttnArgs f;
   int32_t qpad;         // query rows of lse2 and delta: a multiple of 128
   int32_t qblocks;      // 128-query tiles
-  int32_t units;        // attn_dq_kernel: query tiles x heads x sequences x splits
   float* nlse;          // [B][H][qpad] -lse in log2 units; -inf where a row sees nothing or does not exist
   float* ndelta;        // [B][H][qpad] -delta
   const float* lse;
@@ -57,8 +56,9 @@ struct GradArgs {
   float shift;
   int64_t s0[3], s1[3];      // output strides: dQ, or dK and dV
   void *out0, *out1;
-  float* part;               // [splits][...] FP32 parts
-  float* part_e;             // attn_dq_kernel with splits: row sums e [splits][B][H][qpad]
+  float* part;               // FP32 parts [2][slots][128][D]
+  float* part_e;             // attn_dq_kernel: their row sums e [slots][128]
+  int64_t slots;
 };
 
 struct __align__(64) GradMaps {
@@ -298,12 +298,12 @@ struct HeadWalk {
   KeyTiles v;
   TileWalk<KeyTiles> w;
   int hh, steps;
-  __device__ __forceinline__ HeadWalk(const KeyTiles& tiles, int G, int z, int splits) : v(tiles), w(tiles), hh(0) {
+  __device__ __forceinline__ HeadWalk(const KeyTiles& tiles, int G, const Part& part) : v(tiles), w(tiles), hh(0) {
     steps = INT32_MAX;
-    if (splits > 1) {
+    if (part.slot >= 0) {
       const int count = w.count();
-      const int64_t total = (int64_t)count * G, first = total * z / splits;
-      steps = (int)(total * (z + 1) / splits - first);
+      const int64_t total = (int64_t)count * G, first = part.begin(total);
+      steps = part.steps(total);
       if (steps > 0) {
         hh = (int)(first / count);
         w.skip((int)(first % count));
@@ -365,10 +365,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const DocRing docs{sdocs, doc_full, abort_flag, a.err};
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int z = blockIdx.x % a.splits, item = blockIdx.x / a.splits;
+  const Part own(a.parts, blockIdx.x);
   const int heads = a.B * a.KV;
-  const int kt = item / heads;  // the first key tiles first (with a causal mask they have the longest walks)
-  const int b = item % heads / a.KV, kv = item % heads % a.KV;
+  const int kt = own.item / heads;  // the first key tiles first (with a causal mask they have the longest walks)
+  const int b = own.item % heads / a.KV, kv = own.item % heads % a.KV;
   const int j0 = kt * kTile;
 
   if (threadIdx.x == 0) {
@@ -398,13 +398,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int nk = keys_of(a, b), off = nk - a.Nq, pre = prefix_of(a, b);
   if (warp == 16) {
-    HeadWalk walk(KeyTiles(a, b, kt, g.qblocks, off, nk, pre), a.G, z, a.splits);
+    HeadWalk walk(KeyTiles(a, b, kt, g.qblocks, off, nk, pre), a.G, own);
     bool ok = true, whole;
     int t = 0;
     for (int tile; ok && (tile = walk.step(a.G, whole)) >= 0; ++t) {
       if (lane == 0) {
         const int i0 = tile * kTile, s = t & 1, h = kv * a.G + walk.hh;
-        Record rec = {tile, whole ? kWhole : 0, 0, nk, pre, 0, b, h, i0, z, {0, 0}};
+        Record rec = {tile, whole ? kWhole : 0, 0, nk, pre, 0, b, h, i0, own.slot, {0, 0}};
         rec.flags |= walk.w.one_doc(tile, rec.doc);
         ok = ring.put(t, rec);
         if (ok && a.q_pad) docs.load(t, a.q_pad + ((int64_t)b * g.qblocks + tile) * kTile);
@@ -576,8 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t* os = which ? g.s1 : g.s0;
       T* dst = static_cast<T*>(which ? g.out1 : g.out0) + b * os[0] + j * os[1] + kv * os[2];
       float* part = nullptr;
-      if (a.splits > 1)
-        part = g.part + ((((int64_t)z * 2 + which) * heads + b * a.KV + kv) * a.ktiles * kTile + j) * a.D;
+      if (own.slot >= 0) part = g.part + ((which * g.slots + own.slot) * kTile + j - j0) * a.D;
       store_row<T, NB>((which ? tDv : tDk) + lane_off, cq & 1, t > 0, j < a.Nk, a.D, which ? g.v_scale : g.out_scale,
                        dst, part);
     }
@@ -588,14 +587,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 17) tmem_dealloc(tmem, 512);
 }
 
-// A unit of dq work: split z of 128 queries of one head, the last query tiles first.
+// A unit of dq work: a part of 128 queries of one head, the last query tiles first.
 struct DqUnit {
-  int z, b, h, i0, i1, qt;
-  __device__ __forceinline__ DqUnit(const GradArgs& g, int u) {
+  Part part;
+  int b, h, i0, i1, qt;
+  __device__ __forceinline__ DqUnit(const GradArgs& g, int u) : part(g.f.parts, u) {
     const AttnArgs& a = g.f;
-    z = u % a.splits;
-    const int item = u / a.splits, heads = a.B * a.H, at = item % heads;
-    qt = g.qblocks - 1 - item / heads;
+    const int heads = a.B * a.H, at = part.item % heads;
+    qt = g.qblocks - 1 - part.item / heads;
     b = at / a.H;
     h = at % a.H;
     i0 = qt * kTile;
@@ -608,10 +607,10 @@ struct DqWalk : TileWalk<RowTiles> {
       : TileWalk<RowTiles>(RowTiles(g.f, u.b, u.i0, u.i1, off, nk, pre,
                                     g.f.q_range + ((int64_t)u.b * g.qblocks + u.qt) * 2)) {
     steps = INT32_MAX;
-    if (g.f.splits > 1) {
-      const int n = count(), first = (int)((int64_t)n * u.z / g.f.splits);
-      steps = (int)((int64_t)n * (u.z + 1) / g.f.splits) - first;
-      if (steps > 0) skip(first);
+    if (u.part.slot >= 0) {
+      const int n = count();
+      steps = u.part.steps(n);
+      if (steps > 0) skip((int)u.part.begin(n));
     }
   }
   __device__ __forceinline__ int step(bool& whole) { return steps-- > 0 ? next(whole) : -1; }
@@ -621,17 +620,17 @@ struct DqWalk : TileWalk<RowTiles> {
 // corrected delta, or the parts of a split. Out of line: its registers would compete
 // with the loop's.
 template <typename T, int NB>
-__device__ __noinline__ void store_dq(const GradArgs& g, int b, int h, int i, int z, int side, uint32_t tDq, uint32_t tPk,
+__device__ __noinline__ void store_dq(const GradArgs& g, int b, int h, int i, int slot, int side, uint32_t tDq, uint32_t tPk,
                                       bool some, float e) {
   const AttnArgs& a = g.f;
   const bool valid = i < a.Nq;
   T* dst = static_cast<T*>(g.out0) + b * g.s0[0] + i * g.s0[1] + h * g.s0[2];
   const int64_t at = ((int64_t)b * a.H + h) * g.qpad + i;
-  if (a.splits > 1) {
-    const int64_t rows = (int64_t)a.B * a.H * g.qpad, at_row = z * rows + at;
-    store_row<T, NB>(tDq, side, some, valid, a.D, 1.f, dst, g.part + at_row * a.D);
-    store_row<T, NB>(tPk, side, some, valid, a.D, 1.f, dst, g.part + (a.splits * rows + at_row) * a.D);
-    if (valid && side == 0) g.part_e[at_row] = e;
+  if (slot >= 0) {
+    const int64_t row = (int64_t)slot * kTile + i % kTile;
+    store_row<T, NB>(tDq, side, some, valid, a.D, 1.f, dst, g.part + row * a.D);
+    store_row<T, NB>(tPk, side, some, valid, a.D, 1.f, dst, g.part + (g.slots * kTile + row) * a.D);
+    if (valid && side == 0) g.part_e[row] = e;
     return;
   }
   if (valid && side == 0) g.ndelta[at] -= e;
@@ -736,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         after = j >= 0 ? walk.step(whole_next) : -1;
         if (lane == 0) {
           Record rec = {j, first | (after < 0 ? kLast : 0) | (j >= 0 && whole ? kWhole : 0), x, nk, pre, 0, u.b, u.h, u.i0,
-                        u.z, {0, 0}};
+                        u.part.slot, {0, 0}};
           if (j >= 0) rec.flags |= walk.one_doc(j, rec.doc);
           ok = ring.put(r, rec);
           if (after < 0) {
@@ -972,7 +971,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // arrive at p_full only after that
         if (cq < 2) {
           const float e = (srow[row] + srow[kTile + row]) + (srow[2 * kTile + row] + srow[3 * kTile + row]);
-          store_dq<T, NB>(g, rec->b, rec->head, rec->i0 + row, rec->z, cq, tDq + lane_off, tPk + lane_off, some,
+          store_dq<T, NB>(g, rec->b, rec->head, rec->i0 + row, rec->slot, cq, tDq + lane_off, tPk + lane_off, some,
                           e * g.v_scale);
         }
         tc_fence_before();
@@ -986,39 +985,43 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 17) tmem_dealloc(tmem, 512);
 }
 
-// out = scale * sum of the parts, in order; eight head dimensions per thread. For dQ
-// (part_e given) the parts are dS K, and behind them P K, which the summed row error e
-// multiplies; delta is corrected by e.
+// out = scale * sum of the parts of the cut items, in order; eight head dimensions per
+// thread. For dQ (part_e given) the parts are dS K, and behind them P K, which the summed
+// row error e multiplies; delta is corrected by e.
 struct JoinArgs {
-  const float* part;   // [splits][sets][B][heads][rows_pad][D], or dQ: [2][splits][B][heads][rows_pad][D]
-  const float* part_e; // [splits][B][heads][rows_pad] or null
-  float* ndelta;       // [B][heads][rows_pad]
+  Parts parts;
+  const float* part;    // [2][slots][128][D]: dK and dV, or dS K and P K
+  const float* part_e;  // [slots][128], or null
+  float* ndelta;        // [B][heads][qpad]
   void* out[2];
-  int64_t s[2][3];
+  int64_t s[2][3], slots;
   float scale[2];
-  int32_t splits, sets, B, heads, rows, rows_pad, D;
+  int32_t sets, B, heads, rows, tiles, D;
 };
 template <typename T>
 __global__ void __launch_bounds__(256) attn_grad_join_kernel(const __grid_constant__ JoinArgs a) {
   pdl_wait();
   pdl_trigger();
   const int vecs = a.D / 8;
-  const int64_t n = (int64_t)a.sets * a.B * a.heads * a.rows * vecs;
-  const int64_t stride = (int64_t)a.sets * a.B * a.heads * a.rows_pad * a.D;
+  const int64_t n = (int64_t)a.sets * a.parts.count * kTile * vecs;
   for (int64_t x = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; x < n; x += (int64_t)gridDim.x * blockDim.x) {
-    const int d = (int)(x % vecs) * 8;
-    const int64_t r = x / vecs;
-    const int i = (int)(r % a.rows), h = (int)(r / a.rows % a.heads);
-    const int b = (int)(r / a.rows / a.heads % a.B), set = (int)(r / a.rows / a.heads / a.B);
-    const float* p = a.part + ((((int64_t)set * a.B + b) * a.heads + h) * a.rows_pad + i) * a.D + d;
+    const int d = (int)(x % vecs) * 8, row = (int)(x / vecs % kTile);
+    const int64_t nth = x / vecs / kTile;
+    const int set = nth >= a.parts.count, item = a.parts.first + (int)(nth - (set ? a.parts.count : 0));
+    const int grp = a.parts.group_of_item(item), parts = a.parts.parts[grp];
+    const int each = a.B * a.heads, b = item % each / a.heads, h = item % each % a.heads;
+    const int i = (a.part_e ? a.tiles - 1 - item / each : item / each) * kTile + row;
+    if (i >= a.rows) continue;
+    const int64_t at = ((int64_t)a.parts.slot[grp] + (int64_t)(item - a.parts.item[grp]) * parts) * kTile + row;
+    const int64_t step = (int64_t)kTile * a.D;
     float f[8];
     auto sum = [&](const float* q, float (&o)[8]) {
 #pragma unroll
       for (int u = 0; u < 8; ++u) o[u] = 0.f;
 #pragma unroll 4
-      for (int z = 0; z < a.splits; ++z) {
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(q + z * stride));
-        const float4 w = __ldcg(reinterpret_cast<const float4*>(q + z * stride) + 1);
+      for (int z = 0; z < parts; ++z) {
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(q + z * step));
+        const float4 w = __ldcg(reinterpret_cast<const float4*>(q + z * step) + 1);
         o[0] += v.x;
         o[1] += v.y;
         o[2] += v.z;
@@ -1029,15 +1032,15 @@ __global__ void __launch_bounds__(256) attn_grad_join_kernel(const __grid_consta
         o[7] += w.w;
       }
     };
-    sum(p, f);
+    const float* p = a.part + at * a.D + d;
+    sum(p + set * a.slots * step, f);
     if (a.part_e) {
-      const int64_t row = ((int64_t)b * a.heads + h) * a.rows_pad + i, rows = (int64_t)a.B * a.heads * a.rows_pad;
       float e = 0.f, k[8];
-      for (int z = 0; z < a.splits; ++z) e += __ldcg(a.part_e + z * rows + row);
-      sum(p + a.splits * stride, k);
+      for (int z = 0; z < parts; ++z) e += __ldcg(a.part_e + at + (int64_t)z * kTile);
+      sum(p + a.slots * step, k);
 #pragma unroll
       for (int u = 0; u < 8; ++u) f[u] = fmaf(-e, k[u], f[u]);
-      if (d == 0) a.ndelta[row] -= e;
+      if (d == 0) a.ndelta[((int64_t)b * a.heads + h) * a.tiles * kTile + i] -= e;
     }
 #pragma unroll
     for (int u = 0; u < 8; ++u) f[u] *= a.scale[set];
@@ -1049,35 +1052,64 @@ __global__ void __launch_bounds__(256) attn_grad_join_kernel(const __grid_consta
 // ------------------------------------------------------------------ host side
 
 struct GradPlan {
-  int qblocks, ktiles, qpad, dkv_splits, dq_splits;
-  int64_t dkv_items, dq_items;
+  int qblocks, ktiles, qpad;
+  Cut dkv, dq;
   size_t rows_bytes, part_bytes;
 };
+// Time in steps of one SM, which holds one CTA: units start longest first and the last ones
+// end about half the longest unit's steps after the average (of the cut ones, where the rest
+// are full rounds); a unit costs about one step more. Parts cost one more launch and their FP32 rows, written and joined at 2 TB/s (a step
+// takes about 2.1 us at head_dim 64, 2.6 at 128, 0.7 more for capped scores).
+Cut plan_cut(const sd_attention_cfg& c, int64_t items, double steps, double least, double total) {
+  const double step_us = (c.head_dim <= 64 ? 2.1 : 2.6) + (c.softcap > 0.f ? 0.7 : 0.0);
+  Cut best;
+  double best_t = 0;
+  auto offer = [&](const Cut& cut, double longest) {
+    longest = std::ceil(longest) + 1;
+    const double units = (double)cut.units;
+    double t = units <= kSms ? longest : std::max((total + units) / kSms + 0.5 * longest, longest);
+    if (cut.slots) t += (5.0 + cut.slots * kTile * c.head_dim * 16.0 / 2.0e6) / step_us;
+    if (best_t == 0 || t < best_t) {
+      best_t = t;
+      best = cut;
+    }
+  };
+  offer(cut_even(items, 1), steps);
+  // whole items with a causal mask, two or fewer for each SM: a long one meets a short one
+  if (c.causal && items > kSms && items <= 2 * kSms) {
+    const double second = steps - (steps - least) * kSms / items;
+    best_t = std::max(std::max(steps, 2 * second), total / kSms) + 1;
+  }
+  for (int s = 2; s <= kMaxSplits && 2 * s <= steps && items * s <= 16 * kSms; ++s) {
+    offer(cut_even(items, s), steps / s);
+    const int64_t rest = items % kSms;
+    if (!c.causal && items > kSms && rest && rest * s <= 2 * kSms) offer(cut_last(items, rest, s), steps / s);
+    if (c.causal && s <= kGroups) offer(cut_levels(items, s, steps, least), steps / s);
+  }
+  return best;
+}
 GradPlan plan_grad(const sd_attention_cfg& c) {
   GradPlan p;
   p.qblocks = (c.q_len + kTile - 1) / kTile;
   p.ktiles = (c.k_len + kTile - 1) / kTile;
   p.qpad = p.qblocks * kTile;
-  p.dkv_items = (int64_t)c.batch * c.kv_heads * p.ktiles;
-  p.dq_items = (int64_t)c.batch * c.heads * p.qblocks;
-  // split a walk while every part keeps two tiles and all parts fit on the GPU at once
-  const int64_t walk = (int64_t)(c.heads / c.kv_heads) * p.qblocks;
-  auto splits = [](int64_t items, int64_t steps) {
-    const int64_t s = std::min<int64_t>(std::min<int64_t>(kSms / std::max<int64_t>(items, 1), steps / 2), kMaxSplits);
-    return (int)std::max<int64_t>(s, 1);
-  };
-  p.dkv_splits = splits(p.dkv_items, walk);
-  p.dq_splits = splits(p.dq_items, p.ktiles);
+  const int64_t dkv_items = (int64_t)c.batch * c.kv_heads * p.ktiles, dq_items = (int64_t)c.batch * c.heads * p.qblocks;
+  const double walk = (double)(c.heads / c.kv_heads) * p.qblocks, nq = c.q_len, nk = c.k_len;
+  // with a causal mask the first key tiles see all queries, the last query tiles all keys
+  const double seen = !c.causal ? 1.0 : nq <= nk ? 1.0 - nq / (2.0 * std::max(nk, 1.0)) : nk / (2.0 * nq);
+  const double past = c.causal ? std::max(0.0, 1.0 - nk / std::max(nq, 1.0)) : 1.0;
+  const double before = c.causal ? std::max(0.0, 1.0 - nq / std::max(nk, 1.0)) : 1.0;
+  p.dkv = plan_cut(c, dkv_items, walk, walk * past, dkv_items * walk * seen);
+  p.dq = plan_cut(c, dq_items, p.ktiles, p.ktiles * before, (double)dq_items * p.ktiles * seen);
   p.rows_bytes = up256((size_t)c.batch * c.heads * p.qpad * 4);
-  const size_t dkv = p.dkv_splits > 1 ? (size_t)p.dkv_splits * 2 * p.dkv_items * kTile * c.head_dim * 4 : 0;
-  const size_t dq = p.dq_splits > 1 ? (size_t)p.dq_splits * p.dq_items * kTile * (2 * c.head_dim + 1) * 4 : 0;
-  p.part_bytes = up256(std::max(dkv, dq));
+  p.part_bytes = up256(std::max((size_t)p.dkv.slots * 2 * kTile * c.head_dim * 4,
+                                (size_t)p.dq.slots * kTile * (2 * c.head_dim + 1) * 4));
   return p;
 }
 
 template <typename T>
 sd_status join(AttnCall& c, JoinArgs& j) {
-  const int64_t n = (int64_t)j.sets * j.B * j.heads * j.rows * (j.D / 8);
+  const int64_t n = (int64_t)j.sets * j.parts.count * kTile * (j.D / 8);
   const unsigned blocks = (unsigned)std::min<int64_t>((n + 255) / 256, (int64_t)c.dev.sms * 8);
   return launched(launch_pdl(attn_grad_join_kernel<T>, dim3(blocks), dim3(256), 0, c.st, j));
 }
@@ -1138,9 +1170,9 @@ sd_status backward(AttnCall& c) {
   const bool shaped = g.f.cap_out != 0.f || g.f.slopes;
   if (s.q_len) {
     // dq first: it corrects delta
-    g.f.splits = p.dq_splits;
-    g.units = (int32_t)(p.dq_items * p.dq_splits);
-    g.part_e = g.part + (size_t)2 * p.dq_splits * p.dq_items * kTile * s.head_dim;
+    g.f.parts = j.parts = p.dq.parts;
+    g.slots = j.slots = p.dq.slots;
+    g.part_e = g.part + (size_t)2 * g.slots * kTile * s.head_dim;
     for (int i = 0; i < 3; ++i) g.s0[i] = j.s[0][i] = c.qs[i];
     g.out0 = j.out[0] = c.dq;
     auto* kernel = shaped ? attn_dq_kernel<T, NB, true> : attn_dq_kernel<T, NB, false>;
@@ -1151,16 +1183,15 @@ sd_status backward(AttnCall& c) {
     {
       sdp::Scope sc("attn_dq", sdp::F_ATTN, 2.0 * pairs * s.head_dim,
                     act * (3.0 * s.q_len * s.heads + 2.0 * s.k_len * s.kv_heads), c.st);
-      OP_TRY(launched(launch_pdl(kernel, dim3((unsigned)g.units), dim3(kThreads),
+      OP_TRY(launched(launch_pdl(kernel, dim3((unsigned)p.dq.units), dim3(kThreads),
                                  kDqSmem<NB>, c.st, maps, g)));
     }
-    if (p.dq_splits > 1) {
+    if (g.slots) {
       j.scale[0] = g.out_scale;
-      j.splits = p.dq_splits;
       j.sets = 1;
       j.heads = s.heads;
       j.rows = s.q_len;
-      j.rows_pad = p.qpad;
+      j.tiles = p.qblocks;
       j.part_e = g.part_e;
       j.ndelta = g.ndelta;
       sdp::Scope sc("attn_grad_join", sdp::F_OTHER, 0, 0, c.st);
@@ -1168,7 +1199,8 @@ sd_status backward(AttnCall& c) {
     }
   }
   if (s.k_len) {
-    g.f.splits = p.dkv_splits;
+    g.f.parts = j.parts = p.dkv.parts;
+    g.slots = j.slots = p.dkv.slots;
     for (int i = 0; i < 3; ++i) {
       g.s0[i] = j.s[0][i] = c.ks[i];
       g.s1[i] = j.s[1][i] = c.vs[i];
@@ -1183,18 +1215,17 @@ sd_status backward(AttnCall& c) {
     {
       sdp::Scope sc("attn_dkv", sdp::F_ATTN, 8.0 * pairs * s.head_dim,
                     act * (2.0 * s.q_len * s.heads + 4.0 * s.k_len * s.kv_heads), c.st);
-      OP_TRY(launched(launch_pdl(kernel, dim3((unsigned)(p.dkv_items * p.dkv_splits)), dim3(kThreads),
+      OP_TRY(launched(launch_pdl(kernel, dim3((unsigned)p.dkv.units), dim3(kThreads),
                                  kDkvSmem<NB>, c.st, maps, g)));
     }
-    if (p.dkv_splits > 1) {
+    if (g.slots) {
       j.scale[0] = g.out_scale;
       j.scale[1] = g.v_scale;
-      j.splits = p.dkv_splits;
       j.sets = 2;
       j.part_e = nullptr;
       j.heads = s.kv_heads;
       j.rows = s.k_len;
-      j.rows_pad = p.ktiles * kTile;
+      j.tiles = p.ktiles;
       sdp::Scope sc("attn_grad_join", sdp::F_OTHER, 0, 0, c.st);
       OP_TRY(join<T>(c, j));
     }

@@ -58,15 +58,14 @@ struct __align__(64) FwdMaps {
   CUtensorMap q, k, v;
 };
 
-// A unit of work: split z of 128 query rows. The last query tiles come first (with
+// A unit of work: a part of 128 query rows. The last query tiles come first (with
 // a causal mask they are the longest).
 struct Unit {
-  int item, z, b, kv, i0, i1, qt;
-  __device__ __forceinline__ Unit(const AttnArgs& a, int u) {
-    z = u % a.splits;
-    item = u / a.splits;
-    const int heads = a.B * a.KV, at = item % heads;
-    qt = a.qtiles - 1 - item / heads;
+  Part part;
+  int b, kv, i0, i1, qt;
+  __device__ __forceinline__ Unit(const AttnArgs& a, int u) : part(a.parts, u) {
+    const int heads = a.B * a.KV, at = part.item % heads;
+    qt = a.qtiles - 1 - part.item / heads;
     b = at / a.KV;
     kv = at % a.KV;
     i0 = qt * a.tq;
@@ -82,10 +81,10 @@ struct UnitWalk : TileWalk<RowTiles> {
   __device__ __forceinline__ UnitWalk(const AttnArgs& a, const Unit& u, int off, int nk, int pre)
       : TileWalk<RowTiles>(RowTiles(a, u.b, u.i0, u.i1, off, nk, pre, u.docs(a))) {
     steps = INT32_MAX;
-    if (a.splits > 1) {
-      const int n = count(), first = (int)((int64_t)n * u.z / a.splits);
-      steps = (int)((int64_t)n * (u.z + 1) / a.splits) - first;
-      if (steps > 0) skip(first);
+    if (u.part.slot >= 0) {
+      const int n = count();
+      steps = u.part.steps(n);
+      if (steps > 0) skip((int)u.part.begin(n));
     }
   }
   __device__ __forceinline__ int step(bool& whole) { return steps-- > 0 ? next(whole) : -1; }
@@ -95,9 +94,9 @@ struct UnitWalk : TileWalk<RowTiles> {
 // of a split. Out of line: it runs once per unit and its registers would compete with
 // the score row of the loop.
 template <typename T, int NB>
-__device__ __noinline__ void store_rows(const AttnArgs& a, int64_t slot, int b, int i, int h, int half, uint32_t tO,
+__device__ __noinline__ void store_rows(const AttnArgs& a, int64_t at, int b, int i, int h, int half, uint32_t tO,
                                         bool some, bool valid, float m, float l) {
-  const bool part = a.splits > 1;
+  const bool part = at >= 0;
   const float inv = l > 0.f ? 1.f / l : 0.f;
   T* dst = static_cast<T*>(a.o) + b * a.os[0] + i * a.os[1] + h * a.os[2];
 #pragma unroll 1
@@ -113,7 +112,7 @@ __device__ __noinline__ void store_rows(const AttnArgs& a, int64_t slot, int b, 
       for (int q = 0; q < 32; ++q) r[q] = 0u;
     }
     if (valid && part && some) {
-      float4* p = reinterpret_cast<float4*>(a.partial + slot * a.D + c);
+      float4* p = reinterpret_cast<float4*>(a.partial + at * a.D + c);
 #pragma unroll
       for (int q = 0; q < 8; ++q)
         if (c + 4 * q < a.D)
@@ -133,8 +132,8 @@ __device__ __noinline__ void store_rows(const AttnArgs& a, int64_t slot, int b, 
   }
   if (half) return;
   if (valid && part) {
-    a.partial_ml[slot * 2] = m;
-    a.partial_ml[slot * 2 + 1] = l;
+    a.partial_ml[at * 2] = m;
+    a.partial_ml[at * 2 + 1] = l;
   } else if (valid && a.lse) {
     a.lse[((int64_t)b * a.H + h) * a.Nq + i] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
   }
@@ -211,8 +210,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       do {
         after = j >= 0 ? walk.step(whole_next) : -1;
         if (lane == 0) {
-          Record rec = {j, first | (after < 0 ? kLast : 0) | (j >= 0 && whole ? kWhole : 0), u.item, nk, pre, 0, u.b,
-                        u.kv, u.i0, u.z, {0, 0}};
+          Record rec = {j, first | (after < 0 ? kLast : 0) | (j >= 0 && whole ? kWhole : 0), x, nk, pre, 0, u.b,
+                        u.kv, u.i0, u.part.slot, {0, 0}};
           if (j >= 0) rec.flags |= walk.one_doc(j, rec.doc);
           ok = ring.put(r, rec);
           if (after < 0) {
@@ -531,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           asm volatile("bar.sync %0, 64;" ::"r"(1 + q4) : "memory");
           l += sm[(half ^ 1) * kTile + row];
           asm volatile("bar.sync %0, 64;" ::"r"(1 + q4) : "memory");
-          store_rows<T, NB>(a, ((int64_t)rec->unit * a.splits + rec->z) * kTile + row, rec->b, rec->i0 + row_i,
+          store_rows<T, NB>(a, rec->slot < 0 ? -1 : (int64_t)rec->slot * kTile + row, rec->b, rec->i0 + row_i,
                             rec->head * a.G + row_h, half, tOr, some, valid, m, l);
         }
         tc_fence_before();
@@ -545,55 +544,60 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (warp == 9) tmem_dealloc(tmem, 256);
 }
 
-// Joins the parts of split items, one warp per query row: m = max m_z, o = sum
-// 2^(m_z - m) O_z / sum 2^(m_z - m) l_z, over z in order.
-template <typename T>
-__global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ AttnArgs a) {
+// Joins the parts of cut items: m = max m_z, o = sum 2^(m_z - m) O_z / sum 2^(m_z - m) l_z,
+// over z in order, eight parts at a time whose loads are all under way at once. LANES lanes
+// per query row, 16 bytes each.
+template <typename T, int LANES>
+__global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ AttnArgs a) {
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31;
-  const int64_t r = blockIdx.x * (int64_t)4 + (threadIdx.x >> 5);
-  if (r >= (int64_t)a.B * a.H * a.Nq) return;
-  const int i = (int)(r % a.Nq), h = (int)(r / a.Nq % a.H), b = (int)(r / a.Nq / a.H);
-  const int kv = h / a.G;
-  const int64_t item = (int64_t)(a.qtiles - 1 - i / a.tq) * (a.B * a.KV) + b * a.KV + kv;
-  const int64_t slot = item * a.splits * kTile + (i % a.tq) * a.G + h % a.G;
-  float mz[2], lz[2];
-  float m = -INFINITY;
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {  // at most 64 parts
-    const int z = u * 32 + lane;
-    mz[u] = -INFINITY;
-    lz[u] = 0.f;
-    if (z < a.splits) {
-      const float2 v = *reinterpret_cast<const float2*>(a.partial_ml + (slot + (int64_t)z * kTile) * 2);
-      mz[u] = v.x;
-      lz[u] = v.y;
-    }
-    m = fmaxf(m, mz[u]);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  float w[2], l = 0.f;
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    w[u] = mz[u] == -INFINITY ? 0.f : fast_ex2(mz[u] - m);
-    l += w[u] * lz[u];
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  const int lane = threadIdx.x % LANES;
+  const int64_t r = blockIdx.x * (int64_t)(256 / LANES) + threadIdx.x / LANES;
+  const int rows = min(a.tq, a.Nq) * a.G;  // of an item, at most
+  const int64_t nth = r / rows;
+  if (nth >= a.parts.count) return;
+  const int row = (int)(r % rows), item = a.parts.first + (int)nth;
+  const int g = a.parts.group_of_item(item), parts = a.parts.parts[g];
+  const int heads = a.B * a.KV, qt = a.qtiles - 1 - item / heads, b = item % heads / a.KV, kv = item % heads % a.KV;
+  const int i = qt * a.tq + row / a.G, h = kv * a.G + row % a.G;
+  if (i >= a.Nq) return;
+  const int64_t at = ((int64_t)a.parts.slot[g] + (int64_t)(item - a.parts.item[g]) * parts) * kTile + row;
+  const float* pml = a.partial_ml + at * 2;
+  const float* po = a.partial + at * a.D + lane * 4;
   const bool in = lane * 4 < a.D;
-#pragma unroll 4
-  for (int z = 0; z < a.splits; ++z) {
-    const float f = __shfl_sync(0xffffffffu, z < 32 ? w[0] : w[1], z & 31);
-    if (f != 0.f && in) {  // a part that saw no key holds no values
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(a.partial + (slot + (int64_t)z * kTile) * a.D) + lane);
-      acc[0] = fmaf(f, v.x, acc[0]);
-      acc[1] = fmaf(f, v.y, acc[1]);
-      acc[2] = fmaf(f, v.z, acc[2]);
-      acc[3] = fmaf(f, v.w, acc[3]);
+  float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+  constexpr int U = 8;
+  for (int z0 = 0; z0 < parts; z0 += U) {
+    float2 ml[U];
+    float4 v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      ml[u] = make_float2(-INFINITY, 0.f);
+      v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (z0 + u < parts) {
+        ml[u] = __ldcg(reinterpret_cast<const float2*>(pml + (int64_t)(z0 + u) * kTile * 2));
+        if (in) v[u] = __ldcg(reinterpret_cast<const float4*>(po + (int64_t)(z0 + u) * kTile * a.D));
+      }
     }
+    float top = m;
+#pragma unroll
+    for (int u = 0; u < U; ++u) top = fmaxf(top, ml[u].x);
+    if (top == -INFINITY) continue;
+    const float keep = fast_ex2(m - top);
+    m = top;
+    l *= keep;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) acc[x] *= keep;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (ml[u].x != -INFINITY) {  // a part that saw no key holds no values
+        const float f = fast_ex2(ml[u].x - top);
+        l = fmaf(f, ml[u].y, l);
+        acc[0] = fmaf(f, v[u].x, acc[0]);
+        acc[1] = fmaf(f, v[u].y, acc[1]);
+        acc[2] = fmaf(f, v[u].z, acc[2]);
+        acc[3] = fmaf(f, v[u].w, acc[3]);
+      }
   }
   const float inv = l > 0.f ? 1.f / l : 0.f;
   if (in) {
@@ -642,8 +646,9 @@ __global__ void __launch_bounds__(128) attn_doc_range_kernel(const __grid_consta
 int tiles_of(int n) { return (n + kTile - 1) / kTile; }
 
 struct FwdPlan {
-  int tq, qtiles, ktiles, splits;
+  int tq, qtiles, ktiles;
   int64_t items;
+  Cut cut;
 };
 FwdPlan plan_forward(const sd_attention_cfg& c) {
   FwdPlan p;
@@ -652,29 +657,48 @@ FwdPlan plan_forward(const sd_attention_cfg& c) {
   p.qtiles = (c.q_len + p.tq - 1) / p.tq;
   p.ktiles = tiles_of(c.k_len);
   p.items = (int64_t)c.batch * c.kv_heads * p.qtiles;
-  // Time in key tiles of one SM for 1, 2, ... splits of every item. Two CTAs share an SM
-  // and take turns (measured: 1.2 us a tile and SM at head_dim 64, 1.5 at 128, 0.8 more for
-  // capped or biased scores; a CTA alone needs 1.25 or 1.8 of that). Units start longest first, so
-  // the last ones end about half the longest unit's tiles after the average; parts cost
-  // one more launch and their FP32 rows, written and joined at 1.3 TB/s.
-  const double nq = c.q_len, nk = c.k_len;
-  const double seen = !c.causal ? 1.0 : nq <= nk ? 1.0 - nq / (2.0 * std::max(nk, 1.0)) : nk / (2.0 * nq);
-  const double total = (double)p.items * p.ktiles * seen / kSms;
+  // Time in key tiles of one SM. Two CTAs share an SM and take turns (measured: 1.2 us a
+  // tile and SM at head_dim 64, 1.5 at 128, 0.8 more for capped or biased scores; a CTA
+  // alone needs 1.25 or 1.8 of that). Units start longest first, so the last ones end about
+  // half the longest unit's tiles after the average (of the cut ones, where the rest are
+  // full rounds); parts cost one more launch and their
+  // FP32 rows, written and joined at 2 TB/s.
+  const double nq = c.q_len, nk = c.k_len, L = p.ktiles, N = (double)p.items;
+  const double least = !c.causal ? L : std::max(0.0, L - nq / kTile);  // tiles of the shortest item
+  const double total = N * (c.causal && nq > nk ? 0.5 * L * nk / nq : 0.5 * (L + least)) / kSms;
   const double tile_us = (c.head_dim <= 64 ? 1.2 : 1.5) + (c.softcap > 0.f ? 0.8 : 0.0);
   const double alone = c.head_dim <= 64 ? 1.25 : 1.8;
-  const double rows = (double)c.batch * c.heads * nq;
+  const double part_tiles = std::min<double>(p.tq, nq) * g * (c.head_dim + 2) * 8.0 / 2.0e6 / tile_us;
   double best = 0;
-  p.splits = 1;
-  for (int s = 1; s <= std::min(kMaxSplits, std::max(p.ktiles, 1)); ++s) {
+  // units of at most `longest` tiles, the 149th longest has `second`
+  auto offer = [&](const Cut& cut, double longest, double second) {
+    const double units = (double)cut.units;
     // one more tile's time for beginning and ending a unit
-    const double units = (double)p.items * s, longest = 1 + (p.ktiles + s - 1) / s;
-    double t = units <= kSms ? alone * longest : std::max(total + units / kSms + 0.5 * longest, alone * longest);
-    if (s > 1) t += (3.0 + rows * s * (c.head_dim + 2) * 8.0 / 1.3e6) / tile_us;
-    if (s == 1 || t < best) {
+    longest += 1, second += 1;
+    double t = units <= kSms       ? alone * longest
+               : units <= 2 * kSms ? 2 * second + alone * (longest - second)
+                                   : std::max(total + units / kSms + 0.5 * longest, alone * longest);
+    if (cut.slots) t += 5.0 / tile_us + cut.slots * part_tiles;
+    if (best == 0 || t < best) {
       best = t;
-      p.splits = s;
+      p.cut = cut;
     }
-    if (units > 16.0 * kSms) break;
+  };
+  for (int s = 1; s <= std::min(kMaxSplits, std::max(p.ktiles, 1)); ++s) {
+    const double at = c.causal ? std::max(0.0, 1.0 - kSms / (N * s)) : 1.0;
+    offer(cut_even(p.items, s), std::ceil(L / s), std::ceil((least + (L - least) * at) / s));
+    if (N * s > 16.0 * kSms) break;
+  }
+  if (!c.causal) {
+    // the items beyond full rounds of the GPU in parts: they end together
+    const int64_t rest = p.items % (2 * kSms);
+    if (p.items > 2 * kSms && rest)
+      for (int s = 2; s <= std::min(kMaxSplits, p.ktiles) && rest * s <= 2 * kSms; ++s)
+        offer(cut_last(p.items, rest, s), std::ceil(L / s), std::ceil(L / s));
+  } else {
+    // items in parts of at most 1/k of the longest: short ones whole
+    for (int k = 2; k <= std::min(kGroups, p.ktiles); ++k)
+      offer(cut_levels(p.items, k, L, least), std::ceil(L / k), std::ceil(L / k));
   }
   return p;
 }
@@ -695,8 +719,7 @@ DocSpace doc_space(const sd_attention_cfg& c) {
 }
 size_t ranges_bytes(const sd_attention_cfg& c) { return doc_space(c).bytes; }
 size_t parts_bytes(const sd_attention_cfg& c) {
-  const FwdPlan p = plan_forward(c);
-  return p.splits > 1 ? up256((size_t)p.items * p.splits * kTile * (c.head_dim + 2) * 4) : 0;
+  return up256((size_t)plan_forward(c).cut.slots * kTile * (c.head_dim + 2) * 4);
 }
 
 bool strides_ok(const int64_t* s, int batch, int tokens, int heads, int d, int64_t* out) {
@@ -727,7 +750,8 @@ sd_status check(const sd_attention_cfg* c, AttnCall* call) {
       c->k_len > 1 << 20 || (c->dtype != SD_DTYPE_BF16 && c->dtype != SD_DTYPE_F16))
     return SD_ERR_UNSUPPORTED;
   // CTA and row counts within a grid's x extent
-  if ((int64_t)c->batch * c->heads > 1 << 24 || (int64_t)c->batch * c->heads * std::max(c->q_len, 1) > (int64_t)1 << 32)
+  if ((int64_t)c->batch * c->heads > 1 << 24 || (int64_t)c->batch * c->heads * std::max(c->q_len, 1) > (int64_t)1 << 32 ||
+      (int64_t)c->batch * c->kv_heads * std::max(c->k_len, 1) > (int64_t)1 << 36)
     return SD_ERR_UNSUPPORTED;
   if (!strides_ok(c->q_stride, c->batch, c->q_len, c->heads, c->head_dim, call->qs) ||
       !strides_ok(c->k_stride, c->batch, c->k_len, c->kv_heads, c->head_dim, call->ks) ||
@@ -767,12 +791,14 @@ sd_status forward(AttnCall& c, const FwdPlan& p) {
   auto* kernel = shaped ? attn_fwd_kernel<T, NB, true> : attn_fwd_kernel<T, NB, false>;
   const double pairs = (double)g.batch * g.heads * g.q_len * g.k_len;
   const double bytes = 2.0 * g.batch * g.head_dim * (2.0 * g.q_len * g.heads + 2.0 * g.k_len * g.kv_heads);
-  sdp::Scope sc("attn_fwd", sdp::F_ATTN, 4.0 * pairs * g.head_dim, bytes, c.st, p.splits > 1 ? 2 : 1);
-  OP_TRY(launched(launch_pdl(kernel, dim3((unsigned)a.units), dim3(kThreads),
+  sdp::Scope sc("attn_fwd", sdp::F_ATTN, 4.0 * pairs * g.head_dim, bytes, c.st, p.cut.slots ? 2 : 1);
+  OP_TRY(launched(launch_pdl(kernel, dim3((unsigned)p.cut.units), dim3(kThreads),
                              Shape<NB>::kSmem, c.st, maps, a)));
-  if (p.splits == 1) return SD_OK;
-  const int64_t rows = (int64_t)g.batch * g.heads * g.q_len;
-  return launched(launch_pdl(attn_join_kernel<T>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, c.st, a));
+  if (!p.cut.slots) return SD_OK;
+  constexpr int kLanes = NB == 1 ? 16 : 32;
+  const int64_t rows = (int64_t)p.cut.parts.count * std::min(p.tq, g.q_len) * a.G, per = 256 / kLanes;
+  return launched(
+      launch_pdl(attn_join_kernel<T, kLanes>, dim3((unsigned)((rows + per - 1) / per)), dim3(256), 0, c.st, a));
 }
 
 }  // namespace
@@ -884,14 +910,13 @@ sd_status sd_attention_fwd(const sd_attention_cfg* cfg, const void* q, const voi
   AttnArgs& a = c.args;
   a.tq = p.tq;
   a.qtiles = p.qtiles;
-  a.splits = p.splits;
-  a.units = (int32_t)(p.items * p.splits);
+  a.parts = p.cut.parts;
   a.o = o;
   a.lse = lse;
   a.clear_err = 1;
-  if (p.splits > 1) {
+  if (p.cut.slots) {
     a.partial = reinterpret_cast<float*>(c.ws + kOpHeader + ranges_bytes(*cfg));
-    a.partial_ml = a.partial + (size_t)p.items * p.splits * kTile * cfg->head_dim;
+    a.partial_ml = a.partial + (size_t)p.cut.slots * kTile * cfg->head_dim;
   }
   if (cfg->k_len == 0) {
     shaped.k_len = 1;  // a map has no empty dimension; no tile of it is visited

@@ -3,6 +3,8 @@
 // cap and distance bias.
 #pragma once
 
+#include <string.h>
+
 #include "op_tma.cuh"
 
 namespace sdo {
@@ -10,11 +12,52 @@ namespace sdo {
 constexpr int kTile = 128;                       // query rows and keys per tile
 constexpr int kBlockBytes = kTile * 64 * 2;      // 128 rows x 64 head dimensions, swizzled
 
+// How items of work (query tiles, key tiles) are cut into units: groups of consecutive
+// items, each item of a group into the same number of parts. Parts of cut items have
+// slots in the scratch, in unit order; cut items are consecutive over the groups.
+constexpr int kGroups = 8;
+struct Parts {
+  int32_t n;               // groups
+  int32_t item[kGroups];   // first item of each
+  int32_t unit[kGroups];   // first unit
+  int32_t parts[kGroups];  // of an item
+  int32_t slot[kGroups];   // first slot, where parts > 1
+  int32_t first, count;    // the cut items
+  __device__ __forceinline__ int group_of_item(int i) const {
+    int g = 0;
+    while (g + 1 < n && i >= item[g + 1]) ++g;
+    return g;
+  }
+};
+// Part z of `parts` of an item; its slot, or -1 where the item is not cut.
+struct Part {
+  int item, z, parts, slot;
+  __device__ __forceinline__ Part(const Parts& p, int u) {
+    int g = 0;
+    while (g + 1 < p.n && u >= p.unit[g + 1]) ++g;
+    parts = p.parts[g];
+    const int at = u - p.unit[g];
+    item = p.item[g] + at;
+    z = 0;
+    slot = -1;
+    if (parts > 1) {
+      item = p.item[g] + at / parts;
+      z = at % parts;
+      slot = p.slot[g] + at;
+    }
+  }
+  // the first of `count` steps that are this part's, and how many
+  __device__ __forceinline__ int64_t begin(int64_t count) const { return count * z / parts; }
+  __device__ __forceinline__ int steps(int64_t count) const {
+    return (int)(count * (z + 1) / parts - begin(count));
+  }
+};
+
 struct AttnArgs {
   int32_t B, Nq, Nk, H, KV, G, D;   // G = H / KV query heads per key head
   int32_t tq;                       // forward: query tokens of a tile (kTile / G, all G heads of each)
-  int32_t qtiles, ktiles, splits;
-  int32_t units;                    // forward: query tiles x key heads x sequences x splits
+  int32_t qtiles, ktiles;
+  Parts parts;                      // forward: items are query tiles x key heads x sequences
   int32_t causal;
   float sl2;                        // scale * log2(e)
   float cap_in, cap_out;            // tanh(s * cap_in) * cap_out = capped score in log2 units; cap_out 0 = no cap
@@ -26,7 +69,7 @@ struct AttnArgs {
   int64_t os[3];
   void* o;
   float* lse;
-  float* partial;                   // forward split: [items][splits][128][D], then max and sum [items][splits][128][2]
+  float* partial;                   // forward: [slots][128][D], then max and sum [slots][128][2]
   float* partial_ml;
   int* err;
   int32_t clear_err;
@@ -151,7 +194,7 @@ struct TileWalk {
 struct alignas(16) Record {
   int32_t tile, flags, unit, nk;  // nk, pre: keys_of, prefix_of the unit's sequence
   int32_t pre, doc, b, head;      // doc: with kOneDoc; head: of the unit (key head forward)
-  int32_t i0, z, pad[2];          // first query of the unit, its part of a split
+  int32_t i0, slot, pad[2];       // first query of the unit; slot of its part, or -1
 };
 constexpr int kRing = 4;
 struct RecordRing {
@@ -258,6 +301,53 @@ __device__ __forceinline__ float max3f(float a, float b, float c) {
 }
 
 // Launches of the backward pass (attention_grad.cu).
+// Ways to cut items (host side).
+struct Cut {
+  Parts parts;
+  int64_t units, slots;
+  Cut() {
+    memset(this, 0, sizeof(*this));
+  }
+  void add(int64_t items, int n) {
+    if (items <= 0) return;
+    const int g = parts.n++;
+    parts.item[g] = g ? parts.item[g - 1] + (int32_t)((units - parts.unit[g - 1]) / parts.parts[g - 1]) : 0;
+    parts.unit[g] = (int32_t)units;
+    parts.parts[g] = n;
+    parts.slot[g] = (int32_t)slots;
+    units += items * n;
+    if (n == 1) return;
+    if (!slots) parts.first = parts.item[g];
+    parts.count += (int32_t)items;
+    slots += items * n;
+  }
+};
+inline Cut cut_even(int64_t items, int n) {
+  Cut c;
+  c.add(items, n);
+  return c;
+}
+// the last `rest` items
+inline Cut cut_last(int64_t items, int64_t rest, int n) {
+  Cut c;
+  c.add(items - rest, 1);
+  c.add(rest, n);
+  return c;
+}
+// Items whose lengths fall evenly from `longest` to `least`: parts of at most 1 / k of the
+// longest (k <= kGroups).
+inline Cut cut_levels(int64_t items, int k, double longest, double least) {
+  Cut c;
+  int64_t done = 0;
+  for (int n = k; n >= 1; --n) {
+    const double to = longest > least ? (longest - longest * (n - 1) / k) / (longest - least) : 1.0;
+    const int64_t end = n == 1 ? items : (int64_t)(items * (to < 1.0 ? to : 1.0));
+    if (end > done) c.add(end - done, n);
+    done = end > done ? end : done;
+  }
+  return c;
+}
+
 struct AttnCall {
   const sd_attention_cfg* cfg;
   int64_t qs[3], ks[3], vs[3], os[3];
