@@ -322,3 +322,20 @@ def test_empty_tiles_between_documents():
     kd = i32([[0] * 100 + [1] * 200 + [2] * 90 + [3] * 300] * 3)
     for d in (64, 128):
         check(3, 684, 690, 60, 60, d, seed=30 + d, q_doc=qd, k_doc=kd)
+
+
+def test_items_cut_by_group():
+    """More query and key tiles than the GPU holds at once, not a multiple: the last ones are computed in parts. The
+    documents leave some of the parts without a visible tile, and the last sequence's keys end early."""
+    qd = i32([[0] * 700 + [1] * 708])
+    kd = i32([[0] * 600 + [1] * 3300 + [2] * 196])
+    check(1, 1408, 4096, 30, 30, 64, seed=41)
+    check(1, 1408, 4096, 30, 30, 64, seed=42, backward=False, q_doc=qd, k_doc=kd)
+    check(1, 4000, 1408, 30, 30, 40, seed=43, k_lens=i32([1300]))
+
+
+@pytest.mark.parametrize("d", [64, 80])
+def test_long_walks_cut_shorter(d):
+    """A causal mask with few items of unequal lengths: the longest are computed in two to eight parts."""
+    check(2, 2047, 2047, 8, 2, d, seed=44, causal=True, prefix=i32([300, 0]), slopes=torch.linspace(0.01, 0.2, 8).cuda())
+    check(1, 600, 3000, 6, 1, d, seed=45, causal=True, k_lens=i32([2900]))
