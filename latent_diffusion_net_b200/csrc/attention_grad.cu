@@ -212,9 +212,9 @@ __device__ __forceinline__ void pack16(const float* f, uint32_t* pk) {
 
 // Half `side` of the columns of one row of an accumulator: to the output (scaled), or to
 // the FP32 part.
-template <typename T, int NB>
+template <typename T, int NB, bool WIDE>
 __device__ __forceinline__ void store_row(uint32_t tacc, int side, bool have, bool in, int D, float scale, T* dst,
-                                          float* part) {
+                                          bool wide, float* part) {
 #pragma unroll 1
   for (int c = side * NB * 32; c < (side + 1) * NB * 32; c += 32) {
     if (c >= D) break;
@@ -228,25 +228,15 @@ __device__ __forceinline__ void store_row(uint32_t tacc, int side, bool have, bo
     }
     if (!in) continue;
     if (part) {
-#pragma unroll
-      for (int u = 0; u < 8; ++u)
-        if (c + 4 * u < D)
-          __stcg(reinterpret_cast<float4*>(part + c) + u,
-                 make_float4(__uint_as_float(r[4 * u]), __uint_as_float(r[4 * u + 1]), __uint_as_float(r[4 * u + 2]),
-                             __uint_as_float(r[4 * u + 3])));
+      store_part32(part + c, r, D - c);
     } else {
+      float f[32];
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (c + 8 * u < D)
-          *reinterpret_cast<uint4*>(dst + c + 8 * u) = make_uint4(
-              Elem<T>::pack(__uint_as_float(r[8 * u]) * scale, __uint_as_float(r[8 * u + 1]) * scale),
-              Elem<T>::pack(__uint_as_float(r[8 * u + 2]) * scale, __uint_as_float(r[8 * u + 3]) * scale),
-              Elem<T>::pack(__uint_as_float(r[8 * u + 4]) * scale, __uint_as_float(r[8 * u + 5]) * scale),
-              Elem<T>::pack(__uint_as_float(r[8 * u + 6]) * scale, __uint_as_float(r[8 * u + 7]) * scale));
+      for (int u = 0; u < 32; ++u) f[u] = __uint_as_float(r[u]) * scale;
+      store_row32<WIDE, T>(dst + c, f, D - c, wide);
     }
   }
 }
-
 // Tensor memory of both kernels: two score regions of 128 columns, two accumulators, and
 // the packed P and dS that the products take as A operands.
 //   head_dim <= 64: accumulators of 64 columns leave room for P and dS of their own, so
@@ -577,8 +567,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       T* dst = static_cast<T*>(which ? g.out1 : g.out0) + b * os[0] + j * os[1] + kv * os[2];
       float* part = nullptr;
       if (own.slot >= 0) part = g.part + ((which * g.slots + own.slot) * kTile + j - j0) * a.D;
-      store_row<T, NB>((which ? tDv : tDk) + lane_off, cq & 1, t > 0, j < a.Nk, a.D, which ? g.v_scale : g.out_scale,
-                       dst, part);
+      store_row<T, NB, !SHAPED>((which ? tDv : tDk) + lane_off, cq & 1, t > 0, j < a.Nk, a.D, which ? g.v_scale : g.out_scale,
+                       dst, wide_rows(which ? g.out1 : g.out0, which ? g.s1 : g.s0, a.D), part);
     }
   }
   tc_fence_before();
@@ -617,26 +607,20 @@ struct DqWalk : TileWalk<RowTiles> {
 };
 
 // The end of a dq unit, one query row per thread: dQ = scale (dS K - e P K) and the
-// corrected delta, or the parts of a split. Out of line: its registers would compete
-// with the loop's.
-template <typename T, int NB>
-__device__ __noinline__ void store_dq(const GradArgs& g, int b, int h, int i, int slot, int side, uint32_t tDq, uint32_t tPk,
-                                      bool some, float e) {
-  const AttnArgs& a = g.f;
-  const bool valid = i < a.Nq;
-  T* dst = static_cast<T*>(g.out0) + b * g.s0[0] + i * g.s0[1] + h * g.s0[2];
-  const int64_t at = ((int64_t)b * a.H + h) * g.qpad + i;
-  if (slot >= 0) {
-    const int64_t row = (int64_t)slot * kTile + i % kTile;
-    store_row<T, NB>(tDq, side, some, valid, a.D, 1.f, dst, g.part + row * a.D);
-    store_row<T, NB>(tPk, side, some, valid, a.D, 1.f, dst, g.part + (g.slots * kTile + row) * a.D);
-    if (valid && side == 0) g.part_e[row] = e;
+// corrected delta, or (given `part`) the parts of a cut item. Out of line: its registers
+// would compete with the loop's. All by value, as in the forward kernel.
+template <typename T, int NB, bool WIDE>
+__device__ __noinline__ void store_dq(T* dst, bool wide, float* part, float* part_k, float* row_e, int D, float scale,
+                                      int side, uint32_t tDq, uint32_t tPk, bool some, bool valid, float e) {
+  if (part) {
+    store_row<T, NB, WIDE>(tDq, side, some, valid, D, 1.f, dst, wide, part);
+    store_row<T, NB, WIDE>(tPk, side, some, valid, D, 1.f, dst, wide, part_k);
+    if (valid && side == 0) *row_e = e;
     return;
   }
-  if (valid && side == 0) g.ndelta[at] -= e;
 #pragma unroll 1
   for (int c = side * NB * 32; c < (side + 1) * NB * 32; c += 16) {
-    if (c >= a.D) break;
+    if (c >= D) break;
     uint32_t r[16], q[16];
     if (some) {
       tmem_ld_x16(tDq + c, r);
@@ -645,16 +629,21 @@ __device__ __noinline__ void store_dq(const GradArgs& g, int b, int h, int i, in
       tmem_ld_wait_16(q);
     }
     if (!valid) continue;
-    float f[16];
+    uint32_t w[8];
 #pragma unroll
-    for (int y = 0; y < 16; ++y)
-      f[y] = some ? g.out_scale * fmaf(-e, __uint_as_float(q[y]), __uint_as_float(r[y])) : 0.f;
+    for (int y = 0; y < 8; ++y) {
+      float f[2];
 #pragma unroll
-    for (int y = 0; y < 2; ++y)
-      if (c + 8 * y < a.D)
-        *reinterpret_cast<uint4*>(dst + c + 8 * y) =
-            make_uint4(Elem<T>::pack(f[8 * y], f[8 * y + 1]), Elem<T>::pack(f[8 * y + 2], f[8 * y + 3]),
-                       Elem<T>::pack(f[8 * y + 4], f[8 * y + 5]), Elem<T>::pack(f[8 * y + 6], f[8 * y + 7]));
+      for (int x = 0; x < 2; ++x)
+        f[x] = some ? scale * fmaf(-e, __uint_as_float(q[2 * y + x]), __uint_as_float(r[2 * y + x])) : 0.f;
+      w[y] = Elem<T>::pack(f[0], f[1]);
+    }
+    if (WIDE && wide) {
+      st_global_v8(dst + c, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
+    } else {
+      *reinterpret_cast<uint4*>(dst + c) = make_uint4(w[0], w[1], w[2], w[3]);
+      if (c + 8 < D) *reinterpret_cast<uint4*>(dst + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+    }
   }
 }
 
@@ -853,6 +842,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     st.from = 0;
     int nk = 0, lim = 0, pos = 0;
     float nlse = 0.f, ndelta = 0.f;
+    const bool wide = wide_rows(g.out0, g.s0, a.D);
     float e0 = 0.f, e1 = 0.f;  // the row's sum of P (dP - delta) over this half's columns
     for (int r = 0;; ++r) {
       const Record* const rec = ring.at(r);
@@ -971,8 +961,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         // arrive at p_full only after that
         if (cq < 2) {
           const float e = (srow[row] + srow[kTile + row]) + (srow[2 * kTile + row] + srow[3 * kTile + row]);
-          store_dq<T, NB>(g, rec->b, rec->head, rec->i0 + row, rec->slot, cq, tDq + lane_off, tPk + lane_off, some,
-                          e * g.v_scale);
+          const int b = rec->b, h = rec->head, i = rec->i0 + row;
+          const int64_t at = (int64_t)rec->slot * kTile + row;
+          const bool part = rec->slot >= 0, valid = i < a.Nq;
+          const float err = e * g.v_scale;
+          if (valid && !part && cq == 0) g.ndelta[((int64_t)b * a.H + h) * g.qpad + i] = ndelta - err;
+          store_dq<T, NB, !SHAPED>(static_cast<T*>(g.out0) + b * g.s0[0] + i * g.s0[1] + h * g.s0[2], wide,
+                          part ? g.part + at * a.D : nullptr, g.part + (g.slots * kTile + at) * a.D, g.part_e + at, a.D,
+                          g.out_scale, cq, tDq + lane_off, tPk + lane_off, some, valid, err);
         }
         tc_fence_before();
       }
@@ -1057,17 +1053,19 @@ struct GradPlan {
   size_t rows_bytes, part_bytes;
 };
 // Time in steps of one SM, which holds one CTA: units start longest first and the last ones
-// end about half the longest unit's steps after the average (of the cut ones, where the rest
-// are full rounds); a unit costs about one step more. Parts cost one more launch and their FP32 rows, written and joined at 2 TB/s (a step
-// takes about 2.1 us at head_dim 64, 2.6 at 128, 0.7 more for capped scores).
+// end about half the longest unit's steps after the average (of the cut ones where the rest
+// are full rounds). Measured: a step takes 2.0 us at head_dim 64, 2.6 at 128, 1.3 more for
+// capped scores, beginning and ending a unit 2.9 us more. Parts cost one more launch and
+// their FP32 rows, written and joined at 2 TB/s.
 Cut plan_cut(const sd_attention_cfg& c, int64_t items, double steps, double least, double total) {
-  const double step_us = (c.head_dim <= 64 ? 2.1 : 2.6) + (c.softcap > 0.f ? 0.7 : 0.0);
+  const double step_us = (c.head_dim <= 64 ? 2.0 : 2.6) + (c.softcap > 0.f ? 1.3 : 0.0);
+  const double extra = 2.9 / step_us;
   Cut best;
   double best_t = 0;
   auto offer = [&](const Cut& cut, double longest) {
-    longest = std::ceil(longest) + 1;
+    longest = std::ceil(longest) + extra;
     const double units = (double)cut.units;
-    double t = units <= kSms ? longest : std::max((total + units) / kSms + 0.5 * longest, longest);
+    double t = units <= kSms ? longest : std::max((total + extra * units) / kSms + 0.5 * longest, longest);
     if (cut.slots) t += (5.0 + cut.slots * kTile * c.head_dim * 16.0 / 2.0e6) / step_us;
     if (best_t == 0 || t < best_t) {
       best_t = t;
@@ -1078,7 +1076,7 @@ Cut plan_cut(const sd_attention_cfg& c, int64_t items, double steps, double leas
   // whole items with a causal mask, two or fewer for each SM: a long one meets a short one
   if (c.causal && items > kSms && items <= 2 * kSms) {
     const double second = steps - (steps - least) * kSms / items;
-    best_t = std::max(std::max(steps, 2 * second), total / kSms) + 1;
+    best_t = std::max(std::max(steps, 2 * second), total / kSms) + extra;
   }
   for (int s = 2; s <= kMaxSplits && 2 * s <= steps && items * s <= 16 * kSms; ++s) {
     offer(cut_even(items, s), steps / s);

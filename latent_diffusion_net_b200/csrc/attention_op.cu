@@ -91,18 +91,17 @@ struct UnitWalk : TileWalk<RowTiles> {
 };
 
 // The end of a unit: one query row per thread, normalised to the output, or its part
-// of a split. Out of line: it runs once per unit and its registers would compete with
-// the score row of the loop.
-template <typename T, int NB>
-__device__ __noinline__ void store_rows(const AttnArgs& a, int64_t at, int b, int i, int h, int half, uint32_t tO,
-                                        bool some, bool valid, float m, float l) {
-  const bool part = at >= 0;
+// (given `part`) of a cut item. Out of line: it runs once per unit and its registers would
+// compete with the score row of the loop. All by value: what a reference to the kernel's
+// arguments reads comes from far away (77 keys: 5000 cycles a unit, half of its time).
+template <typename T, int NB, bool WIDE>
+__device__ __forceinline__ void store_rows(T* dst, float* part, float* ml, float* lse, int D, bool wide, int half,
+                                        uint32_t tO, bool some, bool valid, float m, float l) {
   const float inv = l > 0.f ? 1.f / l : 0.f;
-  T* dst = static_cast<T*>(a.o) + b * a.os[0] + i * a.os[1] + h * a.os[2];
 #pragma unroll 1
   for (int k = 0; k < NB * 32; k += 32) {
     const int c = half * NB * 32 + k;
-    if (c >= a.D) break;
+    if (c >= D) break;
     uint32_t r[32];
     if (some) {
       tmem_ld_32x32b_x32(tO + k, r);
@@ -112,30 +111,20 @@ __device__ __noinline__ void store_rows(const AttnArgs& a, int64_t at, int b, in
       for (int q = 0; q < 32; ++q) r[q] = 0u;
     }
     if (valid && part && some) {
-      float4* p = reinterpret_cast<float4*>(a.partial + at * a.D + c);
-#pragma unroll
-      for (int q = 0; q < 8; ++q)
-        if (c + 4 * q < a.D)
-          __stcg(p + q, make_float4(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]),
-                                    __uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3])));
+      store_part32(part + c, r, D - c);
     } else if (valid && !part) {
       // a row whose mask leaves nothing has l = 0 and gets zeros
+      float f[32];
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (c + 8 * q < a.D)
-          *reinterpret_cast<uint4*>(dst + c + 8 * q) = make_uint4(
-              Elem<T>::pack(__uint_as_float(r[8 * q]) * inv, __uint_as_float(r[8 * q + 1]) * inv),
-              Elem<T>::pack(__uint_as_float(r[8 * q + 2]) * inv, __uint_as_float(r[8 * q + 3]) * inv),
-              Elem<T>::pack(__uint_as_float(r[8 * q + 4]) * inv, __uint_as_float(r[8 * q + 5]) * inv),
-              Elem<T>::pack(__uint_as_float(r[8 * q + 6]) * inv, __uint_as_float(r[8 * q + 7]) * inv));
+      for (int q = 0; q < 32; ++q) f[q] = __uint_as_float(r[q]) * inv;
+      store_row32<WIDE, T>(dst + c, f, D - c, wide);
     }
   }
-  if (half) return;
-  if (valid && part) {
-    a.partial_ml[at * 2] = m;
-    a.partial_ml[at * 2 + 1] = l;
-  } else if (valid && a.lse) {
-    a.lse[((int64_t)b * a.H + h) * a.Nq + i] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+  if (half || !valid) return;
+  if (part) {
+    *reinterpret_cast<float2*>(ml) = make_float2(m, l);
+  } else if (lse) {
+    *lse = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
   }
 }
 
@@ -342,6 +331,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
     const uint32_t tSr = tS + lane_off + half * 64, tPr = tP + lane_off + half * 32;
     const uint32_t tOr = tO + lane_off + half * NB * 32;  // the columns of O this half rescales and stores
+    const bool wide = wide_rows(a.o, a.os, a.D);
     const float mul = SHAPED ? 1.f : a.sl2;  // shaped scores are in log2 units before the maximum
     int t = 0;
     bool alive = true, valid = false, work = false, some = false;
@@ -530,8 +520,13 @@ __global__ void __launch_bounds__(kThreads, 2)
           asm volatile("bar.sync %0, 64;" ::"r"(1 + q4) : "memory");
           l += sm[(half ^ 1) * kTile + row];
           asm volatile("bar.sync %0, 64;" ::"r"(1 + q4) : "memory");
-          store_rows<T, NB>(a, rec->slot < 0 ? -1 : (int64_t)rec->slot * kTile + row, rec->b, rec->i0 + row_i,
-                            rec->head * a.G + row_h, half, tOr, some, valid, m, l);
+          const int i = rec->i0 + row_i, h = rec->head * a.G + row_h, b = rec->b;
+          const int64_t at = (int64_t)rec->slot * kTile + row;
+          const bool part = rec->slot >= 0;
+          store_rows<T, NB, !SHAPED>(static_cast<T*>(a.o) + b * a.os[0] + i * a.os[1] + h * a.os[2],
+                            part ? a.partial + at * a.D : nullptr, a.partial_ml + at * 2,
+                            a.lse ? a.lse + ((int64_t)b * a.H + h) * a.Nq + i : nullptr, a.D, wide, half, tOr, some,
+                            valid, m, l);
         }
         tc_fence_before();
       }
@@ -551,16 +546,12 @@ template <typename T, int LANES>
 __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ AttnArgs a) {
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x % LANES;
-  const int64_t r = blockIdx.x * (int64_t)(256 / LANES) + threadIdx.x / LANES;
-  const int rows = min(a.tq, a.Nq) * a.G;  // of an item, at most
-  const int64_t nth = r / rows;
-  if (nth >= a.parts.count) return;
-  const int row = (int)(r % rows), item = a.parts.first + (int)nth;
+  const int lane = threadIdx.x % LANES, row = (int)blockIdx.x * (256 / LANES) + threadIdx.x / LANES;
+  const int item = a.parts.first + (int)blockIdx.y;
   const int g = a.parts.group_of_item(item), parts = a.parts.parts[g];
   const int heads = a.B * a.KV, qt = a.qtiles - 1 - item / heads, b = item % heads / a.KV, kv = item % heads % a.KV;
   const int i = qt * a.tq + row / a.G, h = kv * a.G + row % a.G;
-  if (i >= a.Nq) return;
+  if (row >= a.tq * a.G || i >= a.Nq) return;
   const int64_t at = ((int64_t)a.parts.slot[g] + (int64_t)(item - a.parts.item[g]) * parts) * kTile + row;
   const float* pml = a.partial_ml + at * 2;
   const float* po = a.partial + at * a.D + lane * 4;
@@ -657,28 +648,27 @@ FwdPlan plan_forward(const sd_attention_cfg& c) {
   p.qtiles = (c.q_len + p.tq - 1) / p.tq;
   p.ktiles = tiles_of(c.k_len);
   p.items = (int64_t)c.batch * c.kv_heads * p.qtiles;
-  // Time in key tiles of one SM. Two CTAs share an SM and take turns (measured: 1.2 us a
-  // tile and SM at head_dim 64, 1.5 at 128, 0.8 more for capped or biased scores; a CTA
-  // alone needs 1.25 or 1.8 of that). Units start longest first, so the last ones end about
-  // half the longest unit's tiles after the average (of the cut ones, where the rest are
-  // full rounds); parts cost one more launch and their
-  // FP32 rows, written and joined at 2 TB/s.
+  // Time in key tiles of one SM. Two CTAs share an SM and take turns (measured: 1.13 us a
+  // tile and SM at head_dim 64, 1.52 at 128, 0.75 more for capped scores; a CTA alone needs
+  // 1.45 of that). Beginning and ending a unit takes 2.2 us more. The last units end about
+  // half the longest unit's tiles after the average (of the cut ones where the rest are full
+  // rounds). Parts cost one more launch and their FP32 rows, written and joined at 2 TB/s,
+  // 4 TB/s where the items are few (128 queries on 8192 keys: 16 parts 30 us, 8 parts 40).
   const double nq = c.q_len, nk = c.k_len, L = p.ktiles, N = (double)p.items;
   const double least = !c.causal ? L : std::max(0.0, L - nq / kTile);  // tiles of the shortest item
   const double total = N * (c.causal && nq > nk ? 0.5 * L * nk / nq : 0.5 * (L + least)) / kSms;
-  const double tile_us = (c.head_dim <= 64 ? 1.2 : 1.5) + (c.softcap > 0.f ? 0.8 : 0.0);
-  const double alone = c.head_dim <= 64 ? 1.25 : 1.8;
+  const double tile_us = (c.head_dim <= 64 ? 1.13 : 1.52) + (c.softcap > 0.f ? 0.75 : 0.0);
+  const double alone = 1.45, extra = 2.2 / tile_us;
   const double part_tiles = std::min<double>(p.tq, nq) * g * (c.head_dim + 2) * 8.0 / 2.0e6 / tile_us;
   double best = 0;
   // units of at most `longest` tiles, the 149th longest has `second`
   auto offer = [&](const Cut& cut, double longest, double second) {
     const double units = (double)cut.units;
-    // one more tile's time for beginning and ending a unit
-    longest += 1, second += 1;
+    longest += extra, second += extra;
     double t = units <= kSms       ? alone * longest
                : units <= 2 * kSms ? 2 * second + alone * (longest - second)
-                                   : std::max(total + units / kSms + 0.5 * longest, alone * longest);
-    if (cut.slots) t += 5.0 / tile_us + cut.slots * part_tiles;
+                                   : std::max(total + extra * units / kSms + 0.5 * longest, alone * longest);
+    if (cut.slots) t += 5.0 / tile_us + cut.slots * part_tiles * (N < kSms ? 0.5 : 1.0);
     if (best == 0 || t < best) {
       best = t;
       p.cut = cut;
@@ -687,7 +677,7 @@ FwdPlan plan_forward(const sd_attention_cfg& c) {
   for (int s = 1; s <= std::min(kMaxSplits, std::max(p.ktiles, 1)); ++s) {
     const double at = c.causal ? std::max(0.0, 1.0 - kSms / (N * s)) : 1.0;
     offer(cut_even(p.items, s), std::ceil(L / s), std::ceil((least + (L - least) * at) / s));
-    if (N * s > 16.0 * kSms) break;
+    if (N * s > 16.0 * kSms) break;  // far from idle: parts only cost
   }
   if (!c.causal) {
     // the items beyond full rounds of the GPU in parts: they end together
@@ -695,7 +685,7 @@ FwdPlan plan_forward(const sd_attention_cfg& c) {
     if (p.items > 2 * kSms && rest)
       for (int s = 2; s <= std::min(kMaxSplits, p.ktiles) && rest * s <= 2 * kSms; ++s)
         offer(cut_last(p.items, rest, s), std::ceil(L / s), std::ceil(L / s));
-  } else {
+  } else if (N <= 16.0 * kSms) {
     // items in parts of at most 1/k of the longest: short ones whole
     for (int k = 2; k <= std::min(kGroups, p.ktiles); ++k)
       offer(cut_levels(p.items, k, L, least), std::ceil(L / k), std::ceil(L / k));
@@ -796,9 +786,9 @@ sd_status forward(AttnCall& c, const FwdPlan& p) {
                              Shape<NB>::kSmem, c.st, maps, a)));
   if (!p.cut.slots) return SD_OK;
   constexpr int kLanes = NB == 1 ? 16 : 32;
-  const int64_t rows = (int64_t)p.cut.parts.count * std::min(p.tq, g.q_len) * a.G, per = 256 / kLanes;
-  return launched(
-      launch_pdl(attn_join_kernel<T, kLanes>, dim3((unsigned)((rows + per - 1) / per)), dim3(256), 0, c.st, a));
+  const int rows = std::min(p.tq, g.q_len) * a.G, per = 256 / kLanes;  // of an item
+  return launched(launch_pdl(attn_join_kernel<T, kLanes>, dim3((rows + per - 1) / per, p.cut.parts.count), dim3(256), 0,
+                             c.st, a));
 }
 
 }  // namespace
