@@ -33,7 +33,7 @@ namespace {
 // activation bounded it with eight (29 us instead of 22 at 9216 x 320 x 1280), eight
 // elsewhere (the backward gate holds more per thread).
 template <int EPI>
-constexpr int kEpiWarps = EPI == 1 ? 16 : 8;
+constexpr int kEpiWarps = EPI == 0 ? 8 : 16;
 template <int EPI>
 constexpr int kThreads = 64 + 32 * kEpiWarps<EPI>;
 constexpr int kSubA = 128 * 64 * 2;  // one CTA's 128 rows x 64 reduction elements
@@ -71,18 +71,22 @@ struct FfArgs {
   int32_t clear_err;
 };
 
-// 16 FP32 values to 16 consecutive elements of T, and back; n as below.
+// 16 elements of T, packed, to consecutive places, and back; n as below.
 template <typename T>
-__device__ __forceinline__ void store16(T* p, const float (&f)[16], int n, bool wide) {
-  uint32_t w[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) w[j] = Elem<T>::pack(f[2 * j], f[2 * j + 1]);
+__device__ __forceinline__ void put16(T* p, const uint32_t (&w)[8], int n, bool wide) {
   if (wide && n >= 16) {
     st_global_v8(p, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
   } else {
     *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
     if (n > 8) *reinterpret_cast<uint4*>(p + 8) = make_uint4(w[4], w[5], w[6], w[7]);
   }
+}
+template <typename T>
+__device__ __forceinline__ void store16(T* p, const float (&f)[16], int n, bool wide) {
+  uint32_t w[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) w[j] = Elem<T>::pack(f[2 * j], f[2 * j + 1]);
+  put16<T>(p, w, n, wide);
 }
 template <typename T>
 __device__ __forceinline__ void load16(const T* p, uint32_t (&r)[8], int n, bool wide) {
@@ -101,19 +105,20 @@ __device__ __forceinline__ void load16(const T* p, uint32_t (&r)[8], int n, bool
     r[7] = b.w;
   }
 }
-// Sums of 16 columns over the warp's 32 rows (one row per lane): lanes 2j and 2j + 1 get
-// column j. Halves of the columns change places, so it takes 16 exchanges, not 80.
-__device__ __forceinline__ float column_sum16(float (&a)[16], int lane) {
+// Sums of 8 columns over the warp's 32 rows (one row per lane): lanes 4j to 4j + 3 get
+// column j. Halves of the columns change places, so it takes 9 exchanges, not 40.
+__device__ __forceinline__ float column_sum8(float (&a)[8], int lane) {
 #pragma unroll
-  for (int w = 8; w > 0; w >>= 1) {
-    const bool up = lane & (2 * w);
+  for (int w = 4; w > 0; w >>= 1) {
+    const bool up = lane & (4 * w);
 #pragma unroll
     for (int i = 0; i < w; ++i) {
       const float send = up ? a[i] : a[i + w], keep = up ? a[i + w] : a[i];
-      a[i] = keep + __shfl_xor_sync(0xffffffffu, send, 2 * w);
+      a[i] = keep + __shfl_xor_sync(0xffffffffu, send, 4 * w);
     }
   }
-  return a[0] + __shfl_xor_sync(0xffffffffu, a[0], 1);
+  const float s = a[0] + __shfl_xor_sync(0xffffffffu, a[0], 2);
+  return s + __shfl_xor_sync(0xffffffffu, s, 1);
 }
 
 // 32 FP32 values to 32 consecutive elements of T, `n` of them inside (n a multiple of 8).
@@ -308,16 +313,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<EPI>, 1)
       }
       const bool in = grow < M;
       // the saved v and z of this row's first chunk while the main loop runs, each further
-      // chunk's while the one before is computed
-      [[maybe_unused]] uint32_t pv[2][8], pz[2][8];
-      auto load_pre = [&](int c, uint32_t (&v)[8], uint32_t (&z)[8]) {
+      // chunk's once the one before is computed
+      [[maybe_unused]] uint32_t pv[8], pz[8];
+      auto load_pre = [&](int c) {
         const int left = N - (n0 + c);
         if (in && c < step_n && left > 0) {
-          load16<T>(pre + grow * 2 * N + n0 + c, v, left, wide);
-          load16<T>(pre + grow * 2 * N + N + n0 + c, z, left, wide);
+          load16<T>(pre + grow * 2 * N + n0 + c, pv, left, wide);
+          load16<T>(pre + grow * 2 * N + N + n0 + c, pz, left, wide);
         }
       };
-      if (EPI == EPI_GATE_GRAD) load_pre(half * 16, pv[0], pz[0]);
+      if (EPI == EPI_GATE_GRAD) load_pre(half * 16);
       if (!mbar_wait_all(&acc_full[b], (it >> 1) & 1, abort_flag, args.err)) {
         // other warps may have got through, and wait for this one at the barriers
         asm volatile("bar.sync 3, %0;" ::"n"(kEpiThreads) : "memory");
@@ -327,55 +332,52 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<EPI>, 1)
       const uint32_t tacc = tmem + (uint32_t)(b * 256) + lane_off;
       if constexpr (EPI == EPI_GATE_GRAD) {
         float* const cs = csums + b * 2048 + q4 * 512;
-        auto chunk = [&](int c, uint32_t (&v)[8], uint32_t (&z)[8], uint32_t (&v2)[8], uint32_t (&z2)[8]) {
+        for (int c = half * 16; c < step_n && n0 + c < N; c += 64) {
           const int left = N - (n0 + c);
-          uint32_t r[16];
+          uint32_t r[16], of[8], oz[8], oh[8];
           tmem_ld_x16(tacc + c, r);
-          load_pre(c + 32, v2, z2);
           tmem_ld_wait_16(r);
-          float f[16], dz[16], h[16];
 #pragma unroll
           for (int i = 0; i < 16; i += 8) {
-            float zv[8], d[8], a8[8];
+            float zv[8], d[8], a8[8], f[8];
 #pragma unroll
             for (int j = 0; j < 8; j += 2) {
               const int w = (i + j) / 2;
-              zv[j] = Elem<T>::lo(z[w]);
-              zv[j + 1] = Elem<T>::hi(z[w]);
+              zv[j] = Elem<T>::lo(pz[w]);
+              zv[j + 1] = Elem<T>::hi(pz[w]);
               // dz = dh v act'(z)
-              mul2(__uint_as_float(r[i + j]), __uint_as_float(r[i + j + 1]), Elem<T>::lo(v[w]), Elem<T>::hi(v[w]), d[j],
+              mul2(__uint_as_float(r[i + j]), __uint_as_float(r[i + j + 1]), Elem<T>::lo(pv[w]), Elem<T>::hi(pv[w]), d[j],
                    d[j + 1]);
             }
             act_grad_vec<8>(zv, d, a8, act);
 #pragma unroll
             for (int j = 0; j < 8; j += 2) {
               const int w = (i + j) / 2;
-              dz[i + j] = d[j];
-              dz[i + j + 1] = d[j + 1];
-              mul2(__uint_as_float(r[i + j]), __uint_as_float(r[i + j + 1]), a8[j], a8[j + 1], f[i + j], f[i + j + 1]);
-              mul2(Elem<T>::lo(v[w]), Elem<T>::hi(v[w]), a8[j], a8[j + 1], h[i + j], h[i + j + 1]);
+              float h0, h1;
+              mul2(__uint_as_float(r[i + j]), __uint_as_float(r[i + j + 1]), a8[j], a8[j + 1], f[j], f[j + 1]);
+              mul2(Elem<T>::lo(pv[w]), Elem<T>::hi(pv[w]), a8[j], a8[j + 1], h0, h1);
+              of[w] = Elem<T>::pack(f[j], f[j + 1]);
+              oz[w] = Elem<T>::pack(d[j], d[j + 1]);
+              oh[w] = Elem<T>::pack(h0, h1);
+            }
+            if (args.colsum) {
+              if (!in) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) f[j] = d[j] = 0.f;
+              }
+              const float sv = column_sum8(f, lane), sz = column_sum8(d, lane);
+              if (!(lane & 3)) {
+                cs[c + i + (lane >> 2)] = sv;
+                cs[256 + c + i + (lane >> 2)] = sz;
+              }
             }
           }
           if (in) {
-            store16<T>(dpre + grow * 2 * N + n0 + c, f, left, wide);
-            store16<T>(dpre + grow * 2 * N + N + n0 + c, dz, left, wide);
-            if (out) store16<T>(out + grow * N + n0 + c, h, left, wide);
+            put16<T>(dpre + grow * 2 * N + n0 + c, of, left, wide);
+            put16<T>(dpre + grow * 2 * N + N + n0 + c, oz, left, wide);
+            if (out) put16<T>(out + grow * N + n0 + c, oh, left, wide);
           }
-          if (args.colsum) {
-            if (!in) {
-#pragma unroll
-              for (int i = 0; i < 16; ++i) f[i] = dz[i] = 0.f;
-            }
-            const float sv = column_sum16(f, lane), sz = column_sum16(dz, lane);
-            if (!(lane & 1)) {
-              cs[c + (lane >> 1)] = sv;
-              cs[256 + c + (lane >> 1)] = sz;
-            }
-          }
-        };
-        for (int c = half * 16; c < step_n && n0 + c < N; c += 64) {
-          chunk(c, pv[0], pz[0], pv[1], pz[1]);
-          if (c + 32 < step_n && n0 + c + 32 < N) chunk(c + 32, pv[1], pz[1], pv[0], pz[0]);
+          load_pre(c + 64);
         }
       }
       if constexpr (EPI == EPI_GATE) {
