@@ -631,18 +631,28 @@ __global__ void __launch_bounds__(256) ff_join_kernel(const float* __restrict__ 
     float f[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) f[j] = 0.f;
-#pragma unroll 8
-    for (int z = 0; z < splits; ++z) {
-      const float4* p = reinterpret_cast<const float4*>(partial + z * stride + i * 8);
-      const float4 u = __ldcg(p), w = __ldcg(p + 1);
-      f[0] += u.x;
-      f[1] += u.y;
-      f[2] += u.z;
-      f[3] += u.w;
-      f[4] += w.x;
-      f[5] += w.y;
-      f[6] += w.z;
-      f[7] += w.w;
+    // eight parts at a time, all asked for before the first is added
+    for (int z = 0; z < splits; z += 8) {
+      float4 u[8], w[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (z + k < splits) {
+          const float4* p = reinterpret_cast<const float4*>(partial + (z + k) * stride + i * 8);
+          u[k] = __ldcg(p);
+          w[k] = __ldcg(p + 1);
+        }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (z + k >= splits) break;
+        f[0] += u[k].x;
+        f[1] += u[k].y;
+        f[2] += u[k].z;
+        f[3] += u[k].w;
+        f[4] += w[k].x;
+        f[5] += w[k].y;
+        f[6] += w[k].z;
+        f[7] += w[k].w;
+      }
     }
     if (bias) {
       float b[8];
@@ -742,16 +752,23 @@ Plan plan_product(const Product& p) {
   const int64_t kb = (p.K + 63) / 64, pairs_m = (p.M + 255) / 256;
   Plan best{0, 1, 0};
   double best_cost = 0;
+  // reduction blocks of a part for each number of splits, 0 where it would leave none or few
+  int64_t pers[kMaxSplits + 1];
+  for (int sp = 1; sp <= (p.may_split ? kMaxSplits : 1); ++sp) {
+    int64_t per = ((uint32_t)kb + sp - 1) / (uint32_t)sp;
+    per = (per + 1) / 2 * 2;
+    const bool use = sp == 1 || (per >= 4 && ((uint32_t)kb + per - 1) / (uint32_t)per == (uint32_t)sp);
+    pers[sp] = use ? per : 0;
+  }
   for (int bn : widths) {
     if (p.gated && bn % 64) continue;  // each half whole 32-column chunks
     const int step = p.gated ? bn / 2 : bn;
     const int64_t tiles = pairs_m * ((p.N + step - 1) / step);
-    // more splits than fill the GPU twice only cost
-    const int most = !p.may_split ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>(kMaxSplits, 2 * kPairs / tiles));
+    // more splits than fill the GPU four times only cost
+    const int most = !p.may_split ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>(kMaxSplits, 4 * kPairs / tiles));
     for (int sp = 1; sp <= most; ++sp) {
-      int64_t per = (kb + sp - 1) / sp;
-      per = (per + 1) / 2 * 2;
-      if (sp > 1 && ((kb + per - 1) / per != sp || per < 4)) continue;
+      const int64_t per = pers[sp];
+      if (!per) continue;
       if (sp > 1 && (size_t)sp * p.M * p.N * 4 > kSplitBytes) break;
       const int64_t rounds = (tiles * sp + kPairs - 1) / kPairs;
       const double b_bytes = p.b_mn ? (bn / 2 + 63) / 64 * 8192.0 : bn * 64.0;
