@@ -77,11 +77,24 @@ __global__ void __launch_bounds__(256) attn_delta_kernel(const __grid_constant__
   const int64_t rows = (int64_t)a.B * a.H * g.qpad, r0 = blockIdx.x * (int64_t)groups * 4 + (threadIdx.x >> shift);
   uint4 x[4], y[4];
   float lse[4];
+  int64_t to[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const int64_t r = r0 + k * groups;
-    // rows in the order of (token, head), in which o lies when it is contiguous
-    const int h = (int)(r % a.H), i = (int)(r / a.H % g.qpad), b = (int)(r / a.H / g.qpad);
+    // rows in the order of (token, head), in which o lies when it is contiguous; 64-bit
+    // divisions, of which each row needs three, would take longer than the reads
+    int h, i, b;
+    if (rows <= UINT32_MAX) {
+      const uint32_t t = (uint32_t)r / (uint32_t)a.H;
+      h = (int)((uint32_t)r - t * (uint32_t)a.H);
+      b = (int)(t / (uint32_t)g.qpad);
+      i = (int)(t - (uint32_t)b * (uint32_t)g.qpad);
+    } else {
+      h = (int)(r % a.H);
+      i = (int)(r / a.H % g.qpad);
+      b = (int)(r / a.H / g.qpad);
+    }
+    to[k] = ((int64_t)b * a.H + h) * g.qpad + i;
     x[k] = y[k] = make_uint4(0u, 0u, 0u, 0u);
     lse[k] = -INFINITY;
     if (r < rows && i < a.Nq) {
@@ -103,10 +116,8 @@ __global__ void __launch_bounds__(256) attn_delta_kernel(const __grid_constant__
     for (int e = 0; e < 8; ++e) s = fmaf(u[e], v[e], s);
     for (int o = 1 << shift >> 1; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (sub == 0 && r < rows) {
-      const int h = (int)(r % a.H), i = (int)(r / a.H % g.qpad), b = (int)(r / a.H / g.qpad);
-      const int64_t at = ((int64_t)b * a.H + h) * g.qpad + i;
-      g.nlse[at] = lse[k] == -INFINITY ? -INFINITY : fmaf(-lse[k], kLog2e, g.shift);
-      g.ndelta[at] = -s;
+      g.nlse[to[k]] = lse[k] == -INFINITY ? -INFINITY : fmaf(-lse[k], kLog2e, g.shift);
+      g.ndelta[to[k]] = -s;
     }
   }
 }
@@ -998,12 +1009,12 @@ template <typename T>
 __global__ void __launch_bounds__(256) attn_grad_join_kernel(const __grid_constant__ JoinArgs a) {
   pdl_wait();
   pdl_trigger();
-  const int vecs = a.D / 8;
+  const uint32_t vecs = (uint32_t)a.D / 8;
   const int64_t n = (int64_t)a.sets * a.parts.count * kTile * vecs;
   for (int64_t x = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; x < n; x += (int64_t)gridDim.x * blockDim.x) {
-    const int d = (int)(x % vecs) * 8, row = (int)(x / vecs % kTile);
-    const int64_t nth = x / vecs / kTile;
-    const int set = nth >= a.parts.count, item = a.parts.first + (int)(nth - (set ? a.parts.count : 0));
+    const uint32_t at_row = (uint32_t)x / vecs;  // the plan keeps parts far below 2^32
+    const int d = (int)((uint32_t)x - at_row * vecs) * 8, row = (int)(at_row % kTile), nth = (int)(at_row / kTile);
+    const int set = nth >= a.parts.count, item = a.parts.first + nth - (set ? a.parts.count : 0);
     const int grp = a.parts.group_of_item(item), parts = a.parts.parts[grp];
     const int each = a.B * a.heads, b = item % each / a.heads, h = item % each % a.heads;
     const int i = (a.part_e ? a.tiles - 1 - item / each : item / each) * kTile + row;
