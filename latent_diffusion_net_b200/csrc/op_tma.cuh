@@ -23,35 +23,10 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const void* tmap, uint64_
       : "memory");
 }
 
-// Shared-memory descriptor of an MN-major operand: blocks of 64 MN elements (one
-// 128-byte swizzled row per K index), 8 K rows 1024 bytes apart, blocks
-// `block_bytes` apart. Step 16 along K: +2048 bytes.
-__device__ __forceinline__ uint64_t umma_desc_mn(uint32_t smem_addr, uint32_t block_bytes) {
-  uint64_t d = 0;
-  d |= (uint64_t)((smem_addr >> 4) & 0x3FFF);
-  d |= (uint64_t)((block_bytes >> 4) & 0x3FFF) << 16;  // leading byte offset: next 64 MN elements
-  d |= (uint64_t)((1024 >> 4) & 0x3FFF) << 32;         // stride byte offset: next 8 K rows
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
-}
-
 // Instruction descriptor of kind::f16 with FP32 accumulators; A and B of one type.
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool f16, bool a_mn, bool b_mn) {
   return (1u << 4) | (f16 ? 0u : (1u << 7) | (1u << 10)) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-
-// D[tmem] (+)= A[tmem] * B[smem]^T: row i of A is TMEM lane i, two 16-bit elements
-// per column, 8 columns per K step of 16.
-__device__ __forceinline__ void umma_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc,
-                                        uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
-      "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
 }
 
 // The issuing thread builds every operand descriptor itself, and its instructions, not
@@ -165,6 +140,27 @@ __device__ __forceinline__ void mbar_arrive_warp(uint64_t* bar) {
 // A bounded wait whose answer is the same for the whole warp (TMEM accesses are warp-collective).
 __device__ __forceinline__ bool mbar_wait_all(uint64_t* bar, uint32_t parity, volatile int* abort, int* err) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, err));
+}
+
+// A warp that shares named barrier `id` with others leaves its loop. Once a wait has given up
+// (*abort) it keeps arriving there until all `warps` have left: others may have got through
+// that wait and would stay at the barrier for good. `left` counts them.
+static __device__ __noinline__ void leave_barrier(volatile int* abort, int* left, int warps, int id) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) atomicAdd(left, 1);
+  if (!*abort) return;
+  for (uint32_t n = 0; n < kSpinLimit && *reinterpret_cast<volatile int*>(left) < warps; ++n) {
+    __syncwarp();
+    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(32 * warps) : "memory");
+    __nanosleep(200);
+  }
+}
+// Every thread, before a kernel's last barrier: after a wait that gave up, copies and
+// products may still be under way into shared and tensor memory that the CTA is about to
+// give back. About a millisecond, far longer than any of them takes.
+__device__ __forceinline__ void settle(volatile int* abort) {
+  if (*abort)
+    for (int i = 0; i < 1000; ++i) __nanosleep(1000);
 }
 
 // ------------------------------------------------------------------ CTA pairs (cta_group::2)
