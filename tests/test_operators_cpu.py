@@ -140,3 +140,10 @@ def test_attention_refusals():
     assert at_fwd(ok, masks=m(prefix=P, k_lens=P, q_doc=P, k_doc=P, slopes=P)) in NO_DEVICE
     assert at_fwd(c(0, 4, 4, 1), q=None, k=None, v=None, o=None, ws=None) == OK
     assert at_fwd(c(1, 0, 4, 1), q=None, k=None, v=None, o=None, ws=None) == OK
+
+
+def test_attention_sizes_beyond_the_grid_are_refused():
+    """Query rows and key rows of all sequences and heads together have to stay countable."""
+    for cfg in (B.attention_cfg(4096, 1, 1 << 20, 4096, 4096, 8), B.attention_cfg(4096, 1 << 20, 1, 4096, 1, 8),
+                B.attention_cfg(1 << 13, 1, 1, 1 << 12, 1, 8)):
+        assert B.sd_attention_workspace_size(cfg) == 0
