@@ -551,10 +551,10 @@ __global__ void __launch_bounds__(kThreads, 2)
 }
 
 // Joins the parts of cut items: m = max m_z, o = sum 2^(m_z - m) O_z / sum 2^(m_z - m) l_z,
-// over z in order, eight parts at a time whose loads are all under way at once. LANES lanes
-// per query row, 16 bytes each.
-template <typename T, int LANES>
-__global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ AttnArgs a) {
+// over z in order, U parts at a time whose loads are all under way at once (few parts: fewer
+// registers and more rows on an SM). LANES lanes per query row, 16 bytes each.
+template <typename T, int LANES, int U>
+__global__ void __launch_bounds__(256, U <= 4 ? 4 : 2) attn_join_kernel(const __grid_constant__ AttnArgs a) {
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x % LANES, row = (int)blockIdx.x * (256 / LANES) + threadIdx.x / LANES;
@@ -568,7 +568,6 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
   const float* po = a.partial + at * a.D + lane * 4;
   const bool in = lane * 4 < a.D;
   float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-  constexpr int U = 8;
   for (int z0 = 0; z0 < parts; z0 += U) {
     float2 ml[U];
     float4 v[U];
@@ -798,8 +797,10 @@ sd_status forward(AttnCall& c, const FwdPlan& p) {
   if (!p.cut.slots) return SD_OK;
   constexpr int kLanes = NB == 1 ? 16 : 32;
   const int rows = std::min(p.tq, g.q_len) * a.G, per = 256 / kLanes;  // of an item
-  return launched(launch_pdl(attn_join_kernel<T, kLanes>, dim3((rows + per - 1) / per, p.cut.parts.count), dim3(256), 0,
-                             c.st, a));
+  const int most = *std::max_element(p.cut.parts.parts, p.cut.parts.parts + p.cut.parts.n);
+  auto* join = most <= 4 ? attn_join_kernel<T, kLanes, 4> : attn_join_kernel<T, kLanes, 8>;
+  return launched(
+      launch_pdl(join, dim3((rows + per - 1) / per, p.cut.parts.count), dim3(256), 0, c.st, a));
 }
 
 }  // namespace
