@@ -339,3 +339,27 @@ def test_long_walks_cut_shorter(d):
     """A causal mask with few items of unequal lengths: the longest are computed in two to eight parts."""
     check(2, 2047, 2047, 8, 2, d, seed=44, causal=True, prefix=i32([300, 0]), slopes=torch.linspace(0.01, 0.2, 8).cuda())
     check(1, 600, 3000, 6, 1, d, seed=45, causal=True, k_lens=i32([2900]))
+
+
+def test_outputs_on_16_byte_boundaries():
+    """Addresses and strides that are multiples of 16 bytes and not of 32 give the same bits."""
+    def shifted(t):
+        return torch.empty(t.numel() + 8, dtype=t.dtype, device="cuda")[8:].view(t.shape)
+
+    q, k, v, do = inputs(2, 300, 410, 4, 2, 64, "bf16", 51)
+    want = call(q, k, v, do)
+    cfg = B.attention_cfg(2, 300, 410, 4, 2, 64)
+    n = B.sd_attention_workspace_size(cfg)
+    ws, lse = torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda"), torch.empty(2, 4, 300, device="cuda")
+    o, dq, dk, dv = shifted(q), shifted(q), shifted(k), shifted(v)
+    B.sd_attention_fwd(cfg, q, k, v, None, o, lse, ws, n)
+    B.sd_attention_bwd(cfg, q, k, v, None, o, lse, do, dq, dk, dv, ws, n)
+    # rows 16 bytes longer than their heads
+    tall = torch.full((2, 300, 4 * 64 + 8), float("nan"), dtype=q.dtype, device="cuda")
+    odd = B.attention_cfg(2, 300, 410, 4, 2, 64, o_stride=(300 * 264, 264, 64))
+    B.sd_attention_fwd(odd, q, k, v, None, tall, lse, ws, n)
+    torch.cuda.synchronize()
+    for name, t in (("o", o), ("dq", dq), ("dk", dk), ("dv", dv)):
+        assert torch.equal(t, want[name]), name
+    assert torch.equal(tall[:, :, :256].reshape(2, 300, 4, 64), want["o"])
+    assert torch.isnan(tall[:, :, 256:]).all()

@@ -166,3 +166,26 @@ def test_nothing_to_do():
     B.sd_gated_ff_bwd(cfg, None, None, None, None, None, None, g["w1"], g["b1"], g["w2"], g["b2"], None, 0)
     torch.cuda.synchronize()
     assert not any(g[k].any() for k in ("w1", "b1", "w2", "b2"))
+
+
+@pytest.mark.parametrize("m", [3, 300])
+def test_tensors_on_16_byte_boundaries(m):
+    """Every tensor at a multiple of 16 bytes that is none of 32: the same bits."""
+    def shifted(t):
+        return torch.empty(t.numel() + 8, dtype=t.dtype, device="cuda")[8:].view(t.shape).copy_(t)
+
+    p, dy = make(m, 128, 192, 160, "bf16")
+    cfg, ws = plan(m, 128, 192, 160, "gelu", "bf16")
+    pre = torch.empty(m, 384, dtype=dy.dtype, device="cuda")
+    y = forward(p, cfg, ws, pre)
+    want = backward(p, cfg, ws, pre, dy)
+    q = {k: shifted(v) for k, v in p.items()}
+    pre2, y2 = shifted(torch.zeros_like(pre)), shifted(torch.zeros_like(y))
+    B.sd_gated_ff_fwd(cfg, q["w1"], q["b1"], q["w2"], q["b2"], q["x"], pre2, y2, ws, ws.numel())
+    got = {k: shifted(torch.zeros_like(v)) for k, v in p.items()}
+    B.sd_gated_ff_bwd(cfg, q["w1"], q["w2"], q["x"], pre2, shifted(dy), got["x"], got["w1"], got["b1"], got["w2"],
+                      got["b2"], ws, ws.numel())
+    torch.cuda.synchronize()
+    assert torch.equal(y2, y) and torch.equal(pre2, pre)
+    for name in want:
+        assert torch.equal(got[name], want[name]), name
