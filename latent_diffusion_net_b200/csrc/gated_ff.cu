@@ -425,7 +425,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<EPI>, 1)
           tmem_ld_wait_regs(r);
           if (partial) {
             if (in) {
-              // N is a multiple of 8 and the parts start on 256 bytes: whole 32-byte sectors
+              // N is a multiple of 8 and the parts start on 256 bytes (scratch()): whole 32-byte sectors
               float* p = partial + ((int64_t)z * M + grow) * N + n0 + c;
 #pragma unroll
               for (int i = 0; i < 4; ++i)
@@ -878,13 +878,18 @@ Product p_dx(const sd_gated_ff_cfg& c) { return {c.tokens, 2 * (int64_t)c.d_hidd
 Product p_dw1(const sd_gated_ff_cfg& c) { return {2 * (int64_t)c.d_hidden, c.tokens, c.d_in, false, true, true, true}; }
 Product p_dw2(const sd_gated_ff_cfg& c) { return {c.d_out, c.tokens, c.d_hidden, false, true, true, true}; }
 
+// Scratch, from the first 256-byte boundary behind the header: a workspace starts on any
+// 16-byte boundary, and the FP32 parts are written 32 bytes at a time.
 struct Space {
   size_t h, dpre, partial, colsum, colsum2, total;
   int chunks;
 };
+uint8_t* scratch(void* workspace) {
+  return reinterpret_cast<uint8_t*>(up256(reinterpret_cast<uintptr_t>(workspace) + kOpHeader));
+}
 Space plan_space(const sd_gated_ff_cfg& c) {
   Space s;
-  s.h = kOpHeader;
+  s.h = 0;
   s.dpre = s.h + up256((size_t)c.tokens * c.d_hidden * 2);
   s.partial = s.dpre + up256((size_t)c.tokens * c.d_hidden * 4);
   size_t parts = 0;
@@ -894,7 +899,7 @@ Space plan_space(const sd_gated_ff_cfg& c) {
   const int blocks = (c.d_out + 255) / 256;
   s.chunks = (int)std::max<int64_t>(1, std::min<int64_t>((c.tokens + 63) / 64, (592 + blocks - 1) / blocks));
   s.colsum2 = s.colsum + up256((size_t)((c.tokens + 127) / 128) * 2 * c.d_hidden * 4);
-  s.total = s.colsum2 + up256((size_t)s.chunks * c.d_out * 4);
+  s.total = kOpHeader + 240 + s.colsum2 + up256((size_t)s.chunks * c.d_out * 4);
   return s;
 }
 
@@ -1016,9 +1021,9 @@ sd_status sd_gated_ff_fwd(const sd_gated_ff_cfg* cfg, const void* w1, const void
   OP_TRY(check_workspace(s.total, workspace, ws_bytes));
   Call c{cfg};
   OP_TRY(current_device(&c.dev));
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  uint8_t* ws = scratch(workspace);
   c.st = (cudaStream_t)stream;
-  c.err = reinterpret_cast<int*>(ws);
+  c.err = static_cast<int*>(workspace);
   c.partial = reinterpret_cast<float*>(ws + s.partial);
   return cfg->dtype == SD_DTYPE_F16 ? forward<__half>(c, s, ws, w1, b1, w2, b2, x, pre, y)
                                     : forward<__nv_bfloat16>(c, s, ws, w1, b1, w2, b2, x, pre, y);
@@ -1046,9 +1051,9 @@ sd_status sd_gated_ff_bwd(const sd_gated_ff_cfg* cfg, const void* w1, const void
   OP_TRY(check_workspace(s.total, workspace, ws_bytes));
   Call c{cfg};
   OP_TRY(current_device(&c.dev));
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  uint8_t* ws = scratch(workspace);
   c.st = (cudaStream_t)stream;
-  c.err = reinterpret_cast<int*>(ws);
+  c.err = static_cast<int*>(workspace);
   c.partial = reinterpret_cast<float*>(ws + s.partial);
   return cfg->dtype == SD_DTYPE_F16
              ? backward<__half>(c, s, ws, w1, w2, x, pre, dy, dx, dw1, db1, dw2, db2)
