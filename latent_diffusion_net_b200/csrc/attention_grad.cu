@@ -412,7 +412,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         Record rec = {tile, whole ? kWhole : 0, 0, nk, pre, 0, b, h, i0, own.slot, {0, 0}};
         rec.flags |= walk.w.one_doc(tile, rec.doc);
         ok = ring.put(t, rec);
-        if (ok && a.q_pad) docs.load(t, a.q_pad + ((int64_t)b * g.qblocks + tile) * kTile);
+        if (ok && a.q_pad) {
+          if (reads_docs(rec.flags))
+            docs.load(t, a.q_pad + ((int64_t)b * g.qblocks + tile) * kTile);
+          else
+            docs.skip(t);
+        }
         if (t == 0) {
           mbar_arrive_expect_tx(kv_full, 2 * kBytes);
           for (int c = 0; c < NB; ++c) {
@@ -499,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       st.from = j >= nk || ((flags & kOneDoc) && rec->doc != st.doc) ? kTile : a.causal && j >= pre ? j - off - i0 : 0;
       const float* stat = sstat + s * 256 + c0;
       st.sdoc = nullptr;
-      if (!whole && a.q_pad && !(flags & kOneDoc)) {
+      if (a.q_pad && reads_docs(flags)) {
         st.sdoc = docs.get(t, alive);
         if (!alive) break;
       }
@@ -750,9 +755,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive_expect_tx(next_bar, 16);
             ask_unit(next_unit, next_bar);
           }
-          if (ok && a.k_pad && j < 0) docs.skip(r);
+          if (ok && a.k_pad) {
+            if (j >= 0 && reads_docs(rec.flags))
+              docs.load(r, a.k_pad + ((int64_t)u.b * a.ktiles + j) * kTile);
+            else
+              docs.skip(r);
+          }
           if (j >= 0) {
-            if (ok && a.k_pad) docs.load(r, a.k_pad + ((int64_t)u.b * a.ktiles + j) * kTile);
             if (first && (ok = ok && (n == 0 || mbar_wait(q_empty, (n - 1) & 1, abort_flag, a.err)))) {
               mbar_arrive_expect_tx(q_full, 2 * kBytes);
               for (int c = 0; c < NB; ++c) {
@@ -883,7 +892,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (some) {
         const int j0 = tile * kTile;
         st.sdoc = nullptr;
-        if (!whole && a.k_pad && !(flags & kOneDoc)) {
+        if (a.k_pad && reads_docs(flags)) {
           st.sdoc = docs.get(r, alive);
           if (!alive) break;
         }

@@ -217,9 +217,13 @@ __global__ void __launch_bounds__(kThreads, 2)
             mbar_arrive_expect_tx(next_bar, 16);
             ask_unit(next_unit, next_bar);
           }
-          if (ok && a.k_pad && j < 0) docs.skip(r);
+          if (ok && a.k_pad) {
+            if (j >= 0 && reads_docs(rec.flags))
+              docs.load(r, a.k_pad + ((int64_t)u.b * a.ktiles + j) * kTile);
+            else
+              docs.skip(r);
+          }
           if (j >= 0) {
-            if (ok && a.k_pad) docs.load(r, a.k_pad + ((int64_t)u.b * a.ktiles + j) * kTile);
             if (first) {
               const int s = n % KS;
               ok = ok && (n < KS || mbar_wait(&q_empty[s], (n / KS - 1) & 1, abort_flag, a.err));
@@ -443,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 2)
               for (int c = 0; c < 64; ++c)
                 if (c >= lc) sv[c] = __float_as_uint(-INFINITY);
             }
-            if (a.k_pad && !(flags & kOneDoc)) {
+            if (a.k_pad && reads_docs(flags)) {
               const int32_t* sdoc = docs.get(r, alive) + half * 64;
               if (!alive) break;
 #pragma unroll

@@ -236,10 +236,13 @@ struct RecordRing {
   }
 };
 
-// The documents of a step's tile (128 ids), loaded beside its operands. A warp that
-// reads record r has finished step r - 1, and record r is written once all have read
-// record r - kRing: with twice as many slots a load never meets a reader.
+// The documents of a step's tile (128 ids), loaded beside its operands where they are read:
+// every load is waited for by the warps that compute, so none is under way when a CTA ends. A
+// warp that reads record r has finished step r - 1, and record r is written once all have
+// read record r - kRing: with twice as many slots a load never meets a reader.
 constexpr int kDocRing = 2 * kRing;
+// Whether a step with a tile reads the documents of its columns.
+__device__ __forceinline__ bool reads_docs(int32_t flags) { return !(flags & (kWhole | kOneDoc)); }
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
                    smem_u32(dst)),
@@ -251,7 +254,7 @@ struct DocRing {
   uint64_t* full;  // [kDocRing]
   volatile int* abort;
   int* err;
-  // The slot's earlier load has landed (nobody may have waited for it).
+  // The phase of the slot's earlier record has passed (nobody may have waited for it).
   __device__ __forceinline__ bool landed(int r) const {
     return r < kDocRing || mbar_wait(&full[r % kDocRing], (r / kDocRing - 1) & 1, abort, err);
   }
@@ -261,7 +264,7 @@ struct DocRing {
     mbar_arrive_expect_tx(&full[s], kTile * 4);
     bulk_load(slot + s * kTile, src, kTile * 4, &full[s]);
   }
-  // a record without a tile: its slot's phase passes all the same
+  // a record whose documents nobody reads: its slot's phase passes all the same
   __device__ __forceinline__ void skip(int r) const {
     if (landed(r)) mbar_arrive(&full[r % kDocRing]);
   }
