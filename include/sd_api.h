@@ -479,7 +479,8 @@ sd_status sd_gated_ff_bwd(const sd_gated_ff_cfg* cfg, const void* w1, const void
  *   o_i = sum_j softmax_j(s) v_j over the keys that i sees:
  *     j < n_b, and (not causal, or j <= p_i, or j < prefix[b]),
  *     and q_doc[b][i] = k_doc[b][j].
- * A query that sees no key gets o = 0, lse = -infinity and no gradient.
+ * A query that sees no key gets o = 0, lse = -infinity and no gradient. One with NaN
+ * among its scores gets NaN in o and lse, however its keys are divided up.
  *   batch, q_len, k_len >= 0 (k_len <= 2^20); heads a multiple of kv_heads, at most
  *   128 query heads per key head; head_dim a multiple of 8, at most 128; dtype BF16
  *   or F16. scale 0 means 1/sqrt(head_dim); softcap 0 means none.

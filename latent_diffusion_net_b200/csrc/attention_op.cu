@@ -104,7 +104,7 @@ struct UnitWalk : TileWalk<RowTiles> {
 template <typename T, int NB, bool WIDE>
 __device__ __forceinline__ void store_rows(T* dst, float* part, float* ml, float* lse, int D, bool wide, int half,
                                         uint32_t tO, bool some, bool valid, float m, float l) {
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const float inv = l == 0.f ? 0.f : 1.f / l;  // l = 0: a row that sees no key; NaN stays NaN
 #pragma unroll 1
   for (int k = 0; k < NB * 32; k += 32) {
     const int c = half * NB * 32 + k;
@@ -131,7 +131,7 @@ __device__ __forceinline__ void store_rows(T* dst, float* part, float* ml, float
   if (part) {
     *reinterpret_cast<float2*>(ml) = make_float2(m, l);
   } else if (lse) {
-    *lse = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    *lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
   }
 }
 
@@ -587,16 +587,19 @@ __global__ void __launch_bounds__(256, U <= 4 ? 4 : 2) attn_join_kernel(const __
     float top = m;
 #pragma unroll
     for (int u = 0; u < U; ++u) top = fmaxf(top, ml[u].x);
-    if (top == -INFINITY) continue;
-    const float keep = fast_ex2(m - top);
+    // a part that saw no key has l = 0 and holds no values. One whose scores are all NaN has
+    // no maximum either, since a maximum passes NaN over: its l is NaN and has to stay
+    const float base = top == -INFINITY ? 0.f : top, keep = fast_ex2(m - base);
     m = top;
-    l *= keep;
+    if (l != 0.f) {
+      l *= keep;
 #pragma unroll
-    for (int x = 0; x < 4; ++x) acc[x] *= keep;
+      for (int x = 0; x < 4; ++x) acc[x] *= keep;
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (ml[u].x != -INFINITY) {  // a part that saw no key holds no values
-        const float f = fast_ex2(ml[u].x - top);
+      if (ml[u].y != 0.f) {
+        const float f = fast_ex2(ml[u].x - base);
         l = fmaf(f, ml[u].y, l);
         acc[0] = fmaf(f, v[u].x, acc[0]);
         acc[1] = fmaf(f, v[u].y, acc[1]);
@@ -604,13 +607,13 @@ __global__ void __launch_bounds__(256, U <= 4 ? 4 : 2) attn_join_kernel(const __
         acc[3] = fmaf(f, v[u].w, acc[3]);
       }
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
   if (in) {
     T* dst = static_cast<T*>(a.o) + b * a.os[0] + i * a.os[1] + h * a.os[2] + lane * 4;
     *reinterpret_cast<uint2*>(dst) =
         make_uint2(Elem<T>::pack(acc[0] * inv, acc[1] * inv), Elem<T>::pack(acc[2] * inv, acc[3] * inv));
   }
-  if (lane == 0 && a.lse) a.lse[((int64_t)b * a.H + h) * a.Nq + i] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+  if (lane == 0 && a.lse) a.lse[((int64_t)b * a.H + h) * a.Nq + i] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 // One warp per tile: the key tiles of all sequences, then the query tiles.

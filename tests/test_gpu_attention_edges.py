@@ -29,3 +29,48 @@ def test_documents_cut_anywhere_in_long_rows(d, causal):
     q, k, v, do = inputs(2, n, n, 6, 2, d, "bf16", 75)
     kw = dict(causal=causal, q_doc=doc, k_doc=doc, k_lens=i32([n, 2650]))
     compare(call(q, k, v, do, **kw), reference(q, k, v, do, **kw), q.dtype)
+
+
+# one query on many keys: computed in parts; 300 and 200 queries: whole
+NAN_SHAPES = [(1, 4096, 16, 4, 128), (3, 5000, 4, 4, 64), (300, 300, 2, 2, 64), (200, 260, 4, 2, 128)]
+
+
+@pytest.mark.parametrize("nq,nk,h,kv,d", NAN_SHAPES)
+def test_nan_in_a_query_stays_in_its_row(nq, nk, h, kv, d):
+    """Whether keys are taken in parts or not: the row's output and lse are NaN, all others as without it."""
+    q, k, v, _ = inputs(2, nq, nk, h, kv, d, "bf16", 61)
+    clean = call(q, k, v)
+    q[1, nq - 1, h - 1, 3] = math.nan
+    got = call(q, k, v)
+    bad = torch.zeros(2, nq, h, dtype=torch.bool, device="cuda")
+    bad[1, nq - 1, h - 1] = True
+    assert torch.isnan(got["o"][bad]).all() and torch.equal(got["o"][~bad], clean["o"][~bad])
+    bad = bad.permute(0, 2, 1)
+    assert torch.isnan(got["lse"][bad]).all() and torch.equal(got["lse"][~bad], clean["lse"][~bad])
+
+
+@pytest.mark.parametrize("nq,nk,h,kv,d", NAN_SHAPES)
+def test_nan_in_visible_keys_is_not_dropped(nq, nk, h, kv, d):
+    """The newest half of the keys of one head: whole tiles and whole parts whose scores are all NaN."""
+    q, k, v, do = inputs(2, nq, nk, h, kv, d, "bf16", 62)
+    clean = call(q, k, v, do)
+    k[1, nk // 2:, kv - 1] = math.nan
+    got = call(q, k, v, do)
+    g = h // kv
+    assert torch.isnan(got["o"][1, :, -g:]).all() and torch.isnan(got["lse"][1, -g:]).all()
+    assert torch.isnan(got["dq"][1, :, -g:]).all() and torch.isnan(got["dv"][1, :, -1]).all()
+    for name, at in (("o", 2), ("lse", 1), ("dq", 2)):
+        keep = torch.ones_like(clean[name], dtype=torch.bool)
+        keep[1].narrow(at - 1, h - g, g).fill_(False)
+        assert torch.equal(got[name][keep], clean[name][keep]), name
+    assert torch.equal(got["dv"][0], clean["dv"][0]) and torch.equal(got["dk"][0], clean["dk"][0])
+
+
+def test_nan_only_in_the_newest_key():
+    """One key in a tile of its own (and, for one query, perhaps in a part of its own)."""
+    for nq, nk in ((1, 4097), (1, 129), (140, 385)):
+        q, k, v, _ = inputs(1, nq, nk, 2, 2, 64, "f16", 63)
+        k[0, nk - 1, 1] = math.nan
+        got = call(q, k, v)
+        assert torch.isnan(got["o"][0, :, 1]).all() and torch.isnan(got["lse"][0, 1]).all()
+        assert torch.isfinite(got["o"][0, :, 0]).all() and torch.isfinite(got["lse"][0, 0]).all()
