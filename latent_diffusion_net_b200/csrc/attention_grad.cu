@@ -176,8 +176,9 @@ __device__ __forceinline__ void probabilities(const AttnArgs& a, const ScoreTerm
         h0 = h0 || d.x != s.doc;
         h1 = h1 || d.y != s.doc;
       }
-      if (h0) p[u] = 0.f;
-      if (h1) p[u + 1] = 0.f;
+      // the slope too: behind the last key it may come from NaN, and 0 NaN is NaN
+      if (h0) p[u] = f0 = 0.f;
+      if (h1) p[u + 1] = f1 = 0.f;
     }
     if constexpr (kForm > 0) {
       mul2(p[u], p[u + 1], f0, f1, pf[u], pf[u + 1]);

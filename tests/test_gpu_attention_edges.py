@@ -74,3 +74,24 @@ def test_nan_only_in_the_newest_key():
         got = call(q, k, v)
         assert torch.isnan(got["o"][0, :, 1]).all() and torch.isnan(got["lse"][0, 1]).all()
         assert torch.isfinite(got["o"][0, :, 0]).all() and torch.isfinite(got["lse"][0, 0]).all()
+
+
+@pytest.mark.parametrize("d,dt", [(64, "bf16"), (64, "f16"), (80, "bf16"), (128, "f16")])
+@pytest.mark.parametrize("cap,std", [(5.0, 2.0), (50.0, 0.3)])
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_capped_scores_of_padding_are_never_used(d, dt, cap, std, bias, bad):
+    """Large and small capped scores over keys and values that hold anything behind the lengths."""
+    lens = [200, 130, 0]
+    q, k, v, do = inputs(3, 150, 300, 4, 2, d, dt, 64, std)
+    kw = dict(softcap=cap, causal=True, slopes=torch.tensor([0.1, 0.0, 0.02, 0.3], device="cuda") if bias else None)
+    want = reference(q, k, v, do, k_lens=i32(lens), **kw)
+    for b, n in enumerate(lens):
+        k[b, n:] = bad
+        v[b, n:] = bad
+    got = call(q, k, v, do, k_lens=i32(lens), **kw)
+    for name in ("o", "dq", "dk", "dv"):
+        assert torch.isfinite(got[name]).all(), name
+    compare(got, want, q.dtype)
+    for b, n in enumerate(lens):
+        assert not got["dk"][b, n:].any() and not got["dv"][b, n:].any()
