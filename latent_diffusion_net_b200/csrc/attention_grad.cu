@@ -26,8 +26,15 @@
 // warps a thread issues one product in 80 to 100 cycles, so that one thread for all
 // five was what the others waited for. S of the next tile runs beside dS of this one. P and dS
 // are rounded to the inputs' type (the tensor core takes no other); everything else is
-// FP32. For FP16 inputs P carries a factor 2^shift (taken out of the results again)
-// that keeps the small probabilities of long sequences above FP16's subnormals.
+// FP32. FP16 has too few exponents for them, so for FP16 inputs both carry factors that
+// are powers of two and taken out of the results again:
+//   P   2^shift, from k_len alone (P <= 1, so P 2^shift <= 1024): keeps the small
+//       probabilities of long sequences above FP16's subnormals
+//   dS  is bounded by what dO and V hold, not by k_len: |dS| <= 2 |dO_i| max |v_j|. The
+//       factor brings that bound to 2^14 .. 2^15, whatever a loss scale made of dO: in
+//       dQ one for each row i, in dK one for each CTA (largest |dO_i|, largest |v_j| of
+//       its keys). attn_delta_kernel leaves the norms; rows that see nothing and keys
+//       behind the last one take no part.
 //
 // Measured (BF16): a step of 128 x 128 pairs takes 2.0 us an SM at head_dim 64, 2.6 at 128,
 // 3.5 with capped scores; 2 x 4096 tokens causal, 10 heads of 64 293 us; 9216 tokens, 5
@@ -58,6 +65,12 @@ struct GradArgs {
   const void* d_o;
   float out_scale, v_scale;  // factors of dQ and dK, of dV
   float shift;
+  // FP16: norms of the rows of dO [B][H][qpad] (0 where a row sees nothing), the largest of
+  // each 32 [B][H][qblocks][4], and the largest norm of a row of v in each key tile [B][KV][ktiles]
+  float *do_norm, *do_max, *v_max;
+  const void* v;
+  int64_t vs[3];
+  int64_t row_ctas;          // attn_delta_kernel: CTAs of rows, before those of key tiles
   int64_t s0[3], s1[3];      // output strides: dQ, or dK and dV
   void *out0, *out1;
   float* part;               // FP32 parts [2][slots][128][D]
@@ -69,6 +82,46 @@ struct __align__(64) GradMaps {
   CUtensorMap q, k, v, d_o;
 };
 
+// FP16: the largest norm of the rows of v in one key tile, rows behind the last key left
+// out; 16 lanes a row.
+__device__ __forceinline__ void tile_norm(const GradArgs& g, int64_t w) {
+  __shared__ uint32_t top;
+  const AttnArgs& a = g.f;
+  const int kt = (int)(w % a.ktiles), kv = (int)(w / a.ktiles % a.KV), b = (int)(w / a.ktiles / a.KV);
+  if (threadIdx.x == 0) top = 0;
+  __syncthreads();
+  const int d = (threadIdx.x & 15) * 8, end = min(keys_of(a, b), (kt + 1) * kTile);
+  float m = 0.f;
+  bool odd = false;  // NaN, which a maximum would pass over
+#pragma unroll 4
+  for (int k = 0; k < kTile; k += 16) {
+    const int j = kt * kTile + k + (int)(threadIdx.x >> 4);
+    uint4 x = make_uint4(0u, 0u, 0u, 0u);
+    if (j < end && d < a.D)
+      x = *reinterpret_cast<const uint4*>(static_cast<const __half*>(g.v) + b * g.vs[0] + j * g.vs[1] + kv * g.vs[2] + d);
+    float u[8], s = 0.f;
+    unpack_vec<__half, 8>(x, u);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s = fmaf(u[e], u[e], s);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    odd = odd || s != s;
+    m = fmaxf(m, s);
+  }
+  m = odd ? INFINITY : sqrtf(m);
+  // numbers that are not negative compare like their bits
+  const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+  if ((threadIdx.x & 31) == 0) atomicMax(&top, most);
+  __syncthreads();
+  if (threadIdx.x == 0) g.v_max[w] = __uint_as_float(top);
+}
+// FP16: the power of two that brings 2 `bound` below 2^15 (and to 2^14 at least); 1 where the
+// bound is 0 or no number.
+__device__ __forceinline__ float ds_factor(float bound) {
+  const int e = (int)(__float_as_uint(bound) >> 23) - 127;  // bound in 2^e .. 2^(e + 1)
+  return e > -100 && e < 100 ? __uint_as_float((uint32_t)(127 + 13 - e) << 23) : 1.f;
+}
+
 // -lse in log2 units and -delta for rows up to qpad: 2^shift lanes share a row, eight
 // head dimensions each, and take four rows so that eight loads are under way.
 template <typename T>
@@ -77,6 +130,12 @@ __global__ void __launch_bounds__(256) attn_delta_kernel(const __grid_constant__
   pdl_trigger();
   const AttnArgs& a = g.f;
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.err = 0;
+  if constexpr (Elem<T>::kF16) {
+    if (blockIdx.x >= g.row_ctas) {
+      tile_norm(g, blockIdx.x - g.row_ctas);
+      return;
+    }
+  }
   const int sub = threadIdx.x & ((1 << shift) - 1), groups = 256 >> shift;
   const int64_t rows = (int64_t)a.B * a.H * g.qpad, r0 = blockIdx.x * (int64_t)groups * 4 + (threadIdx.x >> shift);
   uint4 x[4], y[4];
@@ -113,12 +172,18 @@ __global__ void __launch_bounds__(256) attn_delta_kernel(const __grid_constant__
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const int64_t r = r0 + k * groups;
-    float u[8], v[8], s = 0.f;
+    float u[8], v[8], s = 0.f, n = 0.f;
     unpack_vec<T, 8>(x[k], u);
     unpack_vec<T, 8>(y[k], v);
 #pragma unroll
     for (int e = 0; e < 8; ++e) s = fmaf(u[e], v[e], s);
     for (int o = 1 << shift >> 1; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if constexpr (Elem<T>::kF16) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) n = fmaf(v[e], v[e], n);
+      for (int o = 1 << shift >> 1; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+      if (sub == 0 && r < rows) g.do_norm[to[k]] = lse[k] == -INFINITY ? 0.f : n == n ? sqrtf(n) : INFINITY;
+    }
     if (sub == 0 && r < rows) {
       g.nlse[to[k]] = lse[k] == -INFINITY ? -INFINITY : fmaf(-lse[k], kLog2e, g.shift);
       g.ndelta[to[k]] = -s;
@@ -227,10 +292,10 @@ __device__ __forceinline__ void pack16(const float* f, uint32_t* pk) {
 }
 
 // Half `side` of the columns of one row of an accumulator: to the output (scaled), or to
-// the FP32 part.
+// the FP32 part. For FP16 inputs `back` takes the row's own factor out first.
 template <typename T, int NB, bool WIDE>
 __device__ __forceinline__ void store_row(uint32_t tacc, int side, bool have, bool in, int D, float scale, T* dst,
-                                          bool wide, float* part) {
+                                          bool wide, float* part, float back) {
 #pragma unroll 1
   for (int c = side * NB * 32; c < (side + 1) * NB * 32; c += 32) {
     if (c >= D) break;
@@ -243,6 +308,10 @@ __device__ __forceinline__ void store_row(uint32_t tacc, int side, bool have, bo
       for (int u = 0; u < 32; ++u) r[u] = 0u;
     }
     if (!in) continue;
+    if constexpr (Elem<T>::kF16) {
+#pragma unroll
+      for (int u = 0; u < 32; ++u) r[u] = __float_as_uint(__uint_as_float(r[u]) * back);
+    }
     if (part) {
       store_part32(part + c, r, D - c);
     } else {
@@ -367,6 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* pv_done = bars + 18 + kDocRing;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 19 + kDocRing);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  uint32_t* do_top = tmem_slot + 2;  // FP16: bits of the largest |dO| of the key head's queries
   const RecordRing ring{recs, rec_full, rec_empty, abort_flag, a.err};
   const DocRing docs{sdocs, doc_full, abort_flag, a.err};
 
@@ -385,6 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(pv_done, 1);
     *abort_flag = 0;
+    *do_top = 0;
     fence_barrier_init();
     tma_prefetch_desc(&maps.q);
     tma_prefetch_desc(&maps.k);
@@ -491,6 +562,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     ScoreTerms st;
     st.to = kTile;
     st.doc = a.k_doc && j < a.Nk ? a.k_doc[(int64_t)b * a.Nk + j] : 0;
+    [[maybe_unused]] float ds_mul = 1.f;  // the CTA's factor of dS, without P's
+    if constexpr (f16) {
+      const int n = a.G * g.qblocks * 4;
+      const uint32_t* const norms =
+          reinterpret_cast<const uint32_t*>(g.do_max) + ((int64_t)b * a.H + kv * a.G) * g.qblocks * 4;
+      uint32_t top = 0;
+      for (int i = threadIdx.x; i < n; i += 32 * kComputeWarps) top = max(top, norms[i]);
+      top = __reduce_max_sync(0xffffffffu, top);
+      if (lane == 0) atomicMax(do_top, top);
+      asm volatile("bar.sync 1, %0;" ::"n"(32 * kComputeWarps) : "memory");
+      ds_mul = ds_factor(__uint_as_float(*do_top) * g.v_max[((int64_t)b * a.KV + kv) * a.ktiles + kt]) * g.v_scale;
+    }
     bool alive = true;
     int t = 0;
     for (;; ++t) {
@@ -565,6 +648,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           score_grads<false>(q, nd, pf + e, ds);
         else
           score_grads<true>(q, nd, pf + e, ds);
+        if constexpr (f16) {
+#pragma unroll
+          for (int u = 0; u < 16; u += 2) mul2(ds[u], ds[u + 1], ds_mul, ds_mul, ds[u], ds[u + 1]);
+        }
         pack16<T>(ds, pk + e / 2);
         if (!Tm::kApart) tmem_st_x8(tDsr + e / 2, pk + e / 2);
       }
@@ -589,7 +676,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       float* part = nullptr;
       if (own.slot >= 0) part = g.part + ((which * g.slots + own.slot) * kTile + j - j0) * a.D;
       store_row<T, NB, !SHAPED>((which ? tDv : tDk) + lane_off, cq & 1, t > 0, j < a.Nk, a.D, which ? g.v_scale : g.out_scale,
-                       dst, wide_rows(which ? g.out1 : g.out0, which ? g.s1 : g.s0, a.D), part);
+                       dst, wide_rows(which ? g.out1 : g.out0, which ? g.s1 : g.s0, a.D), part,
+                       which ? 1.f : 1.f / ds_mul);
     }
   }
   settle(abort_flag);
@@ -629,14 +717,15 @@ struct DqWalk : TileWalk<RowTiles> {
 };
 
 // The end of a dq unit, one query row per thread: dQ = scale (dS K - e P K) and the
-// corrected delta, or (given `part`) the parts of a cut item. Out of line: its registers
+// corrected delta, or (given `part`) the parts of a cut item; `back` as in store_row(). Out of line: its registers
 // would compete with the loop's. All by value, as in the forward kernel.
 template <typename T, int NB, bool WIDE>
 __device__ __noinline__ void store_dq(T* dst, bool wide, float* part, float* part_k, float* row_e, int D, float scale,
-                                      int side, uint32_t tDq, uint32_t tPk, bool some, bool valid, float e) {
+                                      int side, uint32_t tDq, uint32_t tPk, bool some, bool valid, float e,
+                                      float back) {
   if (part) {
-    store_row<T, NB, WIDE>(tDq, side, some, valid, D, 1.f, dst, wide, part);
-    store_row<T, NB, WIDE>(tPk, side, some, valid, D, 1.f, dst, wide, part_k);
+    store_row<T, NB, WIDE>(tDq, side, some, valid, D, 1.f, dst, wide, part, back);
+    store_row<T, NB, WIDE>(tPk, side, some, valid, D, 1.f, dst, wide, part_k, 1.f);
     if (valid && side == 0) *row_e = e;
     return;
   }
@@ -656,8 +745,10 @@ __device__ __noinline__ void store_dq(T* dst, bool wide, float* part, float* par
     for (int y = 0; y < 8; ++y) {
       float f[2];
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
-        f[x] = some ? scale * fmaf(-e, __uint_as_float(q[2 * y + x]), __uint_as_float(r[2 * y + x])) : 0.f;
+      for (int x = 0; x < 2; ++x) {
+        const float d = __uint_as_float(r[2 * y + x]);
+        f[x] = some ? scale * fmaf(-e, __uint_as_float(q[2 * y + x]), Elem<T>::kF16 ? d * back : d) : 0.f;
+      }
       w[y] = Elem<T>::pack(f[0], f[1]);
     }
     if (WIDE && wide) {
@@ -870,6 +961,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     st.from = 0;
     int nk = 0, lim = 0, pos = 0;
     float nlse = 0.f, ndelta = 0.f;
+    [[maybe_unused]] float ds_mul = 1.f;  // the row's factor of dS, without P's
     const bool wide = wide_rows(g.out0, g.s0, a.D);
     float e0 = 0.f, e1 = 0.f;  // the row's sum of P (dP - delta) over this half's columns
     for (int r = 0;; ++r) {
@@ -885,6 +977,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         lim = a.causal ? min(nk, max(pos + 1, rec->pre)) : nk;
         nlse = g.nlse[at];
         ndelta = g.ndelta[at];
+        if constexpr (f16) {
+          const float norm = g.do_norm[at];
+          const uint32_t* const vm =
+              reinterpret_cast<const uint32_t*>(g.v_max) + ((int64_t)rec->b * a.KV + rec->head / a.G) * a.ktiles;
+          uint32_t v = 0;
+          for (int k = lane; k < a.ktiles; k += 32) v = max(v, vm[k]);
+          v = __reduce_max_sync(0xffffffffu, v);
+          ds_mul = ds_factor(norm * __uint_as_float(v)) * g.v_scale;
+          const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(norm));
+          if (cq == 0 && lane == 0)
+            g.do_max[(((int64_t)rec->b * a.H + rec->head) * g.qblocks + rec->i0 / kTile) * 4 + q4] = __uint_as_float(most);
+        }
         st.doc = a.q_doc && i < a.Nq ? a.q_doc[(int64_t)rec->b * a.Nq + i] : 0;
         if (SHAPED) st.slope = a.slopes ? a.slopes[rec->head] * kLog2e : 0.f;
         e0 = e1 = 0.f;
@@ -957,6 +1061,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             score_grads<true>(q, nd, p + e, ds);
 #pragma unroll
           for (int y = 0; y < 16; y += 2) add2(e0, e1, ds[y], ds[y + 1], e0, e1);
+          if constexpr (f16) {
+#pragma unroll
+            for (int y = 0; y < 16; y += 2) mul2(ds[y], ds[y + 1], ds_mul, ds_mul, ds[y], ds[y + 1]);
+          }
           if constexpr (SHAPED) {
 #pragma unroll
             for (int y = 0; y < 16; y += 2)
@@ -996,7 +1104,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (valid && !part && cq == 0) g.ndelta[((int64_t)b * a.H + h) * g.qpad + i] = ndelta - err;
           store_dq<T, NB, !SHAPED>(static_cast<T*>(g.out0) + b * g.s0[0] + i * g.s0[1] + h * g.s0[2], wide,
                           part ? g.part + at * a.D : nullptr, g.part + (g.slots * kTile + at) * a.D, g.part_e + at, a.D,
-                          g.out_scale, cq, tDq + lane_off, tPk + lane_off, some, valid, err);
+                          g.out_scale, cq, tDq + lane_off, tPk + lane_off, some, valid, err, 1.f / ds_mul);
         }
         tc_fence_before();
       }
@@ -1081,6 +1189,7 @@ struct GradPlan {
   int qblocks, ktiles, qpad;
   Cut dkv, dq;
   size_t rows_bytes, part_bytes;
+  size_t do_max_bytes, v_max_bytes;  // FP16 (which has do_norm's rows too), else 0
 };
 // Time in steps of one SM, which holds one CTA: units start longest first and the last ones
 // end about half the longest unit's steps after the average (of the cut ones where the rest
@@ -1130,6 +1239,9 @@ GradPlan plan_grad(const sd_attention_cfg& c) {
   p.dkv = plan_cut(c, dkv_items, walk, walk * past, dkv_items * walk * seen);
   p.dq = plan_cut(c, dq_items, p.ktiles, p.ktiles * before, (double)dq_items * p.ktiles * seen);
   p.rows_bytes = up256((size_t)c.batch * c.heads * p.qpad * 4);
+  const bool f16 = c.dtype == SD_DTYPE_F16;
+  p.do_max_bytes = f16 ? up256((size_t)c.batch * c.heads * p.qblocks * 16) : 0;
+  p.v_max_bytes = f16 ? up256((size_t)c.batch * c.kv_heads * p.ktiles * 4) : 0;
   p.part_bytes = up256(std::max((size_t)p.dkv.slots * 2 * kTile * c.head_dim * 4,
                                 (size_t)p.dq.slots * kTile * (2 * c.head_dim + 1) * 4));
   return p;
@@ -1155,7 +1267,16 @@ sd_status backward(AttnCall& c) {
   g.qblocks = p.qblocks;
   g.nlse = reinterpret_cast<float*>(c.ws);
   g.ndelta = reinterpret_cast<float*>(c.ws + p.rows_bytes);
-  g.part = reinterpret_cast<float*>(c.ws + 2 * p.rows_bytes);
+  uint8_t* w = c.ws + 2 * p.rows_bytes;
+  if (f16) {
+    g.do_norm = reinterpret_cast<float*>(w);
+    g.do_max = reinterpret_cast<float*>(w += p.rows_bytes);
+    g.v_max = reinterpret_cast<float*>(w += p.do_max_bytes);
+    w += p.v_max_bytes;
+  }
+  g.part = reinterpret_cast<float*>(w);
+  g.v = c.v;
+  for (int i = 0; i < 3; ++i) g.vs[i] = c.vs[i];
   g.lse = c.lse;
   g.d_o = c.d_o;
   if (f16)
@@ -1182,12 +1303,14 @@ sd_status backward(AttnCall& c) {
   const double act = 2.0 * s.batch * s.head_dim;
   if (s.q_len) {
     const int64_t rows = (int64_t)s.batch * s.heads * p.qpad;
-    sdp::Scope sc("attn_delta", sdp::F_OTHER, 0, 2 * act * s.q_len * s.heads, c.st);
+    sdp::Scope sc("attn_delta", sdp::F_OTHER, 0, act * (2.0 * s.q_len * s.heads + (f16 ? s.k_len * s.kv_heads : 0)), c.st);
     int lanes = 0;
     while (8 << lanes < s.head_dim) ++lanes;
     const int64_t per = 4 * (256 >> lanes);
-    OP_TRY(launched(
-        launch_pdl(attn_delta_kernel<T>, dim3((unsigned)((rows + per - 1) / per)), dim3(256), 0, c.st, g, lanes)));
+    g.row_ctas = (rows + per - 1) / per;
+    const int64_t ctas = g.row_ctas + (f16 ? (int64_t)s.batch * s.kv_heads * p.ktiles : 0);
+    if (ctas > INT32_MAX) return SD_ERR_UNSUPPORTED;
+    OP_TRY(launched(launch_pdl(attn_delta_kernel<T>, dim3((unsigned)ctas), dim3(256), 0, c.st, g, lanes)));
   }
   if (!s.q_len) OP_TRY(launched(cudaMemsetAsync(c.args.err, 0, sizeof(int), c.st)));
   JoinArgs j;
@@ -1265,7 +1388,7 @@ sd_status backward(AttnCall& c) {
 
 size_t attn_grad_space(const sd_attention_cfg& c) {
   const GradPlan p = plan_grad(c);
-  return 2 * p.rows_bytes + p.part_bytes;
+  return (c.dtype == SD_DTYPE_F16 ? 3 : 2) * p.rows_bytes + p.do_max_bytes + p.v_max_bytes + p.part_bytes;
 }
 
 template <typename T>

@@ -95,3 +95,63 @@ def test_capped_scores_of_padding_are_never_used(d, dt, cap, std, bias, bad):
     compare(got, want, q.dtype)
     for b, n in enumerate(lens):
         assert not got["dk"][b, n:].any() and not got["dv"][b, n:].any()
+
+
+def f16_gradients(scale, nq, nk, d, seed, h=2, kv=1, **kw):
+    """Against 64 bits with dO of that size. The gradients' own subnormal numbers end at 2^-24: half a step of it an
+    element comes on top of the roundings."""
+    q, k, v, do = inputs(1, nq, nk, h, kv, d, "f16", seed)
+    do = (do.float() * scale).half()
+    got, want = call(q, k, v, do, **kw), reference(q, k, v, do, **kw)
+    for name in ("dq", "dk", "dv"):
+        w = want[name]
+        assert w.abs().max().item() < 3e4, "the true gradient has to fit"
+        assert torch.isfinite(got[name]).all(), name
+        tol = (2 if name == "dv" else 4) * 2.0 ** -11 + 1e-5 + 2.0 ** -25 * w.numel() ** 0.5 / w.norm().item()
+        err = R.rel(got[name], w)
+        assert err < tol, (name, err, tol)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("nk", [4096, 16384])
+@pytest.mark.parametrize("scale", [2.0 ** -8, 1.0, 4096.0])
+def test_f16_gradients_over_long_rows(scale, nk, d):
+    """Rows that see all keys, and rows of the same call that see four (large probabilities)."""
+    f16_gradients(scale, 200, nk, d, 65)
+    doc = i32([packed([4] * 32 + [nk // 2], nk)])
+    rows = torch.arange(200, device="cuda", dtype=torch.int32)[None] % 34
+    f16_gradients(scale / 4, 200, nk, d, 66, q_doc=rows, k_doc=doc)
+
+
+def test_f16_gradients_with_one_large_row():
+    """A row of dO 2^12 times the others, peaked and capped scores, parts of long walks, shared heads."""
+    q, k, v, do = inputs(2, 700, 9000, 6, 2, 64, "f16", 67, 1.5)
+    do[1, 600, 4] *= 2.0 ** 12
+    for kw in (dict(causal=True), dict(causal=True, softcap=30.0, k_lens=i32([9000, 8000]))):
+        got, want = call(q, k, v, do, **kw), reference(q, k, v, do, **kw)
+        for name in ("dq", "dk", "dv"):
+            assert torch.isfinite(got[name]).all(), name
+            w = want[name]
+            tol = (2 if name == "dv" else 4) * 2.0 ** -11 + 1e-5 + 2.0 ** -25 * w.numel() ** 0.5 / w.norm().item()
+            assert R.rel(got[name], w) < tol, (name, R.rel(got[name], w), tol)
+        # the other rows of dq by themselves: their factor is their own
+        g, w = got["dq"].double().clone(), want["dq"].clone()
+        g[1, 600, 4] = w[1, 600, 4] = 0
+        assert R.rel(g, w) < 4 * 2.0 ** -11 + 1e-5 + 2.0 ** -25 * w.numel() ** 0.5 / w.norm().item()
+
+
+def test_f16_gradients_ignore_values_that_no_key_holds():
+    """What lies behind the lengths, or in the dO of rows that see nothing, takes no part in any scaling."""
+    q, k, v, do = inputs(2, 300, 500, 4, 2, 64, "f16", 68)
+    kw = dict(k_lens=i32([500, 200]), causal=True)
+    do[1, :100] = 0
+    want = call(q, k, v, do, **kw)
+    k[1, 200:] = v[1, 200:] = 6e4
+    do[1, :100] = 3e4  # positions below zero
+    got = call(q, k, v, do, **kw)
+    for name in want:
+        assert torch.equal(got[name], want[name]), name
+    v[1, 200:] = math.inf
+    got = call(q, k, v, do, **kw)
+    for name in want:
+        assert torch.equal(got[name], want[name]), name
