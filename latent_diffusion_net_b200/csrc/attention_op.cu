@@ -409,6 +409,14 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
           if constexpr (SHAPED) {
             if (a.cap_out != 0.f) {
+              // the form is chosen by what may be seen: neither padding nor what the last call
+              // left in the rows beyond tq * G takes part
+              const int lc = whole && valid ? 64 : lim - j0 - half * 64;  // lim is 0 in those rows
+              if (__any_sync(0xffffffffu, lc < 64)) {
+#pragma unroll
+                for (int c = 0; c < 64; ++c)
+                  if (c >= lc) sv[c] = 0u;
+              }
               float top = 0.f;
 #pragma unroll
               for (int c = 0; c < 64; c += 2)

@@ -155,3 +155,35 @@ def test_f16_gradients_ignore_values_that_no_key_holds():
     got = call(q, k, v, do, **kw)
     for name in want:
         assert torch.equal(got[name], want[name]), name
+
+
+@pytest.mark.parametrize("d,dt", [(64, "bf16"), (128, "f16")])
+def test_capped_results_do_not_depend_on_padding(d, dt):
+    """Small scores beside the cap, and padding whose scores would be large: the same bits for every padding."""
+    lens = [200, 130]
+    q, k, v, do = inputs(2, 150, 300, 4, 2, d, dt, 69, 0.5)
+    outs = []
+    for fill in (0.0, 200.0, -3.0, math.nan):
+        for b, n in enumerate(lens):
+            k[b, n:] = fill
+            v[b, n:] = fill
+        outs.append(call(q, k, v, do, softcap=8.0, k_lens=i32(lens)))
+        outs.append(call(q, k, v, do, softcap=8.0, k_lens=i32(lens), causal=True, prefix=i32([40, 0])))
+    for i, got in enumerate(outs[2:]):
+        for name in got:
+            assert torch.equal(got[name], outs[i % 2][name]), (i, name)
+
+
+@pytest.mark.parametrize("h,kv,d", [(3, 1, 64), (12, 1, 64), (6, 2, 128), (5, 1, 80)])
+def test_capped_results_do_not_depend_on_earlier_calls(h, kv, d):
+    """A tile of 128 / 3 (or 5, 12) tokens leaves rows over, whose place in the chip's memory holds what the last call
+    left there."""
+    q, k, v, do = inputs(2, 512, 640, h, kv, d, "bf16", 70, 0.5)
+    before = inputs(4, 1280, 640, 16, 16, d, "bf16", 71)
+    outs = []
+    for size in (0.0, 300.0, 1.0):
+        call((before[0].float() * size).bfloat16(), before[1], before[2])
+        outs.append(call(q, k, v, do, softcap=8.0))
+    for got in outs[1:]:
+        for name in got:
+            assert torch.equal(got[name], outs[0][name]), name
