@@ -20,10 +20,13 @@
 // 144 rows x 1280 forward 7.6 us, which is launch, cluster barriers and two latencies.
 //
 // A thread owns one 16-byte vector of channels for all its rows (channel terms
-// stay in registers, a warp reads whole sectors whatever C/G is); sums are FP32
-// per channel, relative to the first value of the share's group, and shares
-// are joined from (mean, sum of squared deviations), so a mean far from zero
-// costs no precision.
+// stay in registers, a warp reads whole sectors whatever C/G is). Statistics are FP32
+// pairs (mean, sum of squared deviations from it) at every level: a thread's rows
+// about their own mean, the threads of a channel, the channels of a group, the shares.
+// Every term of the squares is positive and part of the result, so neither a mean far
+// from zero nor an outlier, wherever it stands, costs precision (squares about the
+// first value of a group lost 2^-24 (distance / deviation)^2 a value: with an outlier in
+// that place y was off by up to 1e-3).
 #include <string.h>
 
 #include <algorithm>
@@ -305,6 +308,65 @@ __device__ __forceinline__ void reduce_rows(float* red, float* ch, int C, int c_
   }
 }
 
+// Joins the row threads' pairs (mean, squares about it) of V channels into the channels'
+// pairs ch[c] and ch[C + c]: squares = sum of squares_t + n_t (mean_t - mean)^2. As many lanes
+// share a channel as the CTA has (one lane each: 4 x 9216 x 320 forward 31 us instead of 29).
+template <int V>
+__device__ __forceinline__ void reduce_moments(float* red, float* ch, int C, int c_first, int tx, int ty, int cols_t,
+                                               int rows_t, bool active, int64_t rows, const float (&mean)[V],
+                                               const float (&sq)[V]) {
+  __syncthreads();
+  if (active) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      red[(ty * 2 * V + j) * cols_t + tx] = mean[j];
+      red[(ty * 2 * V + V + j) * cols_t + tx] = sq[j];
+    }
+  }
+  __syncthreads();
+  const int64_t full = rows / rows_t;
+  const int more = (int)(rows - full * rows_t);  // the first threads take a row more
+  const float n0 = (float)full, n1 = (float)(full + 1), inv = rows > 0 ? 1.f / (float)rows : 0.f;
+  int lanes = 1;
+  while (lanes < 32 && 2 * lanes * V * cols_t <= kThreads) lanes *= 2;
+  const int total = V * cols_t * lanes, sub = threadIdx.x & (lanes - 1);
+  for (int i = threadIdx.x; i - (int)(threadIdx.x & 31) < total; i += kThreads) {  // whole warps
+    const int at = min(i, total - 1) / lanes, j = at / cols_t, t = at % cols_t;
+    const float *m = red + j * cols_t + t, *q = m + V * cols_t;
+    const int step = 2 * V * cols_t;
+    const float base = m[0];
+    float d = 0.f, s = 0.f;
+#pragma unroll 4
+    for (int y = sub; y < rows_t; y += lanes) d = fmaf(y < more ? n1 : n0, m[y * step] - base, d);
+    for (int o = lanes >> 1; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+    d *= inv;
+#pragma unroll 4
+    for (int y = sub; y < rows_t; y += lanes) {
+      const float e = (m[y * step] - base) - d;
+      s += fmaf((y < more ? n1 : n0) * e, e, q[y * step]);
+    }
+    for (int o = lanes >> 1; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (sub == 0 && i < total) {
+      const int c = c_first + t * V + j;
+      ch[c] = base + d;
+      ch[C + c] = s;
+    }
+  }
+}
+// A warp joins the pairs of a group's channels (`rows` values each).
+__device__ __forceinline__ float2 join_channels(const float* ch, int C, int cpg, int64_t rows) {
+  const int lane = threadIdx.x & 31;
+  const float base = ch[0];
+  float d = 0.f, s = 0.f;
+  for (int i = lane; i < cpg; i += 32) d += ch[i] - base;
+  d = warp_sum(d) / (float)cpg;
+  for (int i = lane; i < cpg; i += 32) {
+    const float e = (ch[i] - base) - d;
+    s += fmaf((float)rows * e, e, ch[C + i]);
+  }
+  return make_float2(base + d, warp_sum(s));
+}
+
 // ------------------------------------------------------------------ one slice per cluster
 // All of a thread's rows are asked for ahead (16 forward, 8 of both tensors backward)
 // straight into shared memory: with four in registers 4 x 9216 x 320 took 30 us, so 22.
@@ -385,11 +447,9 @@ __global__ void __launch_bounds__(kThreads) gn_cluster_fwd_kernel(const __grid_c
   pdl_trigger();
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.err = 0;
   const T* x = static_cast<const T*>(a.x) + s.n * a.rows * a.ldx;
-  const T* first = x + s.r0 * a.ldx + s.c0;
-  const bool some = s.r0 < s.r1;
-  float k[V], s0[V], s1[V];
+  float mean[V], sq[V];
 #pragma unroll
-  for (int j = 0; j < V; ++j) s0[j] = s1[j] = 0.f;
+  for (int j = 0; j < V; ++j) mean[j] = sq[j] = 0.f;
   if (s.active) {
     constexpr int kAhead = 16;
     const int n = thread_rows(s.r0 + s.ty, s.r1, s.rows_t);
@@ -401,38 +461,42 @@ __global__ void __launch_bounds__(kThreads) gn_cluster_fwd_kernel(const __grid_c
       copy_commit();
     }
     load_affine<T, V>(a, c, t);
-    Groups gk(s.tx * V, a.cpg);
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int g = gk.next();
-      k[j] = some ? -Elem<T>::to_f(first[g * a.cpg]) : 0.f;
-    }
+    // the mean about the first row, then the squares about the mean from shared memory
+    float nk[V], f[V];
     for (int i = 0; i < n; ++i, p += step) {
       copy_wait<kAhead - 1>();
-      float f[V];
       unpack_vec<T, V>(own[i * kThreads], f);
       if (i + kAhead < n) copy_async(own + (i + kAhead) * kThreads, p);
       copy_commit();
-      v_add<V>(f, k, f);
-      v_add<V>(s0, f, s0);
-      v_fma<V>(f, f, s1, s1);
+      if (i == 0) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) nk[j] = -f[j];
+      }
+      v_add<V>(f, nk, f);
+      v_add<V>(mean, f, mean);
+    }
+    if (n > 0) {
+      const float inv = -1.f / (float)n;
+#pragma unroll
+      for (int j = 0; j < V; ++j) nk[j] = fmaf(mean[j], inv, nk[j]);
+#pragma unroll 4
+      for (int i = 0; i < n; ++i) {
+        unpack_vec<T, V>(own[i * kThreads], f);
+        v_add<V>(f, nk, f);
+        v_fma<V>(f, f, sq, sq);
+      }
+#pragma unroll
+      for (int j = 0; j < V; ++j) mean[j] = -nk[j];
     }
   }
-  reduce_rows<V>(red, ch, a.width, 0, s.tx, s.ty, s.cols, s.rows_t, s.active, s0, s1);
+  reduce_moments<V>(red, ch, a.width, 0, s.tx, s.ty, s.cols, s.rows_t, s.active, s.r1 - s.r0, mean, sq);
   __syncthreads();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int g = warp; g < groups; g += kThreads / 32) {
-    float sum = 0.f, sq = 0.f;
-    for (int i = lane; i < a.cpg; i += 32) {
-      sum += ch[g * a.cpg + i];
-      sq += ch[a.width + g * a.cpg + i];
-    }
-    sum = warp_sum(sum);
-    sq = warp_sum(sq);
+    const float2 v = join_channels(ch + g * a.cpg, a.width, a.cpg, s.r1 - s.r0);
     if (lane == 0) {
-      const float d = some ? sum / ((float)(s.r1 - s.r0) * a.cpg) : 0.f;
-      part[2 * g] = (some ? Elem<T>::to_f(first[g * a.cpg]) : 0.f) + d;
-      part[2 * g + 1] = fmaxf(sq - sum * d, 0.f);
+      part[2 * g] = v.x;
+      part[2 * g + 1] = v.y;
     }
   }
   cluster_sync();
@@ -635,59 +699,75 @@ __global__ void __launch_bounds__(kThreads) gn_stats_share_kernel(const __grid_c
   const int chunk = blockIdx.x % a.chunks;
   const int64_t r0 = chunk * a.chunk_rows, r1 = min(a.rows, r0 + a.chunk_rows);
   const T* x = static_cast<const T*>(a.x) + n * a.rows * a.ldx;
-  const T* first = x + r0 * a.ldx;
   const int cols = a.C / V;
   for (int c0 = 0; c0 < cols; c0 += kThreads) {
     const int cols_t = min(kThreads, cols - c0), rows_t = kThreads / cols_t;
     const int tx = threadIdx.x % cols_t, ty = threadIdx.x / cols_t;
     const bool active = ty < rows_t;
     const int c = (c0 + tx) * V;
-    float k[V], s0[V], s1[V];
-    Groups gk(c, a.cpg);
+    float mean[V], sq[V];
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int g = gk.next();
-      k[j] = active ? -Elem<T>::to_f(first[g * a.cpg]) : 0.f;
-      s0[j] = s1[j] = 0.f;
-    }
+    for (int j = 0; j < V; ++j) mean[j] = sq[j] = 0.f;
     if (active) {
+      // eight rows at a time: their mean (about the thread's first row), the squares about
+      // it, and the pair joined to that of the rows before
       constexpr int U = 8;
       const T* p = x + (r0 + ty) * a.ldx + c;
       const int64_t step = rows_t * a.ldx;
-      for (int left = thread_rows(r0 + ty, r1, rows_t); left > 0; left -= U, p += U * step) {
+      const int n = thread_rows(r0 + ty, r1, rows_t);
+      float nk[V];
+      if (n > 0) {
+        to_float<T, V>(load_raw<T, V>(p), nk);
+#pragma unroll
+        for (int j = 0; j < V; ++j) nk[j] = -nk[j];
+      }
+      for (int left = n; left > 0; left -= U, p += U * step) {
         Raw<T, V> raw[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
           if (u < left) raw[u] = load_raw<T, V>(p + u * step);
+        float f[V], d[V], kb[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) d[j] = 0.f;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           if (u >= left) break;
-          float f[V];
           to_float<T, V>(raw[u], f);
-          v_add<V>(f, k, f);
-          v_add<V>(s0, f, s0);
-          v_fma<V>(f, f, s1, s1);
+          v_add<V>(f, nk, f);
+          v_add<V>(d, f, d);
+        }
+        const float before = (float)(n - left), cnt = (float)min(left, U), inv = 1.f / cnt;
+        const float w = cnt / (before + cnt), wn = before * w;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          kb[j] = fmaf(-inv, d[j], nk[j]);
+          d[j] = fmaf(inv, d[j], -mean[j]);  // this mean less the one before
+          mean[j] = fmaf(w, d[j], mean[j]);
+          sq[j] = fmaf(wn * d[j], d[j], sq[j]);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (u >= left) break;
+          to_float<T, V>(raw[u], f);
+          v_add<V>(f, kb, f);
+          v_fma<V>(f, f, sq, sq);
         }
       }
+      if (n > 0) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) mean[j] -= nk[j];
+      }
     }
-    reduce_rows<V>(red, ch, a.C, c0 * V, tx, ty, cols_t, rows_t, active, s0, s1);
+    reduce_moments<V>(red, ch, a.C, c0 * V, tx, ty, cols_t, rows_t, active, r1 - r0, mean, sq);
   }
   __syncthreads();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const float cnt = (float)(r1 - r0) * a.cpg, inv = 1.f / cnt;
   for (int g = warp; g < a.G; g += kThreads / 32) {
-    float s = 0.f, q = 0.f;
-    for (int i = lane; i < a.cpg; i += 32) {
-      s += ch[g * a.cpg + i];
-      q += ch[a.C + g * a.cpg + i];
-    }
-    s = warp_sum(s);
-    q = warp_sum(q);
+    const float2 v = join_channels(ch + g * a.cpg, a.C, a.cpg, r1 - r0);
     if (lane == 0) {
-      const float d = s * inv;
       float* o = a.pg + ((n * a.G + g) * a.chunks + chunk) * 2;
-      o[0] = Elem<T>::to_f(first[g * a.cpg]) + d;
-      o[1] = fmaxf(q - s * d, 0.f);
+      o[0] = v.x;
+      o[1] = v.y;
     }
   }
 }

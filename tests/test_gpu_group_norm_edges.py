@@ -1,0 +1,61 @@
+"""Group norm at the edges of what its description allows, on a B200: outliers and steps in the data, results in place,
+other eps."""
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+if not torch.cuda.is_available():
+    pytest.skip("no CUDA device", allow_module_level=True)
+
+import operator_refs as R  # noqa: E402
+from latent_diffusion_net_b200 import binding as B  # noqa: E402
+from test_gpu_group_norm import ACT, DT, close, make  # noqa: E402
+
+
+def forward(x, groups, act="none", eps=1e-5):
+    n, r, c = x.shape
+    code = {torch.bfloat16: B.SD_DTYPE_BF16, torch.float16: B.SD_DTYPE_F16, torch.float32: B.SD_DTYPE_F32}[x.dtype]
+    cfg = B.group_norm_cfg(n, r, c, groups=groups, eps=eps, act=ACT[act], dtype=code)
+    ws = torch.full((B.sd_group_norm_workspace_size(cfg),), 0xFF, dtype=torch.uint8, device="cuda")
+    y, stats = torch.empty_like(x), torch.empty(n, groups, 2, device="cuda")
+    B.sd_group_norm_fwd(cfg, x, None, None, y, stats, ws, ws.numel())
+    return y, stats
+
+
+# one kernel in clusters, two kernels with whole vectors, two kernels element by element
+PIVOT_SHAPES = [(1, 3000, 64, 8), (1, 9216, 320, 32), (1, 150000, 128, 32), (2, 40000, 60, 20)]
+
+
+def statistics_hold(x, groups, where):
+    """Sums are FP32 over per-thread runs and a tree, of positive terms only: rstd within 2^-18, the mean within 2^-18 of
+    the standard deviation; y - away from the outliers - within 2^-18 of its size and of the mean's error."""
+    y, stats = forward(x, groups)
+    want, mean, rstd = R.group_norm(x.double(), None, None, groups, 1e-5, "none")
+    assert ((stats[..., 1].double() / rstd - 1).abs().max().item()) < 2.0 ** -18
+    far = (mean.abs() * rstd).max().item()
+    assert (((stats[..., 0].double() - mean) * rstd).abs().max().item()) < 2.0 ** -18 + 2.0 ** -23 * far
+    err = (y.double() - want).abs() - 2.0 ** -18 * (1 + want.abs()) - 2.0 ** -22 * far
+    assert err[where].max().item() < 0, err[where].max().item()
+
+
+@pytest.mark.parametrize("n,r,c,groups", PIVOT_SHAPES)
+@pytest.mark.parametrize("size", [30.0, 100.0, 1000.0])
+def test_outlier_in_the_first_place(n, r, c, groups, size):
+    """One value far from all others, wherever a pass over the rows begins."""
+    _, x, _ = make(n, r, c, "f32", 21, mean=0.0, std=1.0)
+    where = torch.ones_like(x, dtype=torch.bool)
+    for row in (0, r // 2, r - 1):
+        x[:, row, ::c // groups] = size
+        where[:, row] = False
+    statistics_hold(x, groups, where)
+
+
+@pytest.mark.parametrize("n,r,c,groups", PIVOT_SHAPES)
+@pytest.mark.parametrize("border", [1, 40, 700])
+def test_padded_border(n, r, c, groups, border):
+    """Zeros in the first and last rows, values far from zero between them: x - mean is exact to 2^-24 of the mean, so y
+    carries 2^-22 |mean| rstd more."""
+    _, x, _ = make(n, r, c, "f32", 22, mean=100.0, std=1.0)
+    x[:, :border] = 0
+    x[:, r - border:] = 0
+    statistics_hold(x, groups, torch.ones_like(x, dtype=torch.bool))
