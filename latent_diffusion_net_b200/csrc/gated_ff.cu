@@ -475,6 +475,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<EPI>, 1)
 // Bound by reading the weights: a warp per weight row (or a few, which share the
 // tokens' values), each lane 16 bytes at a time, several loads under way, FP32 sums
 // joined across the warp.
+// What an earlier kernel may still be writing when one of these starts (x, h, FP32 parts) is
+// read by plain loads behind pdl_wait(): no __restrict__ and no read-only path, which are
+// for memory that nobody writes while the kernel lives.
 constexpr int kSmallThreads = 256;
 constexpr int kSmallTokens = 4;  // 5 to 8 tokens took 29 to 30 us at 1280 x 5120, the tensor cores 24
 
@@ -517,10 +520,8 @@ __device__ __forceinline__ float lane_sum(float v) {
 
 // h = v act(z) (and pre = [v | z]): a warp reads the value and gate rows of C hidden columns.
 template <typename T, int MT, int C>
-__global__ void __launch_bounds__(kSmallThreads) ff_small_up_kernel(const T* __restrict__ x, const T* __restrict__ w1,
-                                                                    const T* __restrict__ b1, T* __restrict__ pre,
-                                                                    T* __restrict__ h, int M, int D, int F, int act,
-                                                                    int* err) {
+__global__ void __launch_bounds__(kSmallThreads) ff_small_up_kernel(const T* x, const T* w1, const T* b1, T* pre, T* h,
+                                                                    int M, int D, int F, int act, int* err) {
   constexpr int R = 2 * C;
   pdl_wait();
   pdl_trigger();
@@ -544,7 +545,7 @@ __global__ void __launch_bounds__(kSmallThreads) ff_small_up_kernel(const T* __r
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int r = 0; r < R; ++r)
-        v[u][r] = i0 + 32 * u < D / 8 ? __ldg(w[r] + i0 + 32 * u) : make_uint4(0u, 0u, 0u, 0u);
+        v[u][r] = i0 + 32 * u < D / 8 ? w[r][i0 + 32 * u] : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
     for (int u = 0; u < U; ++u)
       dot_step<T, MT, R>(v[u], x + (int64_t)(i0 + 32 * u) * 8, D, M, i0 + 32 * u < D / 8, acc);
@@ -573,8 +574,7 @@ __global__ void __launch_bounds__(kSmallThreads) ff_small_up_kernel(const T* __r
 // call writes them, and the kernel before this one started only after everything ahead
 // of the call had finished.
 template <typename T, int MT, int R>
-__global__ void __launch_bounds__(kSmallThreads) ff_small_down_kernel(const T* __restrict__ h, const T* __restrict__ w2,
-                                                                      const T* __restrict__ b2, T* __restrict__ y, int M,
+__global__ void __launch_bounds__(kSmallThreads) ff_small_down_kernel(const T* h, const T* w2, const T* b2, T* y, int M,
                                                                       int F, int N) {
   __shared__ float red[kSmallThreads / 32][R][MT];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp & 3;
@@ -623,8 +623,8 @@ __global__ void __launch_bounds__(kSmallThreads) ff_small_down_kernel(const T* _
 
 // out = sum of the splits (in order) + bias, 8 columns per thread.
 template <typename T>
-__global__ void __launch_bounds__(256) ff_join_kernel(const float* __restrict__ partial, int splits, int64_t M, int N,
-                                                      const T* __restrict__ bias, T* __restrict__ out) {
+__global__ void __launch_bounds__(256) ff_join_kernel(const float* partial, int splits, int64_t M, int N,
+                                                      const T* bias, T* out) {
   pdl_wait();
   pdl_trigger();
   const int64_t vecs = M * N / 8, stride = M * N;
@@ -668,8 +668,8 @@ __global__ void __launch_bounds__(256) ff_join_kernel(const float* __restrict__ 
 // Column sums of dy [rows][n] for db2: a CTA sums 256 columns over a share of the rows
 // into an FP32 part.
 template <typename T>
-__global__ void __launch_bounds__(256) ff_colsum_kernel(const T* __restrict__ m, int n, int64_t rows, int64_t chunk_rows,
-                                                        float* __restrict__ part, int* clear_err) {
+__global__ void __launch_bounds__(256) ff_colsum_kernel(const T* m, int n, int64_t rows, int64_t chunk_rows,
+                                                        float* part, int* clear_err) {
   __shared__ float red[8][256];
   pdl_wait();
   pdl_trigger();

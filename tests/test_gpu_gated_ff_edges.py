@@ -31,3 +31,28 @@ def test_workspace_on_a_16_byte_boundary(m, d, f, offset):
     for name in want:
         assert torch.equal(got[name], want[name]), name
     assert (buf[:offset] == 0xA5).all() and (buf[offset + n:] == 0xA5).all()
+
+
+@pytest.mark.parametrize("m", [1, 2, 4])
+def test_input_written_by_the_call_before(m):
+    """Few tokens through a chain of blocks without anything between the calls: each block reads what the one before it
+    has just written, and h within a block."""
+    blocks = [make(m, 256, 1024, 256, "bf16", seed=40 + i)[0] for i in range(6)]
+    cfg, ws = plan(m, 256, 1024, 256, "silu", "bf16")
+    spaces = [torch.empty_like(ws) for _ in blocks]
+    x0 = blocks[0]["x"]
+    step, want = x0, []
+    for p in blocks:
+        y = forward({**p, "x": step}, cfg, ws)
+        torch.cuda.synchronize()
+        want.append(y)
+        step = y
+    for _ in range(20):
+        outs = [torch.zeros_like(x0) for _ in blocks]
+        src = x0
+        for p, space, y in zip(blocks, spaces, outs):
+            B.sd_gated_ff_fwd(cfg, p["w1"], p["b1"], p["w2"], p["b2"], src, None, y, space, space.numel())
+            src = y
+        torch.cuda.synchronize()
+        for got, w in zip(outs, want):
+            assert torch.equal(got, w)
