@@ -507,7 +507,7 @@ typedef struct {
 /* Device arrays, each may be NULL (as may the struct):
  *   k_lens [batch]: keys that exist, clamped to 0 .. k_len. Keys and values behind
  *     them are never used, whatever they hold (their gradients are zeros).
- *   prefix [batch]: keys that every query sees although causal; needs causal.
+ *   prefix [batch]: keys that every query sees although causal (below 0: none); needs causal.
  *   q_doc [batch][q_len] and k_doc [batch][k_len]: document ids, both or none.
  *   slopes [heads]: FP32 distance slopes, constants of the call.
  * Keys and values hidden by anything but k_lens have to be finite. */

@@ -78,7 +78,7 @@ struct AttnArgs {
 __device__ __forceinline__ int keys_of(const AttnArgs& a, int b) {
   return a.k_lens ? min(max(a.k_lens[b], 0), a.Nk) : a.Nk;
 }
-__device__ __forceinline__ int prefix_of(const AttnArgs& a, int b) { return a.prefix ? a.prefix[b] : 0; }
+__device__ __forceinline__ int prefix_of(const AttnArgs& a, int b) { return a.prefix ? max(a.prefix[b], 0) : 0; }
 
 // Which key tiles 128 query rows (tokens i0 .. i1 of sequence b) may see: those
 // before lim_any whose documents meet [lo, hi]; every row sees all of the tiles

@@ -187,3 +187,11 @@ def test_capped_results_do_not_depend_on_earlier_calls(h, kv, d):
     for got in outs[1:]:
         for name in got:
             assert torch.equal(got[name], outs[0][name]), name
+
+
+def test_prefix_of_any_negative_number_is_none():
+    q, k, v, do = inputs(3, 300, 300, 2, 2, 64, "bf16", 72)
+    want = call(q, k, v, do, causal=True)
+    got = call(q, k, v, do, causal=True, prefix=i32([-2 ** 31, -1, 0]))
+    for name in want:
+        assert torch.equal(got[name], want[name]), name
