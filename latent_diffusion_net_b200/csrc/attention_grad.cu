@@ -192,8 +192,9 @@ __global__ void __launch_bounds__(256) attn_delta_kernel(const __grid_constant__
 }
 
 // What becomes of one 16-column chunk of scores: p, p times the cap's slope, and that
-// slope as FP16 pairs where asked for. The scores' columns lie `c` columns from the diagonal's column p0.
+// slope times kSlopeScale as FP16 pairs where asked for. The scores' columns lie `c` columns from the diagonal's column p0.
 // SHAPED: cap or bias; MASKED: columns outside [from, to) and of other documents are hidden.
+constexpr float kSlopeScale = 32768.f;  // slopes down to 2^-29 keep FP16's full precision
 struct ScoreTerms {
   float slope, p0;
   int from, to, doc;
@@ -226,11 +227,11 @@ __device__ __forceinline__ void probabilities(const AttnArgs& a, const ScoreTerm
       mul2(__uint_as_float(r[u]), __uint_as_float(r[u + 1]), a.cap_in, a.cap_in, x0, x1);
       if constexpr (kForm == 1) {
         tanh_small2(x0, x1, x0, x1);
+        fma2v(-x0, -x1, x0, x1, 1.f, 1.f, f0, f1);
       } else {
-        x0 = tanh_acc(x0);
-        x1 = tanh_acc(x1);
+        x0 = tanh_slope(x0, f0);
+        x1 = tanh_slope(x1, f1);
       }
-      fma2v(-x0, -x1, x0, x1, 1.f, 1.f, f0, f1);
       fma2v(x0, x1, a.cap_out, a.cap_out, nl[u], nl[u + 1], x0, x1);
     } else {
       fma2v(__uint_as_float(r[u]), __uint_as_float(r[u + 1]), a.sl2, a.sl2, nl[u], nl[u + 1], x0, x1);
@@ -259,7 +260,10 @@ __device__ __forceinline__ void probabilities(const AttnArgs& a, const ScoreTerm
       pf[u + 1] = p[u + 1];
     }
     if constexpr (SHAPED) {
-      if (fac) fac[u / 2] = pack_f16x2(f0, f1);
+      if (fac) {
+        mul2(f0, f1, kSlopeScale, kSlopeScale, f0, f1);
+        fac[u / 2] = pack_f16x2(f0, f1);
+      }
     }
   };
   if constexpr (SHAPED) {
@@ -299,8 +303,8 @@ __device__ __forceinline__ void pack16(const float* f, uint32_t* pk) {
 }
 
 // Half `side` of the columns of one row of an accumulator: to the output (scaled), or to
-// the FP32 part. For FP16 inputs `back` takes the row's own factor out first.
-template <typename T, int NB, bool WIDE>
+// the FP32 part. BACK: `back` takes the row's own factor out first.
+template <typename T, int NB, bool WIDE, bool BACK>
 __device__ __forceinline__ void store_row(uint32_t tacc, int side, bool have, bool in, int D, float scale, T* dst,
                                           bool wide, float* part, float back) {
 #pragma unroll 1
@@ -315,7 +319,7 @@ __device__ __forceinline__ void store_row(uint32_t tacc, int side, bool have, bo
       for (int u = 0; u < 32; ++u) r[u] = 0u;
     }
     if (!in) continue;
-    if constexpr (Elem<T>::kF16) {
+    if constexpr (BACK) {
 #pragma unroll
       for (int u = 0; u < 32; ++u) r[u] = __float_as_uint(__uint_as_float(r[u]) * back);
     }
@@ -682,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       T* dst = static_cast<T*>(which ? g.out1 : g.out0) + b * os[0] + j * os[1] + kv * os[2];
       float* part = nullptr;
       if (own.slot >= 0) part = g.part + ((which * g.slots + own.slot) * kTile + j - j0) * a.D;
-      store_row<T, NB, !SHAPED>((which ? tDv : tDk) + lane_off, cq & 1, t > 0, j < a.Nk, a.D, which ? g.v_scale : g.out_scale,
+      store_row<T, NB, !SHAPED, f16>((which ? tDv : tDk) + lane_off, cq & 1, t > 0, j < a.Nk, a.D, which ? g.v_scale : g.out_scale,
                        dst, wide_rows(which ? g.out1 : g.out0, which ? g.s1 : g.s0, a.D), part,
                        which ? 1.f : 1.f / ds_mul);
     }
@@ -724,15 +728,15 @@ struct DqWalk : TileWalk<RowTiles> {
 };
 
 // The end of a dq unit, one query row per thread: dQ = scale (dS K - e P K) and the
-// corrected delta, or (given `part`) the parts of a cut item; `back` as in store_row(). Out of line: its registers
+// corrected delta, or (given `part`) the parts of a cut item; BACK as in store_row(). Out of line: its registers
 // would compete with the loop's. All by value, as in the forward kernel.
-template <typename T, int NB, bool WIDE>
+template <typename T, int NB, bool WIDE, bool BACK>
 __device__ __noinline__ void store_dq(T* dst, bool wide, float* part, float* part_k, float* row_e, int D, float scale,
                                       int side, uint32_t tDq, uint32_t tPk, bool some, bool valid, float e,
                                       float back) {
   if (part) {
-    store_row<T, NB, WIDE>(tDq, side, some, valid, D, 1.f, dst, wide, part, back);
-    store_row<T, NB, WIDE>(tPk, side, some, valid, D, 1.f, dst, wide, part_k, 1.f);
+    store_row<T, NB, WIDE, BACK>(tDq, side, some, valid, D, 1.f, dst, wide, part, back);
+    store_row<T, NB, WIDE, false>(tPk, side, some, valid, D, 1.f, dst, wide, part_k, 1.f);
     if (valid && side == 0) *row_e = e;
     return;
   }
@@ -754,7 +758,7 @@ __device__ __noinline__ void store_dq(T* dst, bool wide, float* part, float* par
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const float d = __uint_as_float(r[2 * y + x]);
-        f[x] = some ? scale * fmaf(-e, __uint_as_float(q[2 * y + x]), Elem<T>::kF16 ? d * back : d) : 0.f;
+        f[x] = some ? scale * fmaf(-e, __uint_as_float(q[2 * y + x]), BACK ? d * back : d) : 0.f;
       }
       w[y] = Elem<T>::pack(f[0], f[1]);
     }
@@ -1012,7 +1016,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         st.to = (flags & kOneDoc) && rec->doc != st.doc ? 0 : lim - j0;
         st.p0 = (float)(j0 - pos);
-        // P, and the cap's slope as FP16 pairs (in [0, 1]: off by 2^-12, below dS's own rounding)
+        // P, and the cap's slope as FP16 pairs: half the registers of FP32, which would spill. Off
+        // by 2^-11 of itself: an eighth of dS's own rounding in BF16, as much as it in FP16
         float p[32];
         [[maybe_unused]] uint32_t fac[SHAPED ? 16 : 1];
         uint32_t pk[16];
@@ -1069,8 +1074,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int y = 0; y < 16; y += 2) add2(e0, e1, ds[y], ds[y + 1], e0, e1);
           if constexpr (f16) {
+            const float by = SHAPED ? ds_mul / kSlopeScale : ds_mul;
 #pragma unroll
-            for (int y = 0; y < 16; y += 2) mul2(ds[y], ds[y + 1], ds_mul, ds_mul, ds[y], ds[y + 1]);
+            for (int y = 0; y < 16; y += 2) mul2(ds[y], ds[y + 1], by, by, ds[y], ds[y + 1]);
           }
           if constexpr (SHAPED) {
 #pragma unroll
@@ -1109,9 +1115,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool part = rec->slot >= 0, valid = i < a.Nq;
           const float err = e * g.v_scale;
           if (valid && !part && cq == 0) g.ndelta[((int64_t)b * a.H + h) * g.qpad + i] = ndelta - err;
-          store_dq<T, NB, !SHAPED>(static_cast<T*>(g.out0) + b * g.s0[0] + i * g.s0[1] + h * g.s0[2], wide,
+          // dS carries the row's factor, for other types kSlopeScale where it took the cap's slope
+          store_dq<T, NB, !SHAPED, f16 || SHAPED>(static_cast<T*>(g.out0) + b * g.s0[0] + i * g.s0[1] + h * g.s0[2], wide,
                           part ? g.part + at * a.D : nullptr, g.part + (g.slots * kTile + at) * a.D, g.part_e + at, a.D,
-                          g.out_scale, cq, tDq + lane_off, tPk + lane_off, some, valid, err, 1.f / ds_mul);
+                          g.out_scale, cq, tDq + lane_off, tPk + lane_off, some, valid, err,
+                          f16 ? 1.f / ds_mul : 1.f / kSlopeScale);
         }
         tc_fence_before();
       }

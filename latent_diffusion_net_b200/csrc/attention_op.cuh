@@ -280,6 +280,13 @@ struct DocRing {
 __device__ __forceinline__ float tanh_acc(float x) {
   return fmaf(-2.f, fast_rcp(1.f + fast_ex2(2.f * kLog2e * x)), 1.f);
 }
+// The same, and the slope 1 - tanh^2 = 4 E / (1 + E)^2 with E = e^2x (held below 2^126): right
+// to 2^-18 of itself however far x is beyond the cap, where 1 - t t would be rounding.
+__device__ __forceinline__ float tanh_slope(float x, float& slope) {
+  const float e = fast_ex2(fminf(2.f * kLog2e * x, 126.f)), r = fast_rcp(1.f + e);
+  slope = (e * r) * (4.f * r);
+  return fmaf(-2.f, r, 1.f);
+}
 
 // tanh of two values of magnitude at most 0.75 as x times a polynomial in x^2 (fitted
 // for the least relative error, 3e-8): packed FP32 only, where the form above takes

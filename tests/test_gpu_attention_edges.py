@@ -195,3 +195,39 @@ def test_prefix_of_any_negative_number_is_none():
     got = call(q, k, v, do, causal=True, prefix=i32([-2 ** 31, -1, 0]))
     for name in want:
         assert torch.equal(got[name], want[name]), name
+
+
+@pytest.mark.parametrize("d,dt", [(64, "bf16"), (128, "bf16"), (64, "f16")])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_saturated_cap_keeps_its_gradient(d, dt, sign):
+    """All scores far beyond the cap: the slope 1 - tanh^2 is near 4 e^-14 and has to be right relative to itself. Scores
+    are near 14 c for a cap of 2 c: x = 7 with a small spread. FP32 scores (sums of D products, 2^-22 of 14 c) move
+    ln(slope) by less than 1e-5.
+
+    q and k lie close to one direction, so that dq = scale sum_j dS_ij k_j adds long vectors to a short one. Roundings of
+    dS are independent and at most u each: as a 2-norm they move dq by u scale (sum_ij dS_ij^2 |k_j|^2)^1/2, which is A u
+    relative to |dq| with A from the 64-bit dS. dS is rounded once, its slope once (FP16 pairs), and dP takes in v and do
+    unrounded; P's rounding enters through delta's correction, once more: 3 A u, and the result's own u. dk likewise with q."""
+    c = 1.0 if dt == "bf16" else 0.5
+    g = torch.Generator(device="cuda").manual_seed(73)
+    t = torch.bfloat16 if dt == "bf16" else torch.float16
+    base = torch.sign(torch.randn(d, generator=g, device="cuda"))
+    n = lambda tok: (base + 0.05 * torch.randn(1, tok, 2, d, generator=g, device="cuda"))  # noqa: E731
+    q, k = n(140).to(t), (sign * n(200)).to(t)
+    v, do = (torch.randn(1, tok, 2, d, generator=g, device="cuda") for tok in (200, 140))
+    v, do = v.to(t), (do * (8192.0 if dt == "f16" else 1.0)).to(t)  # gradients well above FP16's smallest numbers
+    kw = dict(scale=14 * c / d, softcap=2 * c)
+    got, want = call(q, k, v, do, **kw), reference(q, k, v, do, **kw)
+    q8, k8, v8, do8 = (x[0].double().transpose(0, 1) for x in (q, k, v, do))  # [H, tokens, D]
+    th = torch.tanh(q8 @ k8.transpose(1, 2) * (kw["scale"] / kw["softcap"]))
+    p = torch.softmax(kw["softcap"] * th, dim=-1)
+    dp = do8 @ v8.transpose(1, 2)
+    ds2 = (p * (dp - (p * dp).sum(-1, keepdim=True)) / torch.cosh(torch.atanh(th)) ** 2) ** 2
+    u = R.HALF_STEP[t]
+    assert R.rel(got["o"], want["o"]) < 2 * u + 1e-5 and R.rel(got["dv"], want["dv"]) < 2 * u + 1e-5
+    for name, other in (("dq", ds2 @ (k8 ** 2).sum(-1, keepdim=True)),
+                        ("dk", ds2.transpose(1, 2) @ (q8 ** 2).sum(-1, keepdim=True))):
+        a = kw["scale"] * other.sum().sqrt().item() / want[name].norm().item()
+        err = R.rel(got[name], want[name])
+        print(name, "A", a, "err", err, "tol", (1 + 3 * a) * u + 1e-5)
+        assert err < (1 + 3 * a) * u + 1e-5, (name, err, a)
