@@ -28,8 +28,8 @@
 // are rounded to the inputs' type (the tensor core takes no other); everything else is
 // FP32. FP16 has too few exponents for them, so for FP16 inputs both carry factors that
 // are powers of two and taken out of the results again:
-//   P   2^shift, from k_len alone (P <= 1, so P 2^shift <= 1024): keeps the small
-//       probabilities of long sequences above FP16's subnormals
+//   P   2^15 (P <= 1, and FP16 ends at 2^16): probabilities, times the cap's slope in dq,
+//       keep their full precision down to 2^-29
 //   dS  is bounded by what dO and V hold, not by k_len: |dS| <= 2 |dO_i| max |v_j|. The
 //       factor brings that bound to 2^14 .. 2^15, whatever a loss scale made of dO: in
 //       dQ one for each row i, in dK one for each CTA (largest |dO_i|, largest |v_j| of
@@ -64,7 +64,7 @@ struct GradArgs {
   const float* lse;
   const void* d_o;
   float out_scale, v_scale;  // factors of dQ and dK, of dV
-  float shift;
+  float shift;               // of P, as a power of two
   // FP16: norms of the rows of dO [B][H][qpad] (0 where a row sees nothing), the largest of
   // each 32 [B][H][qblocks][4], and the largest norm of a row of v in each key tile [B][KV][ktiles]
   float *do_norm, *do_max, *v_max;
@@ -1294,8 +1294,7 @@ sd_status backward(AttnCall& c) {
   for (int i = 0; i < 3; ++i) g.vs[i] = c.vs[i];
   g.lse = c.lse;
   g.d_o = c.d_o;
-  if (f16)
-    while (s.k_len >> ((int)g.shift + 11)) g.shift += 1.f;  // P 2^shift <= 1024
+  g.shift = f16 ? 15.f : 0.f;
   g.v_scale = exp2f(-g.shift);
   g.out_scale = c.args.sl2 / kLog2e * g.v_scale;
 

@@ -231,3 +231,22 @@ def test_saturated_cap_keeps_its_gradient(d, dt, sign):
         err = R.rel(got[name], want[name])
         print(name, "A", a, "err", err, "tol", (1 + 3 * a) * u + 1e-5)
         assert err < (1 + 3 * a) * u + 1e-5, (name, err, a)
+
+
+def test_f16_small_probabilities_of_short_rows():
+    """Keys far below a row's largest score: P near 2^-20, below FP16's normal numbers, is all that their dv and dk come
+    from. Each such gradient against 64 bits by itself, as large as the others through a large dO."""
+    q, k, v, do = inputs(1, 130, 100, 2, 2, 64, "f16", 76, 0.1)
+    q[..., 0] = 4.0
+    k[:, :50, :, 0], k[:, 50:, :, 0] = 14.0, -14.0  # scores +-7, so that P falls by e^-14
+    do = (do.float() * 2.0 ** 14).half()
+    got, want = call(q, k, v, do), reference(q, k, v, do)
+    for name, rounds in (("dv", 2), ("dk", 4)):
+        for part in (slice(0, 50), slice(50, 100)):
+            w = want[name][:, part]
+            if name == "dk":
+                w, g = w[..., 1:], got[name][:, part, :, 1:]  # q's first column is the same everywhere: it adds up dS
+            else:
+                g = got[name][:, part]
+            tol = rounds * 2.0 ** -11 + 1e-5 + 2.0 ** -25 * w.numel() ** 0.5 / w.norm().item()
+            assert R.rel(g, w) < tol, (name, part, R.rel(g, w), tol)
