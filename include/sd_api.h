@@ -510,7 +510,8 @@ typedef struct {
  *   prefix [batch]: keys that every query sees although causal (below 0: none); needs causal.
  *   q_doc [batch][q_len] and k_doc [batch][k_len]: document ids, both or none.
  *   slopes [heads]: FP32 distance slopes, constants of the call.
- * Keys and values hidden by anything but k_lens have to be finite. */
+ * Keys and values hidden by anything but k_lens have to be finite. A query that sees no
+ * key may hold anything, and so may its d_o. */
 typedef struct {
   const int32_t* k_lens;
   const int32_t* prefix;

@@ -607,6 +607,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_wait_all(s_full, t & 1, abort_flag, a.err)))
         break;
       tc_fence_after();
+      if (!whole && cq < 2) {
+        // queries that see nothing count as zeros in the sums, whatever they hold: S of this
+        // tile is done, and dP is waited for before dO is touched
+        const bool dead = i0 + row < a.Nq && sstat[s * 256 + row] == -INFINITY;
+        if (__any_sync(0xffffffffu, dead)) {
+          if (cq && !(alive = mbar_wait_all(dp_full, t & 1, abort_flag, a.err))) break;
+          if (dead) {
+#pragma unroll
+            for (int c = 0; c < NB; ++c) {
+              uint4* z = reinterpret_cast<uint4*>((cq ? sDo : sQ) + s * kBytes + c * kBlockBytes + row * 128);
+#pragma unroll
+              for (int y = 0; y < 8; ++y) z[y] = make_uint4(0u, 0u, 0u, 0u);
+            }
+          }
+          fence_async_smem();
+        }
+      }
       float pf[32];
       uint32_t pk[16];
 #pragma unroll

@@ -250,3 +250,21 @@ def test_f16_small_probabilities_of_short_rows():
                 g = got[name][:, part]
             tol = rounds * 2.0 ** -11 + 1e-5 + 2.0 ** -25 * w.numel() ** 0.5 / w.norm().item()
             assert R.rel(g, w) < tol, (name, part, R.rel(g, w), tol)
+
+
+@pytest.mark.parametrize("d,dt", [(64, "bf16"), (128, "bf16"), (80, "f16")])
+@pytest.mark.parametrize("cap", [0.0, 10.0])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_queries_that_see_nothing_may_hold_anything(d, dt, cap, bad):
+    """Rows before a sequence's first key, and rows whose document no key has: nothing of their q and dO goes anywhere."""
+    q, k, v, do = inputs(2, 400, 300, 4, 2, d, dt, 77)
+    doc = torch.zeros(2, 400, dtype=torch.int32, device="cuda")
+    doc[0, 350:370] = 9
+    kw = dict(causal=True, k_lens=i32([300, 180]), q_doc=doc, k_doc=doc[:, :300] * 0, softcap=cap)
+    want = call(q, k, v, do, **kw)
+    dead = torch.isneginf(want["lse"])[:, 0]  # [batch, q]
+    assert 300 < dead.sum() < 500 and (dead == torch.isneginf(want["lse"]).all(dim=1)).all()
+    q[dead], do[dead] = bad, bad
+    got = call(q, k, v, do, **kw)
+    for name in want:
+        assert torch.equal(got[name], want[name]), name
