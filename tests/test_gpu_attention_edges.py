@@ -268,3 +268,25 @@ def test_queries_that_see_nothing_may_hold_anything(d, dt, cap, bad):
     got = call(q, k, v, do, **kw)
     for name in want:
         assert torch.equal(got[name], want[name]), name
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+def test_strided_output_and_its_gradient(dt):
+    """o and d_o as columns of a wider tensor: read and written in place, what lies between stays."""
+    q, k, v, do = inputs(2, 190, 210, 4, 2, 64, dt, 74)
+    want = reference(q, k, v, do, causal=True)
+    wide = 4 * 64 + 40
+    buf = torch.full((2, 190, wide), 3.0, dtype=q.dtype, device="cuda")
+    o = buf[:, :, 16:16 + 256].view(2, 190, 4, 64)
+    gbuf = torch.full((2, 190, wide), math.nan, dtype=q.dtype, device="cuda")
+    gbuf[:, :, 16:16 + 256] = do.view(2, 190, 256)
+    d_o = gbuf[:, :, 16:16 + 256].view(2, 190, 4, 64)
+    cfg = B.attention_cfg(2, 190, 210, 4, 2, 64, dtype=B.SD_DTYPE_BF16 if dt == "bf16" else B.SD_DTYPE_F16, causal=True,
+                          o_stride=o.stride()[:3])
+    ws = torch.full((B.sd_attention_workspace_size(cfg),), 0xFF, dtype=torch.uint8, device="cuda")
+    lse = torch.empty(2, 4, 190, device="cuda")
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    B.sd_attention_fwd(cfg, q, k, v, None, o, lse, ws, ws.numel())
+    B.sd_attention_bwd(cfg, q, k, v, None, o, lse, d_o, dq, dk, dv, ws, ws.numel())
+    compare({"o": o, "lse": lse, "dq": dq, "dk": dk, "dv": dv}, want, q.dtype)
+    assert (buf[:, :, :16] == 3).all() and (buf[:, :, 272:] == 3).all()

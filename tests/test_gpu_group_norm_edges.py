@@ -59,3 +59,36 @@ def test_padded_border(n, r, c, groups, border):
     x[:, :border] = 0
     x[:, r - border:] = 0
     statistics_hold(x, groups, torch.ones_like(x, dtype=torch.bool))
+
+
+@pytest.mark.parametrize("n,r,c", [(2, 500, 64), (1, 60000, 128)])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_gradient_in_place(n, r, c, dt):
+    """dx in the place of x, and of dy: the same bits as beside them."""
+    _, x, g = make(n, r, c, dt, 23)
+    _, dy, _ = make(n, r, c, dt, 24, 0, 0.1, 1.0)
+    gamma = (1 + 0.1 * torch.randn(c, generator=g, device="cuda")).to(x.dtype)
+    cfg = B.group_norm_cfg(n, r, c, groups=8, dtype=DT[dt][1])
+    ws = torch.full((B.sd_group_norm_workspace_size(cfg),), 0xFF, dtype=torch.uint8, device="cuda")
+    y, stats = torch.empty_like(x), torch.empty(n, 8, 2, device="cuda")
+    B.sd_group_norm_fwd(cfg, x, gamma, None, y, stats, ws, ws.numel())
+    outs = []
+    for place in (None, "x", "dy"):
+        a, b = x.clone(), dy.clone()
+        dx = {"x": a, "dy": b, None: torch.empty_like(x)}[place]
+        dg, db = torch.empty(c, device="cuda"), torch.empty(c, device="cuda")
+        B.sd_group_norm_bwd(cfg, a, gamma, None, stats, b, dx, dg, db, ws, ws.numel())
+        outs.append((dx, dg, db))
+    torch.cuda.synchronize()
+    for other in outs[1:]:
+        assert all(torch.equal(s, t) for s, t in zip(outs[0], other))
+
+
+@pytest.mark.parametrize("eps", [1e-12, 1e-3, 0.5, 30.0])
+def test_eps(eps):
+    for r in (300, 60000):
+        _, x, _ = make(1, r, 64, "f32", 25, mean=0.3, std=0.7)
+        y, stats = forward(x, 8, "silu", eps)
+        want, mean, rstd = R.group_norm(x.double(), None, None, 8, eps, "silu")
+        close(y, want, torch.float32, "y")
+        assert R.rel(stats[..., 1], rstd) < 1e-5
