@@ -613,9 +613,10 @@ sd_status sd_record_end(int32_t* n_entries);
 sd_status sd_record_read(sd_record_entry* out, int32_t capacity, int32_t* n);
 
 /* Test hook for the device-side timeout path (the pages have no counterpart).
- * The next n_launches tensor-core GEMM kernels enqueued by this process first
- * make one thread of every CTA wait on a barrier that nothing completes, for
- * at most spin_limit polls (1 .. 2^24); the wait gives up, raises the device
+ * The next n_launches tensor-core kernels enqueued by this process (the blocks'
+ * GEMM; the products of sd_gated_ff_*, which come from 5 tokens on; attention forward, dq and
+ * dk / dv of sd_attention_*) first make a thread of every CTA wait on a barrier
+ * that nothing completes, for at most spin_limit polls (1 .. 2^24); the wait gives up, raises the device
  * error flag in the workspace header and makes every role of the CTA skip its
  * work, so the kernel loads nothing, computes nothing, writes no output (the
  * output buffer keeps stale values) and releases its tensor memory before it

@@ -189,6 +189,16 @@ bf16* rec_slot(const char* name, int module, int block, int64_t rows, int64_t co
 // Timeout injection for tests (sd_debug_inject_timeout).
 std::atomic<int> g_inject_n{0}, g_inject_spins{0};
 
+}  // namespace
+namespace sdo {
+int injected_spins() {
+  return g_inject_n.load(std::memory_order_relaxed) > 0 && g_inject_n.fetch_sub(1) > 0
+             ? g_inject_spins.load(std::memory_order_relaxed)
+             : 0;
+}
+}  // namespace sdo
+namespace {
+
 // Launch a GEMM problem under a profiling scope with its algorithmic work:
 // FLOPs 2*M*N*K (K = reduction length; alg_k overrides a zero-padded K), bytes
 // = every A source and B matrix read once, the output (and residual) once.
@@ -198,8 +208,7 @@ int launch_gemm(const Ctx& c, const GemmProblem& p0, double alg_k = 0) {
   GemmProblem p = p0;
   p.force_bn = g_force_bn.load(std::memory_order_relaxed);
   p.force_splits = g_force_splits.load(std::memory_order_relaxed);
-  if (g_inject_n.load(std::memory_order_relaxed) > 0 && g_inject_n.fetch_sub(1) > 0)
-    p.hold_spins = g_inject_spins.load(std::memory_order_relaxed);
+  p.hold_spins = sdo::injected_spins();
   double K = 0;
   for (int i = 0; i < p.nseg; ++i) K += 64.0 * p.seg[i].nkb;
   if (alg_k > 0) K = alg_k;

@@ -487,7 +487,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int nk = keys_of(a, b), off = nk - a.Nq, pre = prefix_of(a, b);
   if (warp == 16) {
     HeadWalk walk(KeyTiles(a, b, kt, g.qblocks, off, nk, pre), a.G, own);
-    bool ok = true, whole;
+    bool ok = a.hold_spins == 0 || mbar_wait(kv_full, 0, abort_flag, a.err, (uint32_t)a.hold_spins), whole;
+    ok = __all_sync(0xffffffffu, ok);
     int t = 0;
     for (int tile; ok && (tile = walk.step(a.G, whole)) >= 0; ++t) {
       if (lane == 0) {
@@ -855,7 +856,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 16) {
     int t = 0, n = 0, r = 0, asked = 0;
-    bool ok = true;
+    bool ok = a.hold_spins == 0 || mbar_wait(next_bar, 0, abort_flag, a.err, (uint32_t)a.hold_spins);
+    ok = __all_sync(0xffffffffu, ok);
     for (int x = blockIdx.x; x >= 0 && ok;) {
       const DqUnit u(g, x);
       const int nk = keys_of(a, u.b), pre = prefix_of(a, u.b), kv = u.h / a.G;
@@ -1340,7 +1342,6 @@ sd_status backward(AttnCall& c) {
     const int64_t per = 4 * (256 >> lanes);
     g.row_ctas = (rows + per - 1) / per;
     const int64_t ctas = g.row_ctas + (f16 ? (int64_t)s.batch * s.kv_heads * p.ktiles : 0);
-    if (ctas > INT32_MAX) return SD_ERR_UNSUPPORTED;
     OP_TRY(launched(launch_pdl(attn_delta_kernel<T>, dim3((unsigned)ctas), dim3(256), 0, c.st, g, lanes)));
   }
   if (!s.q_len) OP_TRY(launched(cudaMemsetAsync(c.args.err, 0, sizeof(int), c.st)));
@@ -1353,6 +1354,7 @@ sd_status backward(AttnCall& c) {
   if (s.q_len) {
     // dq first: it corrects delta
     g.f.parts = j.parts = p.dq.parts;
+    g.f.hold_spins = injected_spins();
     g.slots = j.slots = p.dq.slots;
     g.part_e = g.part + (size_t)2 * g.slots * kTile * s.head_dim;
     for (int i = 0; i < 3; ++i) g.s0[i] = j.s[0][i] = c.qs[i];
@@ -1382,6 +1384,7 @@ sd_status backward(AttnCall& c) {
   }
   if (s.k_len) {
     g.f.parts = j.parts = p.dkv.parts;
+    g.f.hold_spins = injected_spins();
     g.slots = j.slots = p.dkv.slots;
     for (int i = 0; i < 3; ++i) {
       g.s0[i] = j.s[0][i] = c.ks[i];

@@ -197,7 +197,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   // barrier's phase.
   if (warp == 8) {
     int t = 0, n = 0, r = 0, asked = 0;
-    bool ok = true;
+    bool ok = a.hold_spins == 0 || mbar_wait(next_bar, 0, abort_flag, a.err, (uint32_t)a.hold_spins);
+    ok = __all_sync(0xffffffffu, ok);
     for (int x = blockIdx.x; x >= 0 && ok;) {
       const Unit u(a, x);
       const int nk = keys_of(a, u.b), pre = prefix_of(a, u.b);
@@ -803,6 +804,7 @@ sd_status forward(AttnCall& c, const FwdPlan& p) {
     OP_TRY((allow_smem<attn_fwd_kernel<T, NB, true>>(Shape<NB>::kSmem, c.dev.index)));
   else
     OP_TRY((allow_smem<attn_fwd_kernel<T, NB, false>>(Shape<NB>::kSmem, c.dev.index)));
+  a.hold_spins = injected_spins();
   auto* kernel = shaped ? attn_fwd_kernel<T, NB, true> : attn_fwd_kernel<T, NB, false>;
   const double pairs = (double)g.batch * g.heads * g.q_len * g.k_len;
   const double bytes = 2.0 * g.batch * g.head_dim * (2.0 * g.q_len * g.heads + 2.0 * g.k_len * g.kv_heads);

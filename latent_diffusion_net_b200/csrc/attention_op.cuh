@@ -73,6 +73,7 @@ struct AttnArgs {
   float* partial_ml;
   int* err;
   int32_t clear_err;
+  int32_t hold_spins;               // tests only: the loading warp first waits, this long, for what never comes
 };
 
 __device__ __forceinline__ int keys_of(const AttnArgs& a, int b) {

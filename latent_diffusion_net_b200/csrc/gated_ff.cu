@@ -69,6 +69,7 @@ struct FfArgs {
   float* colsum;          // EPI_GATE_GRAD: [M / 128][2N] column sums of dpre, or null
   int* err;
   int32_t clear_err;
+  int32_t hold_spins;     // tests only: the loading thread first waits, this long, for what never comes
 };
 
 // 16 elements of T, packed, to consecutive places, and back; n as below.
@@ -189,7 +190,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<EPI>, 1)
       const int bblocks = (half + 63) >> 6;
       int s = 0;
       uint32_t ph = 0, q = 0;
-      bool ok = true;
+      bool ok = args.hold_spins == 0 || mbar_wait(&full[0], 0, abort_flag, args.err, (uint32_t)args.hold_spins);
       for (int u = pair; u < args.units && ok; u += npairs) {
         const int z = u % args.splits, rest = u / args.splits;
         const int m0 = ((rest / args.tiles_n) * 2 + (int)rank) * 128;
@@ -840,6 +841,7 @@ sd_status product(Call& c, const char* name, const Product& p, const void* A, co
   a.act = c.cfg->act;
   a.err = c.err;
   a.clear_err = c.first;
+  a.hold_spins = injected_spins();
   c.first = false;
   const void* bias = a.bias;
   if (g.splits > 1) {

@@ -237,6 +237,10 @@ struct Device {
 // The current device's index and SM count; SD_ERR_NOT_SM100 off compute capability 10.0.
 sd_status current_device(Device* d);
 
+// Polls of the wait that sd_debug_inject_timeout asks the next tensor-core kernel to give up; 0
+// for none (api.cpp).
+int injected_spins();
+
 inline bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) != 0; }
 inline size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 
