@@ -290,3 +290,22 @@ def test_strided_output_and_its_gradient(dt):
     B.sd_attention_bwd(cfg, q, k, v, None, o, lse, d_o, dq, dk, dv, ws, ws.numel())
     compare({"o": o, "lse": lse, "dq": dq, "dk": dk, "dv": dv}, want, q.dtype)
     assert (buf[:, :, :16] == 3).all() and (buf[:, :, 272:] == 3).all()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+def test_workspace_on_a_16_byte_boundary(dt):
+    """A workspace taken out of a larger buffer, with documents and with rows computed in parts: the same bits, and
+    nothing written outside it."""
+    q, k, v, do = inputs(2, 300, 3000, 6, 2, 72, dt, 78)
+    doc = torch.zeros(2, 3000, dtype=torch.int32, device="cuda")
+    doc[:, 1111:] = 1
+    kw = dict(causal=True, q_doc=doc[:, 2700:].contiguous(), k_doc=doc, k_lens=i32([3000, 2900]))
+    want = call(q, k, v, do, **kw)
+    cfg = B.attention_cfg(2, 300, 3000, 6, 2, 72, dtype=B.SD_DTYPE_BF16 if dt == "bf16" else B.SD_DTYPE_F16, causal=True)
+    n = B.sd_attention_workspace_size(cfg)
+    for offset in (16, 48, 240):
+        buf = torch.full((n + 512,), 0xA5, dtype=torch.uint8, device="cuda")
+        got = call(q, k, v, do, ws=buf[offset:offset + n], **kw)
+        for name in want:
+            assert torch.equal(got[name], want[name]), name
+        assert (buf[:offset] == 0xA5).all() and (buf[offset + n:] == 0xA5).all()

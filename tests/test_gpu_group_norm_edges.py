@@ -92,3 +92,25 @@ def test_eps(eps):
         want, mean, rstd = R.group_norm(x.double(), None, None, 8, eps, "silu")
         close(y, want, torch.float32, "y")
         assert R.rel(stats[..., 1], rstd) < 1e-5
+
+
+@pytest.mark.parametrize("n,r,c", [(3, 500, 64), (1, 60000, 128), (2, 3000, 60)])
+def test_workspace_on_a_16_byte_boundary(n, r, c):
+    """A workspace taken out of a larger buffer: the same bits, and nothing written outside it."""
+    _, x, _ = make(n, r, c, "bf16", 26)
+    _, dy, _ = make(n, r, c, "bf16", 27, 0, 0.1, 1.0)
+    cfg = B.group_norm_cfg(n, r, c, groups=4)
+    size = B.sd_group_norm_workspace_size(cfg)
+    outs = []
+    for offset in (0, 16, 240):
+        buf = torch.full((size + 512,), 0xA5, dtype=torch.uint8, device="cuda")
+        ws = buf[offset:offset + size]
+        y, dx, stats = torch.empty_like(x), torch.empty_like(x), torch.empty(n, 4, 2, device="cuda")
+        dg, db = torch.empty(c, device="cuda"), torch.empty(c, device="cuda")
+        B.sd_group_norm_fwd(cfg, x, None, None, y, stats, ws, size)
+        B.sd_group_norm_bwd(cfg, x, None, None, stats, dy, dx, dg, db, ws, size)
+        assert B.sd_query_device_status(ws) == 0
+        assert (buf[:offset] == 0xA5).all() and (buf[offset + size:] == 0xA5).all()
+        outs.append((y, stats, dx, dg, db))
+    for other in outs[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(outs[0], other))
