@@ -206,17 +206,19 @@ __device__ __forceinline__ void probabilities(const AttnArgs& a, const ScoreTerm
   bool small = false;
   if constexpr (SHAPED) {
     if (a.cap_out != 0.f) {
-      // the form is chosen by the columns inside [from, to): padding takes no part
+      // neither padded keys (columns from `to` on, or a row that starts behind its columns) nor
+      // queries that see nothing take part in choosing the form
       float top = 0.f;
 #pragma unroll
       for (int u = 0; u < 16; u += 2) {
         float x0 = fabsf(__uint_as_float(r[u])), x1 = fabsf(__uint_as_float(r[u + 1]));
         if constexpr (MASKED) {
-          if (c + u < s.from || c + u >= s.to) x0 = 0.f;
-          if (c + u + 1 < s.from || c + u + 1 >= s.to) x1 = 0.f;
+          if (c + u >= s.to || nl[u] == -INFINITY) x0 = 0.f;
+          if (c + u + 1 >= s.to || nl[u + 1] == -INFINITY) x1 = 0.f;
         }
         top = max3f(top, x0, x1);
       }
+      if (MASKED && s.from >= kTile) top = 0.f;
       small = __all_sync(0xffffffffu, top * a.cap_in <= kTanhSmall);
     }
   }
