@@ -394,8 +394,9 @@ sd_status sd_vae_decode(const sd_vae_cfg* cfg, const void* packed_w, const void*
  *   - `workspace` holds scratch between the launches of one call and nothing from
  *     one call to the next; it needs no initialisation. Calls that may overlap on
  *     the GPU (other streams, two captured graphs) need workspaces of their own.
- *     After a call, sd_query_device_status(workspace, stream) reports a bounded
- *     wait that gave up;
+ *     After a call that launched a kernel, sd_query_device_status(workspace, stream)
+ *     reports a bounded wait that gave up; one that had nothing to write leaves the
+ *     workspace as it was;
  *   - a workspace size is host arithmetic on the configuration (0 for one that
  *     is refused) and serves the forward and the backward call;
  *   - all work runs on the current device, which must be the one that owns the

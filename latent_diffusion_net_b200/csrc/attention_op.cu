@@ -2,9 +2,10 @@
 // lengths: o = softmax(mask(cap(scale q k^T) - slope |p - j|)) v, one pass over the
 // keys with a running maximum and sum. The backward kernels are in attention_grad.cu.
 //
-// Bound by the exponentials and the tensor cores for long sequences (4 D
-// operations and one exponential a pair; three with a cap), by reading keys and
-// values for single tokens.
+// Long sequences take 4 D operations and one exponential a pair (three with a cap), single
+// tokens the reading of keys and values. Neither is reached: on 9216 tokens x 5 heads of 64 in
+// three documents the exponential unit is busy 53 % of the time and the tensor pipe 18 %; a tile's steps follow one
+// another, and one thread issues its twelve products.
 //
 // A unit of work is 128 query rows: kTile / G tokens with the G query heads that
 // share a key head, so a key tile is read once for all of them. Its key tiles are
@@ -35,7 +36,8 @@
 // the exponentials and the MMA issue take turns; 9216 tokens x 5 heads of 64 190 us (572);
 // 4096 queries x 77 keys, 10 heads, batch 4 29 us, two thirds of it a unit's beginning and
 // end; one FP16 query each on 4096 keys, 16 heads of 128 over 4 key heads, batch 8 24 us
-// with the join (2.1 TB/s of keys and values: the latencies of a short kernel and its join).
+// with the join (2.1 TB/s of keys and values: one stage of K and V at head_dim 128, so that a
+// tile is asked for only when the one before is done, and the join's launch).
 #include "attention_op.cuh"
 
 #include <string.h>
@@ -98,9 +100,8 @@ struct UnitWalk : TileWalk<RowTiles> {
 };
 
 // The end of a unit: one query row per thread, normalised to the output, or its part
-// (given `part`) of a cut item. Out of line: it runs once per unit and its registers would
-// compete with the score row of the loop. All by value: what a reference to the kernel's
-// arguments reads comes from far away (77 keys: 5000 cycles a unit, half of its time).
+// (given `part`) of a cut item. All by value: what a reference to the kernel's arguments
+// reads comes from far away (77 keys: 5000 cycles a unit, half of its time).
 template <typename T, int NB, bool WIDE>
 __device__ __forceinline__ void store_rows(T* dst, float* part, float* ml, float* lse, int D, bool wide, int half,
                                         uint32_t tO, bool some, bool valid, float m, float l) {

@@ -311,12 +311,12 @@ __device__ __forceinline__ float max3f(float a, float b, float c) {
   return y;
 }
 
-// Launches of the backward pass (attention_grad.cu).
 // 32 FP32 values to a row of the output, or of FP32 parts; n of them are inside (a multiple
 // of 8). A thread stores a row of its own, so only 32-byte stores fill whole sectors (WIDE:
 // where `wide` says that rows start on 32-byte boundaries; 9216 tokens forward: 200 us, 190).
-// The kernels with capped or biased scores do without: nvcc 12.9 kept only the first element
-// of their 32-byte stores.
+// The kernels with capped or biased scores do without: in an early form of theirs only the
+// first element of each such store arrived. The cause was not found, and the present form
+// shows nothing of it (forward, with the wide stores put in).
 template <bool WIDE, typename T>
 __device__ __forceinline__ void store_row32(T* p, const float (&f)[32], int n, bool wide) {
 #pragma unroll
@@ -402,6 +402,7 @@ struct AttnCall {
   Device dev;
   cudaStream_t st;
 };
+// The backward pass (attention_grad.cu).
 size_t attn_grad_space(const sd_attention_cfg& c);
 template <typename T>
 sd_status attn_backward(AttnCall& c);

@@ -12,12 +12,14 @@
 //       shared memory of up to eight CTAs: read once, summed, the sums joined
 //       through distributed shared memory, normalised from shared memory
 //   otherwise two kernels: the first sums over a share of an image's rows per CTA,
-//       the second joins the shares and walks the same rows from their end, so that
-//       it finds the rows that the first one read last still in L2
+//       the second joins the shares and walks the same rows from their end, where L2 may
+//       still hold what the first one read last
 // Sums are joined in a fixed order, so results repeat bit for bit.
-// Measured (BF16, SiLU): 768 x 768 x 128 forward 89 us, 302 MB of x and y at 3.4 TB/s (x is
-// read twice, in part from L2); 4 x 9216 rows x 320 forward 22 us, gradients 31 us;
-// 144 rows x 1280 forward 7.6 us, which is launch, cluster barriers and two latencies.
+// Measured (BF16, SiLU): 768 x 768 x 128 forward 92 us, 302 MB of x and y at 3.3 TB/s (x is
+// read twice; the second kernel takes 58 us for 302 MB with cold caches: a CTA loads eight rows
+// a thread, waits and stores, and has nothing under way meanwhile); 4 x 9216 rows x 320 forward
+// 24 us (one wave of 128 CTAs: all load, join, then store), gradients 31 us; 144 rows x 1280
+// forward 8.2 us, which is launch, cluster barriers and two latencies.
 //
 // A thread owns one 16-byte vector of channels for all its rows (channel terms
 // stay in registers, a warp reads whole sectors whatever C/G is). Statistics are FP32
