@@ -193,8 +193,9 @@ __global__ void __launch_bounds__(256) attn_delta_kernel(const __grid_constant__
   }
 }
 
-// What becomes of one 16-column chunk of scores: p, p times the cap's slope, and that
-// slope times kSlopeScale as FP16 pairs where asked for. The scores' columns lie `c` columns from the diagonal's column p0.
+// What becomes of one 16-column chunk of scores: p, p times the cap's slope (pf), and as FP16
+// pairs where asked for the slope times kSlopeScale, or the rest p - pf (REST). The scores'
+// columns lie `c` columns from the diagonal's column p0.
 // SHAPED: cap or bias; MASKED: columns outside [from, to) and of other documents are hidden.
 constexpr float kSlopeScale = 32768.f;  // slopes down to 2^-29 keep FP16's full precision
 struct ScoreTerms {
@@ -202,9 +203,9 @@ struct ScoreTerms {
   int from, to, doc;
   const int32_t* sdoc;  // the columns' documents, or null
 };
-template <bool SHAPED, bool MASKED>
+template <bool SHAPED, bool MASKED, bool REST = false>
 __device__ __forceinline__ void probabilities(const AttnArgs& a, const ScoreTerms& s, const uint32_t (&r)[16], int c,
-                                              const float (&nl)[16], float* p, float* pf, uint32_t* fac = nullptr) {
+                                              const float (&nl)[16], float* p, float* pf, uint32_t* side = nullptr) {
   bool small = false;
   if constexpr (SHAPED) {
     if (a.cap_out != 0.f) {
@@ -264,9 +265,12 @@ __device__ __forceinline__ void probabilities(const AttnArgs& a, const ScoreTerm
       pf[u + 1] = p[u + 1];
     }
     if constexpr (SHAPED) {
-      if (fac) {
-        mul2(f0, f1, kSlopeScale, kSlopeScale, f0, f1);
-        fac[u / 2] = pack_f16x2(f0, f1);
+      if (side) {
+        if constexpr (REST)
+          fma2v(pf[u], pf[u + 1], -1.f, -1.f, p[u], p[u + 1], f0, f1);
+        else
+          mul2(f0, f1, kSlopeScale, kSlopeScale, f0, f1);
+        side[u / 2] = pack_f16x2(f0, f1);
       }
     }
   };
@@ -1039,23 +1043,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         st.to = (flags & kOneDoc) && rec->doc != st.doc ? 0 : lim - j0;
         st.p0 = (float)(j0 - pos);
-        // P, and the cap's slope as FP16 pairs: half the registers of FP32, which would spill. Off
-        // by 2^-11 of itself: an eighth of dS's own rounding in BF16, as much as it in FP16
+        // With a cap dS needs P times the slope, and e needs P; both in FP32 would spill. BF16:
+        // P, and the slope as FP16 pairs, off by 2^-11 of itself, an eighth of dS's own
+        // rounding. FP16, whose dS is rounded no more than that: P times the slope, and the
+        // rest of P as FP16 pairs, which go into nothing but e, the small correction
+        // (head_dim 80: 203 us instead of 197 backward; BF16 would pay 8 of 190).
+        constexpr bool kRest = f16 && SHAPED;
         float p[32];
-        [[maybe_unused]] uint32_t fac[SHAPED ? 16 : 1];
+        [[maybe_unused]] uint32_t side[SHAPED ? 16 : 1];
         uint32_t pk[16];
 #pragma unroll
         for (int e = 0; e < 32; e += 16) {
           uint32_t q[16];
-          float nl[16], pf[16];
+          float nl[16], other[16];
           tmem_ld_x16(tSr + e, q);
 #pragma unroll
           for (int y = 0; y < 16; ++y) nl[y] = nlse;
           tmem_ld_wait_16(q);
+          float *const all = kRest ? other : p + e, *const pf = kRest ? p + e : other;
           if (whole)
-            probabilities<SHAPED, false>(a, st, q, c0 + e, nl, p + e, pf, SHAPED ? fac + e / 2 : nullptr);
+            probabilities<SHAPED, false, kRest>(a, st, q, c0 + e, nl, all, pf, SHAPED ? side + e / 2 : nullptr);
           else
-            probabilities<SHAPED, true>(a, st, q, c0 + e, nl, p + e, pf, SHAPED ? fac + e / 2 : nullptr);
+            probabilities<SHAPED, true, kRest>(a, st, q, c0 + e, nl, all, pf, SHAPED ? side + e / 2 : nullptr);
           pack16<T>(pf, pk + e / 2);
           if (!Tm::kApart) tmem_st_x8(tPr + e / 2, pk + e / 2);  // over scores already read
         }
@@ -1090,22 +1099,36 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int y = 0; y < 16; ++y) nd[y] = ndelta;
           tmem_ld_wait_16(q);
-          if (whole)
-            score_grads<false>(q, nd, p + e, ds);
-          else
-            score_grads<true>(q, nd, p + e, ds);
+          if constexpr (kRest) {
 #pragma unroll
-          for (int y = 0; y < 16; y += 2) add2(e0, e1, ds[y], ds[y + 1], e0, e1);
-          if constexpr (f16) {
-            const float by = SHAPED ? ds_mul / kSlopeScale : ds_mul;
+            for (int y = 0; y < 16; y += 2) {
+              const uint32_t r = side[(e + y) / 2];
+              float x0, x1, p0, p1;
+              add2(__uint_as_float(q[y]), __uint_as_float(q[y + 1]), ndelta, ndelta, x0, x1);
+              add2(p[e + y], p[e + y + 1], Elem<__half>::lo(r), Elem<__half>::hi(r), p0, p1);
+              // dP of keys that do not exist may be anything
+              if (!whole && p0 == 0.f) x0 = 0.f;
+              if (!whole && p1 == 0.f) x1 = 0.f;
+              fma2v(x0, x1, p0, p1, e0, e1, e0, e1);
+              mul2(x0, x1, p[e + y], p[e + y + 1], ds[y], ds[y + 1]);
+            }
+          } else {
+            if (whole)
+              score_grads<false>(q, nd, p + e, ds);
+            else
+              score_grads<true>(q, nd, p + e, ds);
 #pragma unroll
-            for (int y = 0; y < 16; y += 2) mul2(ds[y], ds[y + 1], by, by, ds[y], ds[y + 1]);
+            for (int y = 0; y < 16; y += 2) add2(e0, e1, ds[y], ds[y + 1], e0, e1);
+            if constexpr (SHAPED) {
+#pragma unroll
+              for (int y = 0; y < 16; y += 2)
+                mul2(ds[y], ds[y + 1], Elem<__half>::lo(side[(e + y) / 2]), Elem<__half>::hi(side[(e + y) / 2]), ds[y],
+                     ds[y + 1]);
+            }
           }
-          if constexpr (SHAPED) {
+          if constexpr (f16) {
 #pragma unroll
-            for (int y = 0; y < 16; y += 2)
-              mul2(ds[y], ds[y + 1], Elem<__half>::lo(fac[(e + y) / 2]), Elem<__half>::hi(fac[(e + y) / 2]), ds[y],
-                   ds[y + 1]);
+            for (int y = 0; y < 16; y += 2) mul2(ds[y], ds[y + 1], ds_mul, ds_mul, ds[y], ds[y + 1]);
           }
           pack16<T>(ds, pk + e / 2);
           if (!Tm::kApart) tmem_st_x8(tDsr + e / 2, pk + e / 2);
@@ -1138,7 +1161,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool part = rec->slot >= 0, valid = i < a.Nq;
           const float err = e * g.v_scale;
           if (valid && !part && cq == 0) g.ndelta[((int64_t)b * a.H + h) * g.qpad + i] = ndelta - err;
-          // dS carries the row's factor, for other types kSlopeScale where it took the cap's slope
+          // dS carries the row's factor, in BF16 kSlopeScale where it took the cap's slope
           store_dq<T, NB, !SHAPED, f16 || SHAPED>(static_cast<T*>(g.out0) + b * g.s0[0] + i * g.s0[1] + h * g.s0[2], wide,
                           part ? g.part + at * a.D : nullptr, g.part + (g.slots * kTile + at) * a.D, g.part_e + at, a.D,
                           g.out_scale, cq, tDq + lane_off, tPk + lane_off, some, valid, err,
