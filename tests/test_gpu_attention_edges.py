@@ -309,3 +309,40 @@ def test_workspace_on_a_16_byte_boundary(dt):
         for name in want:
             assert torch.equal(got[name], want[name]), name
         assert (buf[:offset] == 0xA5).all() and (buf[offset + n:] == 0xA5).all()
+
+
+def test_f16_backward_captured_and_replayed_with_other_sizes_of_gradient():
+    """The factors of dS come from the tensors at the time of the replay."""
+    q, k, v, do = inputs(2, 300, 700, 4, 2, 64, "f16", 79)
+    cfg = B.attention_cfg(2, 300, 700, 4, 2, 64, dtype=B.SD_DTYPE_F16, softcap=15.0)
+    ws = torch.full((B.sd_attention_workspace_size(cfg),), 0xFF, dtype=torch.uint8, device="cuda")
+    o, lse = torch.empty_like(q), torch.empty(2, 4, 300, device="cuda")
+    out = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dv": torch.empty_like(v)}
+    given, s = do.clone(), torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    B.sd_attention_fwd(cfg, q, k, v, None, o, lse, ws, ws.numel(), torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        B.sd_attention_bwd(cfg, q, k, v, None, o, lse, given, out["dq"], out["dk"], out["dv"], ws, ws.numel(), s)
+    for scale in (2.0 ** -6, 4096.0, 1.0):
+        given.copy_(do.float() * scale)
+        want = call(q, k, v, given, softcap=15.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        for name in out:
+            assert torch.isfinite(out[name]).all() and torch.equal(out[name], want[name]), (scale, name)
+
+
+def test_f16_infinite_gradient_stays_in_its_row_of_dq():
+    q, k, v, do = inputs(1, 300, 400, 4, 2, 64, "f16", 80)
+    want = reference(q, k, v, do)
+    do[0, 100, 3] = math.inf
+    got = call(q, k, v, do)
+    assert not torch.isfinite(got["dq"][0, 100, 3]).any()
+    keep = torch.ones_like(do, dtype=torch.bool)
+    keep[0, 100, 3] = False
+    assert R.rel(got["dq"][keep], want["dq"][keep]) < 4 * 2.0 ** -11 + 1e-5
+    # the other key head's gradients
+    assert R.rel(got["dk"][:, :, 0], want["dk"][:, :, 0]) < 4 * 2.0 ** -11 + 1e-5
+    assert R.rel(got["dv"][:, :, 0], want["dv"][:, :, 0]) < 2 * 2.0 ** -11 + 1e-5
